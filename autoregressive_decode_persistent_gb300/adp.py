@@ -83,6 +83,13 @@ class BatchLayout(ctypes.Structure):
                 ("down_segment", ctypes.c_int32), ("control_bytes", ctypes.c_uint64), ("smem_bytes", ctypes.c_uint64)]
 
 
+class PagedKV(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "table", "lens")] + \
+               [("page_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64)] + \
+               [(n, ctypes.c_int32) for n in ("n_pages", "page_size", "n_kv_heads", "head_dim", "dtype", "n_seqs",
+                                               "table_width")]
+
+
 _lib = None
 
 # (name, restype, argtypes)
@@ -141,6 +148,17 @@ _SIGS = [
     ("adp_debug_set_l2_pacing", ctypes.c_int, [ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint32]),
     ("adp_measure_read_bandwidth", ctypes.c_int, [ctypes.c_void_p, ctypes.c_uint64, ctypes.c_int32, ctypes.c_void_p,
                                                   ctypes.POINTER(ctypes.c_double)]),
+    ("adp_paged_kv_write", ctypes.c_int, [ctypes.POINTER(PagedKV), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                          ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32,
+                                          ctypes.c_void_p, ctypes.c_void_p]),
+    ("adp_paged_kv_read", ctypes.c_int, [ctypes.POINTER(PagedKV), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                         ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32,
+                                         ctypes.c_void_p, ctypes.c_void_p]),
+    ("adp_paged_attention", ctypes.c_int, [ctypes.POINTER(PagedKV), ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                           ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_int64,
+                                           ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p]),
+    ("adp_paged_attention_workspace", ctypes.c_int, [ctypes.POINTER(PagedKV), ctypes.c_int32,
+                                                     ctypes.POINTER(ctypes.c_uint64)]),
     ("adp_debug_set_ring_slots", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32]),
     ("adp_debug_ring_slots", ctypes.c_int, [ctypes.c_void_p]),
     ("adp_debug_set_epoch_base", ctypes.c_int, [ctypes.c_void_p, ctypes.c_uint32]),
@@ -428,6 +446,31 @@ def adp_measure_read_bandwidth(dev_buf, nbytes: int, reps: int, stream: int = 0)
     _check(load_library().adp_measure_read_bandwidth(_ptr(dev_buf), int(nbytes), int(reps), stream or None,
                                                       ctypes.byref(g)), "adp_measure_read_bandwidth")
     return g.value
+
+
+def adp_paged_kv_write(kv: PagedKV, k, v, rows_dtype: int, k_stride: int, v_stride: int, cu_rows, n_rows: int,
+                       dev_status=None, stream: int = 0):
+    _check(load_library().adp_paged_kv_write(kv, _ptr(k), _ptr(v), rows_dtype, k_stride, v_stride, _ptr(cu_rows), n_rows,
+                                             _ptr(dev_status), stream), "adp_paged_kv_write")
+
+
+def adp_paged_kv_read(kv: PagedKV, k, v, rows_dtype: int, k_stride: int, v_stride: int, cu_rows, n_rows: int,
+                      dev_status=None, stream: int = 0):
+    _check(load_library().adp_paged_kv_read(kv, _ptr(k), _ptr(v), rows_dtype, k_stride, v_stride, _ptr(cu_rows), n_rows,
+                                            _ptr(dev_status), stream), "adp_paged_kv_read")
+
+
+def adp_paged_attention_workspace(kv: PagedKV, n_heads: int) -> int:
+    n = ctypes.c_uint64()
+    _check(load_library().adp_paged_attention_workspace(kv, n_heads, ctypes.byref(n)), "adp_paged_attention_workspace")
+    return n.value
+
+
+def adp_paged_attention(kv: PagedKV, q, q_dtype: int, n_heads: int, q_stride: int, scale: float, out, out_stride: int,
+                        workspace, workspace_bytes: int, dev_status=None, stream: int = 0):
+    _check(load_library().adp_paged_attention(kv, _ptr(q), q_dtype, n_heads, q_stride, scale, _ptr(out), out_stride,
+                                              _ptr(workspace), workspace_bytes, _ptr(dev_status), stream),
+           "adp_paged_attention")
 
 
 def adp_debug_set_l2_pacing(model, bytes_per_us: int, burst_bytes: int):

@@ -1,0 +1,753 @@
+// Attention of one new token per sequence over the pages of a KV cache.
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include <type_traits>
+
+#include "../../include/adp.h"
+#include "device.cuh"
+#include "paged.cuh"
+
+namespace adp {
+namespace {
+
+__device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
+  uint4 v;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ldg8(const uint8_t* p) {
+  uint2 v;
+  asm("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
+// D += A B on the warp-level tensor instruction, 16 x 16 by 16 x 8, fp32 accumulators.
+template <bool BF16>
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+  if constexpr (BF16) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  } else {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
+}
+// Transpose of an 8 x 8 matrix of 16-bit elements held by a warp (row lane / 4, columns 2 (lane % 4) and + 1).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xFFFFu), __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// Softmax state of a piece of a segment, in shared or global memory.
+template <int HD, int NT>
+struct Partial {
+  float o[NT * 8][HD];
+  float m[NT * 8];
+  float l[NT * 8];
+};
+struct SplitMeta {
+  int32_t seg;   // sequence x tile of heads that starts in this CTA and goes on behind it, -1: none
+  int32_t last;  // the CTA that it ends in
+};
+
+struct AttnArgs {
+  PagedView c;
+  const uint8_t* q;
+  uint8_t* out;
+  int64_t q_stride, out_stride;  // bytes
+  int32_t group, tiles;          // query heads per KV head; tiles of query heads per KV head
+  float scale_log2;
+  void* partials;                // Partial [2 ctas]
+  SplitMeta* meta;               // [ctas]
+  int32_t* status;
+};
+
+// One new token per sequence over its pages.  The line of units (a unit: 4 KB of keys, i.e. 16 to 64 positions, of
+// one sequence, KV head and tile of up to 8 NT query heads) is cut into even ranges, one per CTA and in it one per
+// warp, whatever the sequences' lengths are: a long context spreads over the GPU and short ones share a warp.
+// A warp runs its range segment by segment (segment: one sequence and tile of heads) with its own running maximum,
+// sum and output in registers.  Segments that several warps share are joined in shared memory, segments that
+// several CTAs share in paged_attention_join_kernel.
+//
+// Bound by reading K and V once.  Both go from global memory straight into the registers of the 16 x 8 x 16 tensor
+// instruction: S^T = K Q^T takes a K row's 16-byte pieces as the A operand (the order of the contraction index is
+// free, and Q's is chosen alike), O^T = V^T P^T takes V's with the 16-bit halves of two keys interleaved.  With the
+// query heads as the 8-wide side a group of up to 8 heads costs one instruction per 16 x 16 of K; nothing is staged
+// in shared memory.  e4m3 codes become fp16 (exact), their scales multiply the scores and the probabilities.
+template <int HD, int CDT, int QDT, int NT, bool SMALL>
+__global__ void __launch_bounds__(kPagedWarps * 32, 1) paged_attention_kernel(AttnArgs a) {
+  constexpr int EB = elem_bytes(CDT);
+  constexpr int ROWB = HD * EB;
+  constexpr int UNIT = 4096 / ROWB;  // positions
+  constexpr int RG = UNIT / 16;      // groups of 16 positions
+  constexpr int KC = ROWB / 64;      // 16-byte pieces of a K row per lane
+  constexpr int KS = 4 / EB;         // contraction steps per piece (a step: 4 elements per lane)
+  constexpr int VB = ROWB / 8;       // bytes of a V row per lane
+  constexpr int VW = VB / 4;         // 32-bit words
+  constexpr int MT = HD / 16;        // 16-row tiles of O^T
+  constexpr bool Q8 = CDT == DT_E4M3;
+  constexpr bool BF = CDT == DT_BF16;  // type of the tensor instruction (e4m3: fp16)
+  using Part = Partial<HD, NT>;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Part* slots = reinterpret_cast<Part*>(smem_raw);  // [warps][2]
+  __shared__ int32_t s_seg[kPagedWarps * 2];
+  __shared__ int64_t s_u0[kPagedWarps * 2], s_u1[kPagedWarps * 2];
+  __shared__ int64_t s_chunk[kPagedMaxSeqs / 32 + 1];
+  const PagedView& c = a.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l4 = lane & 3, r8 = lane >> 2;
+  const int nvt = c.n_kv_heads * a.tiles;
+
+  auto units_of = [&](int b) {
+    const int len = paged_length(c.lens[b], c.table_width, c.log2_page);
+    return (len + UNIT - 1) / UNIT;
+  };
+  // ---- the line's length: units of every 32 sequences, and zeros for the sequences without any
+  const int n_chunks = (c.n_seqs + 31) / 32;
+  for (int ch = warp; ch < n_chunks; ch += kPagedWarps) {
+    const int b = ch * 32 + lane;
+    int n = 0;
+    bool empty = false;
+    if (b < c.n_seqs) {
+      const int32_t raw = c.lens[b], len = paged_length(raw, c.table_width, c.log2_page);
+      if (raw > len) report(a.status, ADP_ERR_CONTEXT_OVERFLOW);
+      if (raw < 0) report(a.status, ADP_ERR_INVALID_ARG);
+      n = (len + UNIT - 1) / UNIT;
+      empty = n == 0 && b % gridDim.x == blockIdx.x;
+    }
+    for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, empty); todo; todo &= todo - 1) {
+      uint8_t* o = a.out + (int64_t)(ch * 32 + __ffs(todo) - 1) * a.out_stride;
+      const int words = c.n_kv_heads * a.group * HD / 8;
+      for (int w = lane; w < words; w += 32) reinterpret_cast<uint4*>(o)[w] = make_uint4(0, 0, 0, 0);
+    }
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+    if (lane == 0) s_chunk[ch] = n;
+  }
+  if (threadIdx.x < kPagedWarps * 2) s_seg[threadIdx.x] = -1;
+  __syncthreads();
+  if (warp == 0) {  // running sums over the chunks, in place: s_chunk[i] = units before chunk i
+    int64_t run = 0;
+    for (int ch = 0; ch <= n_chunks; ch += 32) {
+      int64_t n = ch + lane < n_chunks ? s_chunk[ch + lane] : 0, sum = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+        if (lane >= d) sum += o;
+      }
+      if (ch + lane <= n_chunks) s_chunk[ch + lane] = run + sum - n;
+      run += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+  }
+  __syncthreads();
+  const int64_t total = s_chunk[n_chunks] * nvt;
+  const int parts = split_parts(total, gridDim.x);
+  if ((int)blockIdx.x >= parts || total == 0) {
+    if (threadIdx.x == 0) a.meta[blockIdx.x].seg = -1;
+    return;
+  }
+  const int64_t c0 = split_begin(total, parts, blockIdx.x), c1 = split_begin(total, parts, blockIdx.x + 1);
+  int64_t u = c0 + split_begin(c1 - c0, kPagedWarps, warp);
+  const int64_t u_end = c0 + split_begin(c1 - c0, kPagedWarps, warp + 1);
+  const int64_t u_first = u;
+
+  if (u < u_end) {
+    // ---- the sequence, head tile and unit of u
+    int b, vt, t;
+    {
+      const int64_t seq_u = u / nvt;
+      int ch = 0;
+      for (int at = 0; at < n_chunks; at += 32) {
+        const int n = __popc(__ballot_sync(0xFFFFFFFFu, at + lane < n_chunks && s_chunk[at + lane] <= seq_u));
+        if (n) ch = at + n - 1;
+        if (n < 32) break;
+      }
+      const int bl = ch * 32 + lane;
+      const int n = bl < c.n_seqs ? units_of(bl) : 0;
+      int sum = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+        if (lane >= d) sum += o;
+      }
+      const int64_t rest = u - s_chunk[ch] * nvt;
+      const int skip = __popc(__ballot_sync(0xFFFFFFFFu, (int64_t)sum * nvt <= rest));
+      b = min(ch * 32 + skip, c.n_seqs - 1);
+      const int nb = max(1, __shfl_sync(0xFFFFFFFFu, n, skip & 31));
+      const int before = __shfl_sync(0xFFFFFFFFu, sum - n, skip & 31);
+      const int64_t in = rest - (int64_t)before * nvt;
+      vt = (int)(in / nb);
+      t = (int)(in - (int64_t)vt * nb);
+    }
+    while (u < u_end) {
+      const int len = paged_length(c.lens[b], c.table_width, c.log2_page);
+      const int n_units = (len + UNIT - 1) / UNIT;
+      const int n = (int)min((int64_t)(n_units - t), u_end - u);
+      if (n <= 0 || vt >= nvt) break;  // the lengths changed while this call ran
+      const int kvh = vt / a.tiles, head0 = (vt % a.tiles) * (NT * 8);
+      const int heads = min(NT * 8, a.group - head0);
+      const int32_t* trow = c.table + (int64_t)b * c.table_width;
+
+      // ---- the queries, as the B operand (columns: heads)
+      uint32_t qf[NT][MT][2];
+      float qs[NT][2];  // score factor of this lane's two columns
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int h = nt * 8 + r8;
+        const uint8_t* qr = a.q + (int64_t)b * a.q_stride + (int64_t)(kvh * a.group + head0 + h) * HD * 2;
+#pragma unroll
+        for (int ks = 0; ks < MT; ++ks) {
+          const int d = (ks / KS) * (64 / EB) + l4 * (16 / EB) + (ks % KS) * 4;
+          const uint2 w = h < heads ? ldg8(qr + d * 2) : make_uint2(0, 0);
+          qf[nt][ks][0] = w.x;
+          qf[nt][ks][1] = w.y;
+        }
+        float f = 1.0f;
+        if constexpr (Q8 && QDT == DT_BF16) {
+          // bf16 queries meet fp16 codes: the row is brought to a largest magnitude in [1, 2) by a power of two,
+          // so that its 8-bit significands fit fp16 (an element below 2^-17 loses bits: at most 2^-25, half fp16's
+          // least step)
+          float top = 0.0f;
+#pragma unroll
+          for (int ks = 0; ks < MT; ++ks)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[nt][ks][j] << 16)),
+                                     fabsf(__uint_as_float(qf[nt][ks][j] & 0xFFFF0000u))));
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+          const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);
+          f = __uint_as_float(e << 23);
+          const float inv = __uint_as_float((254u - e) << 23);
+#pragma unroll
+          for (int ks = 0; ks < MT; ++ks)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              qf[nt][ks][j] = pack2(__uint_as_float(qf[nt][ks][j] << 16) * inv,
+                                    __uint_as_float(qf[nt][ks][j] & 0xFFFF0000u) * inv, DT_F16);
+        }
+        // this lane's scores are of heads 2 l4 and 2 l4 + 1, whose factors lanes 8 l4 and 8 l4 + 4 hold
+        qs[nt][0] = __shfl_sync(0xFFFFFFFFu, f, l4 * 8) * a.scale_log2;
+        qs[nt][1] = __shfl_sync(0xFFFFFFFFu, f, l4 * 8 + 4) * a.scale_log2;
+      }
+
+      float o[MT][NT][4];
+      float m[NT][2], l[NT][2];
+      float vref = kScaleMin, vinv = 1.0f / kScaleMin;  // e4m3: O is held in units of vref, a power of two
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.0f;
+      }
+
+      uint32_t kr[RG][2][KC * 4];
+      uint32_t vr[RG][4][VW];
+      float ksc[RG][2], vsc[RG][2];
+      // Page of a position that is attended, else -1.
+      auto page_at = [&](int pos) {
+        if (pos >= len) return -1;
+        const int page = paged_page(trow, c.table_width, c.n_pages, c.log2_page, pos);
+        if (page < 0) report(a.status, ADP_ERR_INVALID_ARG);
+        return page;
+      };
+      const int in_page = (1 << c.log2_page) - 1;
+      int pg[RG];  // pages of the next unit's groups (pages of 16 positions and more: a group lies in one)
+      auto fetch_pages = [&](int ut) {
+        if constexpr (!SMALL) {
+#pragma unroll
+          for (int g = 0; g < RG; ++g) pg[g] = page_at(ut * UNIT + g * 16);
+        }
+      };
+      uint32_t kmask = 0;  // bit 2 g + j: position row j of group g is attended
+      auto load_k = [&](int ut) {
+        kmask = 0;
+#pragma unroll
+        for (int g = 0; g < RG; ++g) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int pos = ut * UNIT + g * 16 + r8 + 8 * j;
+            const int page = SMALL ? page_at(pos) : pg[g];
+            const bool on = page >= 0 && pos < len;
+            const int64_t cell = ((int64_t)kvh << c.log2_page) + (pos & in_page);
+            const uint8_t* p = c.k + (int64_t)page * c.page_bytes + cell * ROWB;
+            kmask |= (on ? 1u : 0u) << (2 * g + j);
+#pragma unroll
+            for (int kc = 0; kc < KC; ++kc) {
+              const uint4 w = on ? ldg16(p + kc * 64 + l4 * 16) : make_uint4(0, 0, 0, 0);
+              kr[g][j][kc * 4] = w.x, kr[g][j][kc * 4 + 1] = w.y, kr[g][j][kc * 4 + 2] = w.z, kr[g][j][kc * 4 + 3] = w.w;
+            }
+            if constexpr (Q8) {
+              ksc[g][j] = vsc[g][j] = 0.0f;
+              if (on) {
+                ksc[g][j] = __ldg(c.k_scale + (int64_t)page * c.scale_stride + cell);
+                vsc[g][j] = __ldg(c.v_scale + (int64_t)page * c.scale_stride + cell);
+              }
+            }
+          }
+        }
+      };
+      auto load_v = [&](int ut) {
+#pragma unroll
+        for (int g = 0; g < RG; ++g) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int pos = ut * UNIT + g * 16 + 2 * l4 + (j & 1) + 8 * (j >> 1);
+            const int page = SMALL ? page_at(pos) : pg[g];
+            const bool on = page >= 0 && pos < len;
+            const uint8_t* p = c.v + (int64_t)page * c.page_bytes + (((int64_t)kvh << c.log2_page) + (pos & in_page)) * ROWB;
+            if constexpr (VB >= 16) {
+#pragma unroll
+              for (int h = 0; h < VB / 16; ++h) {
+                const uint4 w = on ? ldg16(p + (h * 8 + r8) * 16) : make_uint4(0, 0, 0, 0);
+                vr[g][j][h * 4] = w.x, vr[g][j][h * 4 + 1] = w.y, vr[g][j][h * 4 + 2] = w.z, vr[g][j][h * 4 + 3] = w.w;
+              }
+            } else {
+              const uint2 w = on ? ldg8(p + r8 * 8) : make_uint2(0, 0);
+              vr[g][j][0] = w.x, vr[g][j][1] = w.y;
+            }
+          }
+        }
+      };
+
+      fetch_pages(t);
+      load_k(t);
+      load_v(t);
+      for (int i = 0; i < n; ++i) {
+        const bool more = i + 1 < n;
+        if (more) fetch_pages(t + i + 1);
+        // ---- S^T = K Q^T: rows are keys, columns heads
+        float s[RG][NT][4];
+#pragma unroll
+        for (int g = 0; g < RG; ++g) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) s[g][nt][0] = s[g][nt][1] = s[g][nt][2] = s[g][nt][3] = 0.0f;
+#pragma unroll
+          for (int ks = 0; ks < MT; ++ks) {
+            uint32_t f[4];
+            if constexpr (Q8) {
+              const uint32_t w0 = kr[g][0][ks], w1 = kr[g][1][ks];
+              f[0] = e4m3x2_to_f16x2(w0), f[1] = e4m3x2_to_f16x2(w1);
+              f[2] = e4m3x2_to_f16x2(w0 >> 16), f[3] = e4m3x2_to_f16x2(w1 >> 16);
+            } else {
+              f[0] = kr[g][0][2 * ks], f[1] = kr[g][1][2 * ks], f[2] = kr[g][0][2 * ks + 1], f[3] = kr[g][1][2 * ks + 1];
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16<BF>(s[g][nt], f[0], f[1], f[2], f[3], qf[nt][ks][0], qf[nt][ks][1]);
+          }
+        }
+        const uint32_t on = kmask;
+        float ks_now[RG][2], vs_now[RG][2];
+        if constexpr (Q8) {
+#pragma unroll
+          for (int g = 0; g < RG; ++g)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) ks_now[g][j] = ksc[g][j], vs_now[g][j] = vsc[g][j];
+        }
+        if (more) load_k(t + i + 1);
+        // ---- running maximum
+        float grow = 1.0f;  // e4m3: the old unit of O in the new one
+        if constexpr (Q8) {
+          float top = 0.0f;
+#pragma unroll
+          for (int g = 0; g < RG; ++g) top = fmaxf(top, fmaxf(vs_now[g][0], vs_now[g][1]));
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+          if (top > vref) {
+            const float nref = __uint_as_float((__float_as_uint(top) + 0x7FFFFFu) & 0x7F800000u);
+            vinv = 1.0f / nref;
+            grow = vref * vinv;
+            vref = nref;
+          }
+        }
+        float alpha[NT][2];
+        bool change = grow != 1.0f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < RG; ++g)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                float x = s[g][nt][2 * r + j] * qs[nt][j];
+                if constexpr (Q8) x *= ks_now[g][r];
+                x = (on >> (2 * g + r)) & 1 ? x : -INFINITY;
+                s[g][nt][2 * r + j] = x;
+                top = fmaxf(top, x);
+              }
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+            const float mn = fmaxf(m[nt][j], top);
+            change |= mn != m[nt][j];
+            alpha[nt][j] = exp2_fast(m[nt][j] - safe_max(mn));
+            m[nt][j] = mn;
+          }
+        }
+        if (__any_sync(0xFFFFFFFFu, change)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            l[nt][0] *= alpha[nt][0];
+            l[nt][1] *= alpha[nt][1];
+            const float f0 = alpha[nt][0] * grow, f1 = alpha[nt][1] * grow;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              o[mt][nt][0] *= f0, o[mt][nt][2] *= f0;
+              o[mt][nt][1] *= f1, o[mt][nt][3] *= f1;
+            }
+          }
+        }
+        // ---- P, and O^T += V^T P^T
+#pragma unroll
+        for (int g = 0; g < RG; ++g) {
+          uint32_t pf[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float p0 = exp2_fast(s[g][nt][2 * r] - safe_max(m[nt][0]));
+              float p1 = exp2_fast(s[g][nt][2 * r + 1] - safe_max(m[nt][1]));
+              l[nt][0] += p0;
+              l[nt][1] += p1;
+              if constexpr (Q8) {
+                const float f = vs_now[g][r] * vinv;
+                p0 *= f, p1 *= f;
+              }
+              pf[nt][r] = transpose8x8(pack2(p0, p1, BF ? DT_BF16 : DT_F16));
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < VW; ++w) {
+            const uint32_t x0 = vr[g][0][w], x1 = vr[g][1][w], x2 = vr[g][2][w], x3 = vr[g][3][w];
+            if constexpr (Q8) {
+              const uint32_t ya = __byte_perm(x0, x1, 0x5140), yb = __byte_perm(x2, x3, 0x5140);
+              const uint32_t za = __byte_perm(x0, x1, 0x7362), zb = __byte_perm(x2, x3, 0x7362);
+              const uint32_t f[8] = {e4m3x2_to_f16x2(ya), e4m3x2_to_f16x2(ya >> 16), e4m3x2_to_f16x2(yb),
+                                     e4m3x2_to_f16x2(yb >> 16), e4m3x2_to_f16x2(za), e4m3x2_to_f16x2(za >> 16),
+                                     e4m3x2_to_f16x2(zb), e4m3x2_to_f16x2(zb >> 16)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma16<BF>(o[2 * w][nt], f[0], f[1], f[2], f[3], pf[nt][0], pf[nt][1]);
+                mma16<BF>(o[2 * w + 1][nt], f[4], f[5], f[6], f[7], pf[nt][0], pf[nt][1]);
+              }
+            } else {
+              const uint32_t f0 = __byte_perm(x0, x1, 0x5410), f1 = __byte_perm(x0, x1, 0x7632);
+              const uint32_t f2 = __byte_perm(x2, x3, 0x5410), f3 = __byte_perm(x2, x3, 0x7632);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16<BF>(o[w][nt], f0, f1, f2, f3, pf[nt][0], pf[nt][1]);
+            }
+          }
+        }
+        if (more) load_v(t + i + 1);
+      }
+
+      // ---- end of the piece: sums over the lanes that share a head
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int d = 4; d <= 16; d <<= 1) l[nt][j] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][j], d);
+      // Element d of this lane's head 2 l4 + j: tile mt, register j (even d) and 2 + j (odd d).
+      auto elem = [&](int mt) { return Q8 ? r8 * VB + 2 * mt : ((mt / 4) * 8 + r8) * 8 + 2 * (mt % 4); };
+      const bool whole = t == 0 && n == n_units;
+      if (whole) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int h = nt * 8 + 2 * l4 + j;
+            if (h >= heads) continue;
+            const float inv = l[nt][j] == 0.0f ? 0.0f : 1.0f / l[nt][j];
+            uint8_t* po = a.out + (int64_t)b * a.out_stride + (int64_t)(kvh * a.group + head0 + h) * HD * 2;
+#pragma unroll
+            for (int mt = 0; mt < MT; mt += 4) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float f = Q8 ? vref : 1.0f;
+                w[e] = pack2(o[mt + e][nt][j] * inv * f, o[mt + e][nt][2 + j] * inv * f, QDT);
+              }
+              *reinterpret_cast<uint4*>(po + elem(mt) * 2) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+      } else {
+        const int sl = warp * 2 + (u == u_first ? 0 : 1);
+        Part& P = slots[sl];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int h = nt * 8 + 2 * l4 + j;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              const float f = Q8 ? vref : 1.0f;
+              *reinterpret_cast<float2*>(&P.o[h][elem(mt)]) = make_float2(o[mt][nt][j] * f, o[mt][nt][2 + j] * f);
+            }
+            if (r8 == 0) {
+              P.m[h] = m[nt][j];
+              P.l[h] = l[nt][j];
+            }
+          }
+        if (lane == 0) {
+          s_seg[sl] = b * nvt + vt;
+          s_u0[sl] = u - t;
+          s_u1[sl] = u - t + n_units;
+        }
+      }
+      u += n;
+      t = 0;
+      if (u < u_end && ++vt == nvt) {
+        vt = 0;
+        do {
+          ++b;
+        } while (b < c.n_seqs && units_of(b) == 0);
+        if (b >= c.n_seqs) break;
+      }
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __syncthreads();
+
+  // ---- join the warps' pieces: consecutive slots of one segment
+  if (threadIdx.x == 0) a.meta[blockIdx.x].seg = -1;
+  for (int i = 0; i < kPagedWarps * 2;) {
+    const int seg = s_seg[i];
+    if (seg < 0) {
+      ++i;
+      continue;
+    }
+    int e = i + 1;
+    while (e < kPagedWarps * 2 && (s_seg[e] < 0 || s_seg[e] == seg)) ++e;
+    const int vt = seg % nvt, b = seg / nvt;
+    const int kvh = vt / a.tiles, head0 = (vt % a.tiles) * (NT * 8);
+    const int heads = min(NT * 8, a.group - head0);
+    const bool before = s_u0[i] < c0, behind = s_u1[i] > c1;
+    Part* dst = reinterpret_cast<Part*>(a.partials) + blockIdx.x * 2 + (before ? 0 : 1);
+    for (int x = threadIdx.x; x < heads * (HD / 4); x += kPagedWarps * 32) {
+      const int h = x / (HD / 4), d = (x % (HD / 4)) * 4;
+      float top = -INFINITY;
+      for (int k = i; k < e; ++k)
+        if (s_seg[k] >= 0) top = fmaxf(top, slots[k].m[h]);
+      float sum = 0.0f;
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int k = i; k < e; ++k) {
+        if (s_seg[k] < 0) continue;
+        const float f = exp2_fast(slots[k].m[h] - safe_max(top));
+        const float4 p = *reinterpret_cast<const float4*>(&slots[k].o[h][d]);
+        sum = fmaf(f, slots[k].l[h], sum);
+        acc.x = fmaf(f, p.x, acc.x), acc.y = fmaf(f, p.y, acc.y), acc.z = fmaf(f, p.z, acc.z), acc.w = fmaf(f, p.w, acc.w);
+      }
+      if (before || behind) {
+        *reinterpret_cast<float4*>(&dst->o[h][d]) = acc;
+        if (d == 0) dst->m[h] = top, dst->l[h] = sum;
+      } else {
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        uint8_t* po = a.out + (int64_t)b * a.out_stride + ((int64_t)(kvh * a.group + head0 + h) * HD + d) * 2;
+        *reinterpret_cast<uint2*>(po) = make_uint2(pack2(acc.x * inv, acc.y * inv, QDT), pack2(acc.z * inv, acc.w * inv, QDT));
+      }
+    }
+    if (!before && behind && threadIdx.x == 0) {
+      a.meta[blockIdx.x].seg = seg;
+      a.meta[blockIdx.x].last = split_owner(total, parts, s_u1[i] - 1);
+    }
+    i = e;
+  }
+}
+
+// Joins the segments that several CTAs share: block (c, h) takes the segment that starts in CTA c and goes on behind
+// it, and its head h.  Four warps read the parts in turn; the first threads join the warps' results.
+template <int HD, int QDT, int NT>
+__global__ void __launch_bounds__(128) paged_attention_join_kernel(AttnArgs a) {
+  using Part = Partial<HD, NT>;
+  constexpr int W = HD / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const SplitMeta meta = a.meta[blockIdx.x];
+  if (meta.seg < 0) return;
+  const int nvt = a.c.n_kv_heads * a.tiles;
+  const int vt = meta.seg % nvt, b = meta.seg / nvt;
+  const int kvh = vt / a.tiles, head0 = (vt % a.tiles) * (NT * 8), h = blockIdx.y;
+  if (h >= min(NT * 8, a.group - head0)) return;
+  const Part* parts = reinterpret_cast<const Part*>(a.partials);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = meta.last - (int)blockIdx.x + 1;
+  // part 0 is this CTA's second slot, part k the first slot of CTA c + k
+  float m = -INFINITY, l = 0.0f, o[W];
+#pragma unroll
+  for (int e = 0; e < W; ++e) o[e] = 0.0f;
+#pragma unroll 4
+  for (int k = warp; k < n; k += 4) {
+    const Part& p = parts[(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)];
+    const float pm = p.m[h], pl = p.l[h];
+    float x[W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) x[e] = p.o[h][e * 32 + lane];
+    const float mn = fmaxf(m, pm);
+    const float f = exp2_fast(m - safe_max(mn)), g = exp2_fast(pm - safe_max(mn));
+    m = mn;
+    l = fmaf(l, f, g * pl);
+#pragma unroll
+    for (int e = 0; e < W; ++e) o[e] = fmaf(o[e], f, g * x[e]);
+  }
+  __shared__ float s_m[4], s_l[4], s_o[4][HD];
+  if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+#pragma unroll
+  for (int e = 0; e < W; ++e) s_o[warp][e * 32 + lane] = o[e];
+  __syncthreads();
+  const float top = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+  float sum = 0.0f, f[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    f[w] = exp2_fast(s_m[w] - safe_max(top));
+    sum = fmaf(f[w], s_l[w], sum);
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  if (threadIdx.x < HD / 2) {
+    float x[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      x[e] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) x[e] = fmaf(f[w], s_o[w][threadIdx.x * 2 + e], x[e]);
+    }
+    uint8_t* po = a.out + (int64_t)b * a.out_stride + (int64_t)(kvh * a.group + head0 + h) * HD * 2;
+    reinterpret_cast<uint32_t*>(po)[threadIdx.x] = pack2(x[0] * inv, x[1] * inv, QDT);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+// Query heads per KV head take tiles of 8 (a group of up to 8) or 16 columns of the tensor instruction.
+int head_tiles(int group) { return group <= 8 ? 1 : 2; }
+
+// CTAs of an attention call: one per SM, or fewer where even full tables would not fill them.
+int attention_ctas(const adp_paged_kv* kv, int group, int sms) {
+  const int nt = head_tiles(group), tiles = (group + nt * 8 - 1) / (nt * 8);
+  const int unit = 4096 / (kv->head_dim * elem_bytes(kv->dtype));
+  const int64_t per_seq = ((int64_t)kv->table_width * kv->page_size + unit - 1) / unit;
+  return split_parts(per_seq * kv->n_kv_heads * tiles * (kv->n_seqs > 0 ? kv->n_seqs : 1), sms);
+}
+
+size_t attention_bytes(int ctas, int nt, int hd) {
+  return (size_t)ctas * 2 * (nt * 8) * (hd + 2) * sizeof(float) + (size_t)ctas * sizeof(SplitMeta);
+}
+
+template <int HD, int CDT, int QDT, int NT, bool SMALL>
+struct AttentionKey {};
+
+template <int HD, int CDT, int QDT, int NT, bool SMALL>
+cudaError_t attention_launch(const AttnArgs& a, int ctas, cudaStream_t st) {
+  constexpr size_t smem = sizeof(Partial<HD, NT>) * kPagedWarps * 2;
+  auto* kernel = paged_attention_kernel<HD, CDT, QDT, NT, SMALL>;
+  cudaError_t e = allow_smem<AttentionKey<HD, CDT, QDT, NT, SMALL>>((const void*)kernel, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<ctas, kPagedWarps * 32, smem, st>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess || ctas == 1) return e;  // one CTA shares no segment
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas - 1, a.group < NT * 8 ? a.group : NT * 8);  // no segment goes on behind the last CTA
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_attention_join_kernel<HD, QDT, NT>, a);
+}
+
+int attention_check(const adp_paged_kv* kv, int32_t n_heads, PagedView* c) {
+  const int rc = paged_view(kv, c);
+  if (rc) return rc;
+  if (n_heads < 1 || n_heads % kv->n_kv_heads) return ADP_ERR_INVALID_ARG;
+  if (n_heads > 4096 || kv->n_seqs > kPagedMaxSeqs) return ADP_ERR_UNSUPPORTED_CONFIG;
+  return ADP_OK;
+}
+
+}  // namespace
+}  // namespace adp
+
+using namespace adp;
+
+extern "C" int adp_paged_attention_workspace(const adp_paged_kv* kv, int32_t n_heads, uint64_t* bytes) {
+  PagedView c;
+  int rc = bytes ? attention_check(kv, n_heads, &c) : ADP_ERR_INVALID_ARG;
+  int sms = 0;
+  if (rc || (rc = sm_count(&sms))) return rc;
+  const int group = n_heads / kv->n_kv_heads;
+  *bytes = attention_bytes(attention_ctas(kv, group, sms), head_tiles(group), kv->head_dim);
+  return ADP_OK;
+}
+
+extern "C" int adp_paged_attention(const adp_paged_kv* kv, const void* q, int32_t q_dtype, int32_t n_heads, int64_t q_stride,
+                                   float scale, void* out, int64_t out_stride, void* workspace, uint64_t workspace_bytes,
+                                   int32_t* dev_status, void* cuda_stream) {
+  AttnArgs a{};
+  int rc = attention_check(kv, n_heads, &a.c);
+  if (rc) return rc;
+  if (q_dtype != ADP_F16 && q_dtype != ADP_BF16) return ADP_ERR_UNSUPPORTED_CONFIG;
+  if (kv->dtype != ADP_E4M3 && kv->dtype != q_dtype) return ADP_ERR_UNSUPPORTED_CONFIG;
+  const int64_t width = (int64_t)n_heads * kv->head_dim;
+  if (!isfinite(scale) || ((uintptr_t)dev_status & 3)) return ADP_ERR_INVALID_ARG;
+  if (kv->n_seqs == 0) return ADP_OK;
+  if (!q || !out || !aligned16(q) || !aligned16(out) || q_stride < width || out_stride < width || q_stride % 8 || out_stride % 8)
+    return ADP_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((rc = sm_count(&sms))) return rc;
+  const int group = n_heads / kv->n_kv_heads, nt = head_tiles(group);
+  const int ctas = attention_ctas(kv, group, sms);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < attention_bytes(ctas, nt, kv->head_dim))
+    return ADP_ERR_INVALID_ARG;
+  a.q = static_cast<const uint8_t*>(q);
+  a.out = static_cast<uint8_t*>(out);
+  a.q_stride = q_stride * 2;
+  a.out_stride = out_stride * 2;
+  a.group = group;
+  a.tiles = (group + nt * 8 - 1) / (nt * 8);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.partials = workspace;
+  a.meta = reinterpret_cast<SplitMeta*>(static_cast<uint8_t*>(workspace) +
+                                        (size_t)ctas * 2 * (nt * 8) * (kv->head_dim + 2) * sizeof(float));
+  a.status = dev_status;
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  const bool small = kv->page_size < 16;
+  cudaError_t e = cudaErrorInvalidValue;
+  auto by_page = [&](auto hd, auto cdt, auto qdt, auto n) {
+    constexpr int H = decltype(hd)::value, C = decltype(cdt)::value, Q = decltype(qdt)::value, N = decltype(n)::value;
+    e = small ? attention_launch<H, C, Q, N, true>(a, ctas, st) : attention_launch<H, C, Q, N, false>(a, ctas, st);
+  };
+  auto by_group = [&](auto hd, auto cdt, auto qdt) {
+    if (nt == 1) by_page(hd, cdt, qdt, std::integral_constant<int, 1>());
+    else by_page(hd, cdt, qdt, std::integral_constant<int, 2>());
+  };
+  auto by_type = [&](auto hd) {
+    using F = std::integral_constant<int, DT_F16>;
+    using B = std::integral_constant<int, DT_BF16>;
+    using E = std::integral_constant<int, DT_E4M3>;
+    if (kv->dtype == ADP_F16) by_group(hd, F(), F());
+    else if (kv->dtype == ADP_BF16) by_group(hd, B(), B());
+    else if (q_dtype == ADP_F16) by_group(hd, E(), F());
+    else by_group(hd, E(), B());
+  };
+  if (kv->head_dim == 128) by_type(std::integral_constant<int, 128>());
+  else by_type(std::integral_constant<int, 64>());
+  return cuda_status(e, "adp_paged_attention");
+}

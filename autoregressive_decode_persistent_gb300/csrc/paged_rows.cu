@@ -1,0 +1,200 @@
+// Packed K/V rows written into the pages of a cache (16-bit, or e4m3 with one scale per row and head), and
+// cached rows read back.
+#include <cuda_runtime.h>
+
+#include <type_traits>
+
+#include "../../include/adp.h"
+#include "device.cuh"
+#include "paged.cuh"
+
+namespace adp {
+namespace {
+
+constexpr float kE4m3Max = 448.0f;
+
+// The sequence that packed row i belongs to: the number of entries of cu[1 .. n] that are at most i (n for
+// rows behind the last sequence).  A whole warp asks; 32 entries are compared at a time.
+__device__ __forceinline__ int find_sequence(const int32_t* cu, int n, int i, int lane) {
+  int lo = 0;
+  while (n > 32) {
+    const int step = (n + 31) / 32;
+    const int at = min((lane + 1) * step, n) - 1;
+    const int c = __popc(__ballot_sync(0xFFFFFFFFu, lane * step < n && cu[1 + lo + at] <= i));
+    const int skip = min(c * step, n);
+    lo += skip;
+    n = min(step, n - skip);
+  }
+  return lo + __popc(__ballot_sync(0xFFFFFFFFu, lane < n && cu[1 + lo + min(lane, max(n - 1, 0))] <= i));
+}
+
+// 8 consecutive elements in fp32 (exact).
+template <int DT>
+__device__ __forceinline__ void load_row8(const uint8_t* p, float (&x)[8]) {
+  if constexpr (DT == DT_F32) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 16);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+    load8<DT>(p, x);
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void store_row8(uint8_t* p, const float (&x)[8]) {
+  if constexpr (DT == DT_F32) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(p + 16) = make_float4(x[4], x[5], x[6], x[7]);
+  } else if constexpr (DT == DT_E4M3) {
+    uint32_t w[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * j], x[4 * j + 1]), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * j + 2], x[4 * j + 3]), __NV_SATFINITE, __NV_E4M3);
+      w[j] = a | (b << 16);
+    }
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = pack2(x[2 * j], x[2 * j + 1], DT);
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Rows into pages (WRITE) or pages into rows, one warp per packed row.  Its K heads and then its V heads are one
+// line of 8-element pieces, a piece per lane, so that small rows fill a warp too.  Copying: bound by memory.
+// Quantising takes a row's absolute maximum over the HD / 8 lanes that hold it (NaN carried along), divides by
+// the scale max / 448 and rounds to the nearest code.
+template <int ROWDT, int CDT, int HD, bool WRITE>
+__global__ void __launch_bounds__(256)
+    paged_rows_kernel(PagedView c, uint8_t* rows_k, uint8_t* rows_v, int64_t k_stride, int64_t v_stride,
+                      const int32_t* __restrict__ cu, int n_rows, int32_t* status) {
+  constexpr int LPR = HD / 8;  // lanes that hold one row of one head
+  const int lane = threadIdx.x & 31;
+  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (i >= n_rows) return;
+  const int b = find_sequence(cu, c.n_seqs, i, lane);
+  if (b >= c.n_seqs) return;  // behind the last sequence
+  const int64_t pos = paged_position(c.lens[b], cu[b + 1], i);
+  const int page = paged_page(c.table + (int64_t)b * c.table_width, c.table_width, c.n_pages, c.log2_page, pos);
+  if (page < 0 && lane == 0) report(status, ADP_ERR_INVALID_ARG);
+  if (WRITE && page < 0) return;
+  const int slot = (int)(pos & ((1 << c.log2_page) - 1));
+  const int heads = 2 * c.n_kv_heads;
+  constexpr int kAhead = 4;  // pieces per lane in flight
+  for (int h0 = 0; h0 < heads; h0 += kAhead * (32 / LPR)) {
+    float x[kAhead][8];
+    uint8_t* cell[kAhead];
+    uint8_t* row[kAhead];
+    float* scale[kAhead];
+    bool on[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int hh = h0 + a * (32 / LPR) + lane / LPR;
+      on[a] = hh < heads;
+      const bool is_v = hh >= c.n_kv_heads;
+      const int h = is_v ? hh - c.n_kv_heads : hh;
+      const int64_t at = ((int64_t)h << c.log2_page) + slot;
+      cell[a] = (is_v ? c.v : c.k) + (int64_t)page * c.page_bytes + (at * HD + (lane % LPR) * 8) * elem_bytes(CDT);
+      row[a] = (is_v ? rows_v + (int64_t)i * v_stride : rows_k + (int64_t)i * k_stride) +
+               (int64_t)(h * HD + (lane % LPR) * 8) * elem_bytes(ROWDT);
+      scale[a] = CDT == DT_E4M3 ? (is_v ? c.v_scale : c.k_scale) + (int64_t)page * c.scale_stride + at : nullptr;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[a][e] = 0.0f;
+      if (on[a]) {
+        if (WRITE) {
+          load_row8<ROWDT>(row[a], x[a]);
+        } else if (page >= 0) {
+          load_row8<CDT>(cell[a], x[a]);
+        }
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      if constexpr (CDT == DT_E4M3 && WRITE) {
+        float top = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(x[a][e]));
+#pragma unroll
+        for (int d = LPR / 2; d >= 1; d >>= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        const float s = max_nan(__fdiv_rn(top, kE4m3Max), kScaleMin);
+        if (on[a]) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[a][e] = __fdiv_rn(x[a][e], s);
+          store_row8<DT_E4M3>(cell[a], x[a]);
+          if (lane % LPR == 0) *scale[a] = s;
+        }
+      } else if (on[a]) {
+        if constexpr (CDT == DT_E4M3) {
+          const float s = page >= 0 ? *scale[a] : 0.0f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[a][e] = __fmul_rn(x[a][e], s);
+        }
+        if (WRITE) {
+          store_row8<CDT>(cell[a], x[a]);
+        } else {
+          store_row8<ROWDT>(row[a], x[a]);
+        }
+      }
+    }
+  }
+}
+
+template <bool WRITE>
+int paged_rows(const adp_paged_kv* kv, uint8_t* k, uint8_t* v, int32_t rows_dtype, int64_t k_stride, int64_t v_stride,
+               const int32_t* cu_rows, int32_t n_rows, int32_t* status, void* stream) {
+  PagedView c;
+  const int rc = paged_view(kv, &c);
+  if (rc) return rc;
+  if (rows_dtype != ADP_F16 && rows_dtype != ADP_BF16 && rows_dtype != ADP_F32) return ADP_ERR_UNSUPPORTED_CONFIG;
+  if (n_rows < 0 || !cu_rows || ((uintptr_t)cu_rows & 3) || ((uintptr_t)status & 3)) return ADP_ERR_INVALID_ARG;
+  if (n_rows == 0 || kv->n_seqs == 0) return ADP_OK;
+  const int eb = elem_bytes(rows_dtype);
+  const int64_t width = (int64_t)kv->n_kv_heads * kv->head_dim;
+  if (!k || !v || !aligned16(k) || !aligned16(v)) return ADP_ERR_INVALID_ARG;
+  if (k_stride < width || v_stride < width || (k_stride * eb) % 16 || (v_stride * eb) % 16) return ADP_ERR_INVALID_ARG;
+  const int grid = (int)(((int64_t)n_rows + 7) / 8);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  auto go = [&](auto kernel) {
+    kernel<<<grid, 256, 0, st>>>(c, k, v, k_stride * eb, v_stride * eb, cu_rows, n_rows, status);
+  };
+  auto by_rows = [&](auto cdt, auto hd) {
+    constexpr int C = decltype(cdt)::value, H = decltype(hd)::value;
+    if (rows_dtype == ADP_F16) go(paged_rows_kernel<DT_F16, C, H, WRITE>);
+    else if (rows_dtype == ADP_BF16) go(paged_rows_kernel<DT_BF16, C, H, WRITE>);
+    else go(paged_rows_kernel<DT_F32, C, H, WRITE>);
+  };
+  auto by_cache = [&](auto hd) {
+    if (kv->dtype == ADP_F16) by_rows(std::integral_constant<int, DT_F16>(), hd);
+    else if (kv->dtype == ADP_BF16) by_rows(std::integral_constant<int, DT_BF16>(), hd);
+    else by_rows(std::integral_constant<int, DT_E4M3>(), hd);
+  };
+  if (kv->head_dim == 128) by_cache(std::integral_constant<int, 128>());
+  else by_cache(std::integral_constant<int, 64>());
+  return cuda_status(cudaGetLastError(), WRITE ? "adp_paged_kv_write" : "adp_paged_kv_read");
+}
+
+}  // namespace
+}  // namespace adp
+
+using namespace adp;
+
+extern "C" int adp_paged_kv_write(const adp_paged_kv* kv, const void* k, const void* v, int32_t rows_dtype, int64_t k_stride,
+                                  int64_t v_stride, const int32_t* cu_rows, int32_t n_rows, int32_t* dev_status,
+                                  void* cuda_stream) {
+  return paged_rows<true>(kv, static_cast<uint8_t*>(const_cast<void*>(k)), static_cast<uint8_t*>(const_cast<void*>(v)),
+                          rows_dtype, k_stride, v_stride, cu_rows, n_rows, dev_status, cuda_stream);
+}
+
+extern "C" int adp_paged_kv_read(const adp_paged_kv* kv, void* k, void* v, int32_t rows_dtype, int64_t k_stride,
+                                 int64_t v_stride, const int32_t* cu_rows, int32_t n_rows, int32_t* dev_status,
+                                 void* cuda_stream) {
+  return paged_rows<false>(kv, static_cast<uint8_t*>(k), static_cast<uint8_t*>(v), rows_dtype, k_stride, v_stride, cu_rows,
+                           n_rows, dev_status, cuda_stream);
+}

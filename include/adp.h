@@ -337,6 +337,85 @@ int adp_launches_per_step(const adp_model* m, int32_t* n);      /* kernel launch
 int adp_measure_read_bandwidth(const void* dev_buf, uint64_t bytes, int32_t reps, void* cuda_stream,
                                double* gb_per_s);
 
+/* ---- Operators over a paged KV cache.
+ *
+ * The caches above belong to one request each and to the persistent kernels, whose batch is small.
+ * The operators below serve many requests of one layer at a time from caller-owned memory: K/V rows
+ * are written into the pages of a shared pool (16-bit, or quantised to e4m3 as they are written), read
+ * back, and attended to by one new token per sequence.  The pages name attention, and the KV cache as
+ * the other stream of a decode step ([H] §"GPU推論の速度制限要因：メモリ帯域幅"), and fix no paged
+ * algorithm; these operators are not part of the persistent step's arithmetic contract.
+ *
+ * All of them enqueue on `cuda_stream` (NULL: the legacy default stream) and return without
+ * synchronising; they allocate nothing and may be captured into a CUDA graph.  Arguments that the host
+ * can see are checked before anything is launched.  What only the GPU sees (lengths, page numbers, row
+ * offsets) is checked there before it becomes an address: where it is wrong, *dev_status (optional
+ * DEVICE int32, 4-byte aligned, else NULL; left alone when all is well) receives an ADP_ERR_* code and
+ * the row or position is treated as said below.  head_dim is 64 or 128.  Tables, lengths and offsets
+ * must not change while a call that reads them runs. */
+
+/* One layer of a paged cache: the pools and the sequences that use them.  Position p of sequence s lies
+ * in page table[s][p / page_size] at slot p % page_size.  Pages may be shared between sequences (a
+ * common prefix) as long as nobody writes them. */
+typedef struct {
+  void *k, *v;              /* DEVICE [n_pages][n_kv_heads][page_size][head_dim] of dtype, 16-byte aligned */
+  float *k_scale, *v_scale; /* dtype ADP_E4M3: DEVICE [n_pages][n_kv_heads][page_size], an element is
+                               scale x code; else ignored */
+  const int32_t* table;     /* DEVICE [n_seqs][table_width] page numbers, those behind a sequence's length unread */
+  const int32_t* lens;      /* DEVICE [n_seqs] cached positions (the rows being written included) */
+  int64_t page_stride;      /* elements from one page of k or v to the next (a multiple of 16 bytes; at least
+                               n_kv_heads * page_size * head_dim: other layers may lie between) */
+  int64_t scale_stride;     /* floats from one page of k_scale or v_scale to the next */
+  int32_t n_pages, page_size; /* page_size: a power of two up to 1024 */
+  int32_t n_kv_heads, head_dim, dtype; /* dtype: ADP_F16, ADP_BF16 or ADP_E4M3 */
+  int32_t n_seqs, table_width;
+} adp_paged_kv;
+
+/* Write packed K and V rows into their pages.  Sequence s owns rows cu_rows[s] .. cu_rows[s + 1] - 1 and
+ * they are its LAST positions: row i goes to position lens[s] - (cu_rows[s + 1] - i).
+ *  k, v        DEVICE rows [n_rows][n_kv_heads][head_dim] of rows_dtype (ADP_F16, ADP_BF16 or ADP_F32),
+ *              consecutive rows k_stride / v_stride elements apart (multiples of 16 bytes; a slice of a
+ *              fused projection's output will do), 16-byte aligned
+ *  cu_rows     DEVICE [n_seqs + 1], ascending from 0; rows from cu_rows[n_seqs] on are padding
+ * 16-bit pages: rounded to nearest even.  e4m3 pages: per row and head the scale is max|x| / 448 (at least
+ * 2^-126) and the codes are x / scale to nearest even; a row that holds an infinity or NaN reads back as NaN.
+ * A row without a page (a position below 0 or behind the table, a page number outside the pool) is not
+ * written, and reported as ADP_ERR_INVALID_ARG.  Two rows that name one slot leave it with either row's
+ * values, per head and per 16 bytes: name each slot once.
+ * Errors: ADP_ERR_INVALID_ARG, ADP_ERR_UNSUPPORTED_CONFIG, ADP_ERR_CUDA. */
+int adp_paged_kv_write(const adp_paged_kv* kv, const void* k, const void* v, int32_t rows_dtype, int64_t k_stride,
+                       int64_t v_stride, const int32_t* cu_rows, int32_t n_rows, int32_t* dev_status,
+                       void* cuda_stream);
+
+/* Read cached positions back into packed rows: the same geometry the other way round (row i of sequence s
+ * is position lens[s] - (cu_rows[s + 1] - i)), so cu_rows made of the lengths reads whole caches.  e4m3
+ * elements become scale x code in fp32; every value is rounded once to rows_dtype.  A row without a page is
+ * filled with zeros and reported as ADP_ERR_INVALID_ARG; padding rows are left as they were. */
+int adp_paged_kv_read(const adp_paged_kv* kv, void* k, void* v, int32_t rows_dtype, int64_t k_stride,
+                      int64_t v_stride, const int32_t* cu_rows, int32_t n_rows, int32_t* dev_status,
+                      void* cuda_stream);
+
+/* Attention of one new token per sequence: out[s][h] = sum_p softmax_p(scale q[s][h] . K[p][g]) V[p][g]
+ * over positions p < lens[s] (the new token's own row is cached first), g = h / (n_heads / n_kv_heads).
+ *  q, out      DEVICE [n_seqs][n_heads][head_dim] of q_dtype (ADP_F16 or ADP_BF16; the cache's own type
+ *              where that is a 16-bit one), rows q_stride / out_stride elements apart (multiples of 8),
+ *              16-byte aligned
+ *  n_heads     a multiple of n_kv_heads, at most 4096; n_seqs at most 8192
+ *  scale       finite
+ *  workspace   DEVICE scratch of at least adp_paged_attention_workspace bytes, 16-byte aligned; its contents
+ *              do not matter.  Calls that may run at the same time need one each.
+ * Scores, softmax and sums are fp32; probabilities are rounded to the cache's 16-bit type (e4m3: fp16)
+ * before they weigh V.  A sequence of length 0 gives zeros.  A position whose page number is outside the
+ * pool is left out and reported as ADP_ERR_INVALID_ARG; a length behind the table is cut and reported as
+ * ADP_ERR_CONTEXT_OVERFLOW; one below 0 counts as 0 and is reported as ADP_ERR_INVALID_ARG.  Equal inputs
+ * give equal bits on one GPU. */
+int adp_paged_attention(const adp_paged_kv* kv, const void* q, int32_t q_dtype, int32_t n_heads, int64_t q_stride,
+                        float scale, void* out, int64_t out_stride, void* workspace, uint64_t workspace_bytes,
+                        int32_t* dev_status, void* cuda_stream);
+/* Bytes of scratch adp_paged_attention needs for this cache (a few MB at most; asks the current device for
+ * its SM count). */
+int adp_paged_attention_workspace(const adp_paged_kv* kv, int32_t n_heads, uint64_t* bytes);
+
 /* Debug and ablation hooks ([H] §"標準推論スタックのボトルネックとKogの工夫": the launch
  * overhead the persistent kernel removes is measured by running the same device code as one
  * launch per phase).
