@@ -159,6 +159,11 @@ _SIGS = [
                                            ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p]),
     ("adp_paged_attention_workspace", ctypes.c_int, [ctypes.POINTER(PagedKV), ctypes.c_int32,
                                                      ctypes.POINTER(ctypes.c_uint64)]),
+    ("adp_packed_attention", ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                            ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64,
+                                            ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                            ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
+                                            ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p]),
     ("adp_debug_set_ring_slots", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32]),
     ("adp_debug_ring_slots", ctypes.c_int, [ctypes.c_void_p]),
     ("adp_debug_set_epoch_base", ctypes.c_int, [ctypes.c_void_p, ctypes.c_uint32]),
@@ -471,6 +476,14 @@ def adp_paged_attention(kv: PagedKV, q, q_dtype: int, n_heads: int, q_stride: in
     _check(load_library().adp_paged_attention(kv, _ptr(q), q_dtype, n_heads, q_stride, scale, _ptr(out), out_stride,
                                               _ptr(workspace), workspace_bytes, _ptr(dev_status), stream),
            "adp_paged_attention")
+
+
+def adp_packed_attention(q, k, v, dtype: int, n_heads: int, n_kv_heads: int, head_dim: int, q_stride: int, k_stride: int,
+                         v_stride: int, cu_q, cu_k, n_seqs: int, n_q: int, n_k: int, scale: float, out, out_stride: int,
+                         dev_status=None, stream: int = 0):
+    _check(load_library().adp_packed_attention(_ptr(q), _ptr(k), _ptr(v), dtype, n_heads, n_kv_heads, head_dim, q_stride,
+                                               k_stride, v_stride, _ptr(cu_q), _ptr(cu_k), n_seqs, n_q, n_k, scale,
+                                               _ptr(out), out_stride, _ptr(dev_status), stream), "adp_packed_attention")
 
 
 def adp_debug_set_l2_pacing(model, bytes_per_us: int, burst_bytes: int):

@@ -158,6 +158,48 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) 
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// ---- 128-byte-swizzled operands, as the tensor copies below write them: rows of 128 bytes (64 16-bit elements), eight
+// rows to an atom of 1,024 bytes, the 16-byte piece p of row r of an atom at piece p ^ (r % 8).
+
+// Descriptor of such an operand.  K-major (rows are M or N, the row holds K): sbo 1024 between 8-row groups, lbo unused;
+// 16 elements of K further is 32 bytes.  MN-major (rows are K, the row holds 64 of M or N): sbo 1024 between 8-row
+// groups of K, lbo between the 64-wide blocks of M or N; 16 rows of K further is 2,048 bytes.
+__device__ __forceinline__ uint64_t tc_smem_desc_sw128(uint32_t smem_addr, uint32_t lbo, uint32_t sbo) {
+  return tc_smem_desc(smem_addr, lbo, sbo) | (2ull << 61);
+}
+// The instruction descriptor's bit for an MN-major B operand.
+constexpr uint32_t kTcIdescBMn = 1u << 16;
+
+// D[tmem] (+)= A[tmem] * B[smem], issued by one thread.  A: lane = row, two 16-bit elements of K per 32-bit column.
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                              bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+
+// Tensor copy of a 3-D box into this CTA's shared memory, completing on an mbarrier (coordinates innermost first; the
+// innermost one times the element size is a multiple of 16 bytes; elements outside the tensor are zeros).
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Store 16 consecutive 32-bit columns of this thread's TMEM lane; tmem_st_wait before anyone is told.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // Generic-proxy writes to shared memory made visible to the tensor cores' (async proxy) reads.
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 

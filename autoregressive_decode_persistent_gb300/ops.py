@@ -1,4 +1,4 @@
-"""The paged KV cache operators on PyTorch tensors (include/adp.h has their semantics).
+"""The paged KV cache operators and packed prompt attention on PyTorch tensors (include/adp.h has their semantics).
 
 Argument checks and marshalling only: every computation runs in libadp.so's kernels, on the current
 stream of the tensors' device, without synchronising.  Nothing is differentiable.  Wrong arguments raise
@@ -166,3 +166,37 @@ def _attention(kv, q, dt, heads, scale, out, workspace, status, stream):
         workspace = torch.empty(adp.adp_paged_attention_workspace(kv, heads), dtype=torch.uint8, device=q.device)
     adp.adp_paged_attention(kv, q.data_ptr(), dt, heads, _row_stride(q), scale, out.data_ptr(), _row_stride(out),
                             workspace.data_ptr(), workspace.numel(), status, stream)
+
+
+def packed_attention(q, k, v, cu_q, cu_k, *, scale: float | None = None, out=None, status=None):
+    """Causal attention of packed prompts: q [rows, heads, head_dim], k, v [key rows, kv_heads, head_dim], f16 or bf16.
+
+    cu_q, cu_k: int32 [seqs + 1] row offsets; query i of a sequence with lq queries and lk keys sees keys up to
+    i + lk - lq.  scale: default 1 / sqrt(head_dim).  Rows of q from cu_q[-1] on are padding: their rows of `out`
+    are left as they were (unset where out is allocated here)."""
+    where = "packed_attention"
+    device = q.device
+    if device.type != "cuda" or q.dim() != 3 or k.dim() != 3:
+        _refuse(where, "q, k and v must be [rows, heads, head_dim] on a CUDA device")
+    n_q, heads, hd = q.shape
+    n_k, kv_heads, _ = k.shape
+    _rows(where, "q", q, None, hd, device)
+    _rows(where, "k", k, kv_heads, hd, device)
+    _rows(where, "v", v, kv_heads, hd, device)
+    dt = _HALF.get(q.dtype)
+    if dt is None or k.dtype != q.dtype or v.dtype != q.dtype or v.shape[0] != n_k:
+        _refuse(where, "q, k and v must be alike, of f16 or bf16, with as many rows of v as of k")
+    _indices(where, "cu_q", cu_q, 1, device)
+    _indices(where, "cu_k", cu_k, 1, device)
+    if cu_q.shape[0] < 1 or cu_k.shape != cu_q.shape:
+        _refuse(where, "cu_q and cu_k must both have one entry more than there are sequences")
+    if out is None:
+        out = torch.empty((n_q, heads, hd), dtype=q.dtype, device=device)
+    else:
+        _rows(where, "out", out, heads, hd, device)
+        if out.dtype != q.dtype or out.shape[0] != n_q:
+            _refuse(where, "out must be like q")
+    _call(device, adp.adp_packed_attention, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, heads, kv_heads, hd, _row_stride(q),
+          _row_stride(k), _row_stride(v), cu_q.data_ptr(), cu_k.data_ptr(), cu_q.shape[0] - 1, n_q, n_k,
+          hd ** -0.5 if scale is None else scale, out.data_ptr(), _row_stride(out), _status(where, status, device))
+    return out

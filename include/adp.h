@@ -337,14 +337,15 @@ int adp_launches_per_step(const adp_model* m, int32_t* n);      /* kernel launch
 int adp_measure_read_bandwidth(const void* dev_buf, uint64_t bytes, int32_t reps, void* cuda_stream,
                                double* gb_per_s);
 
-/* ---- Operators over a paged KV cache.
+/* ---- Operators over a paged KV cache, and packed prompt attention.
  *
  * The caches above belong to one request each and to the persistent kernels, whose batch is small.
  * The operators below serve many requests of one layer at a time from caller-owned memory: K/V rows
  * are written into the pages of a shared pool (16-bit, or quantised to e4m3 as they are written), read
- * back, and attended to by one new token per sequence.  The pages name attention, and the KV cache as
- * the other stream of a decode step ([H] §"GPU推論の速度制限要因：メモリ帯域幅"), and fix no paged
- * algorithm; these operators are not part of the persistent step's arithmetic contract.
+ * back, and attended to by one new token per sequence; packed prompts attend to their own keys on the
+ * tensor cores.  The pages name attention, and the KV cache as the other stream of a decode step ([H]
+ * §"GPU推論の速度制限要因：メモリ帯域幅"), and fix no paged algorithm; these operators are not part of
+ * the persistent step's arithmetic contract.
  *
  * All of them enqueue on `cuda_stream` (NULL: the legacy default stream) and return without
  * synchronising; they allocate nothing and may be captured into a CUDA graph.  Arguments that the host
@@ -415,6 +416,25 @@ int adp_paged_attention(const adp_paged_kv* kv, const void* q, int32_t q_dtype, 
 /* Bytes of scratch adp_paged_attention needs for this cache (a few MB at most; asks the current device for
  * its SM count). */
 int adp_paged_attention_workspace(const adp_paged_kv* kv, int32_t n_heads, uint64_t* bytes);
+
+/* Causal attention of packed prompts: query i of sequence s (row cu_q[s] + i) sees keys j <= i + (lk - lq) of
+ * sequence s, lq and lk its numbers of query and key rows, so that the last query sees every key: a prompt's
+ * chunk behind a cached prefix has more keys than queries.  out = softmax(scale q . K) V as above.
+ *  q, out      DEVICE [n_q][n_heads][head_dim] of dtype (ADP_F16 or ADP_BF16), rows q_stride / out_stride
+ *              elements apart (multiples of 8), 16-byte aligned
+ *  k, v        DEVICE [n_k][n_kv_heads][head_dim] of dtype, rows k_stride / v_stride elements apart
+ *  cu_q, cu_k  DEVICE [n_seqs + 1], ascending from 0; query rows from cu_q[n_seqs] on are padding, and their rows of
+ *              out are left as they were
+ *  n_heads     a multiple of n_kv_heads, at most 128 times as many
+ *  scale       finite
+ * Scores, softmax and sums are fp32; probabilities are rounded to dtype before they weigh V.  A query that sees
+ * no key gives zeros.  Keys and values that a query does not see do not reach it, whatever they hold.  Offsets
+ * that descend or lie outside [0, n_q] / [0, n_k] are cut to it and reported as ADP_ERR_INVALID_ARG; a wait
+ * inside the kernel that ran out is reported as ADP_ERR_PIPELINE_TIMEOUT.  Needs no workspace. */
+int adp_packed_attention(const void* q, const void* k, const void* v, int32_t dtype, int32_t n_heads,
+                         int32_t n_kv_heads, int32_t head_dim, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                         const int32_t* cu_q, const int32_t* cu_k, int32_t n_seqs, int32_t n_q, int32_t n_k,
+                         float scale, void* out, int64_t out_stride, int32_t* dev_status, void* cuda_stream);
 
 /* Debug and ablation hooks ([H] §"標準推論スタックのボトルネックとKogの工夫": the launch
  * overhead the persistent kernel removes is measured by running the same device code as one
