@@ -15,7 +15,7 @@ namespace adp {
 
 constexpr int kPagedMaxSeqs = 8192;   // sequences of one attention call
 constexpr int kPagedMaxPage = 1024;   // positions of a page
-constexpr int kPagedWarps = 8;        // warps of an attention CTA, each with a share of the CTA's units
+constexpr int kPagedWarps = 4;        // warps of an attention CTA, each with a share of the CTA's units
 
 // Cached positions of a sequence: its length, within what its table row can name.
 ADP_INLINE int32_t paged_length(int32_t len, int32_t table_width, int log2_page) {

@@ -42,15 +42,19 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xFFFFu), __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// Four e4m3 codes as fp16 (exact): the low pair and the high pair.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
 }
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+constexpr float kStale = 8.0f;  // how far scores may exceed the maximum in use (base-2 exponents)
+
 __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.0f : m; }
 
 // Softmax state of a piece of a segment, in shared or global memory.
@@ -77,6 +81,10 @@ struct AttnArgs {
   int32_t* status;
 };
 
+// CTAs per SM: 12 warps of 168 registers, or 8 of 255 for the wider tile of heads.
+template <int NT>
+constexpr int kResident = NT == 1 ? 3 : 2;
+
 // One new token per sequence over its pages.  The line of units (a unit: 4 KB of keys, i.e. 16 to 64 positions, of
 // one sequence, KV head and tile of up to 8 NT query heads) is cut into even ranges, one per CTA and in it one per
 // warp, whatever the sequences' lengths are: a long context spreads over the GPU and short ones share a warp.
@@ -90,7 +98,7 @@ struct AttnArgs {
 // query heads as the 8-wide side a group of up to 8 heads costs one instruction per 16 x 16 of K; nothing is staged
 // in shared memory.  e4m3 codes become fp16 (exact), their scales multiply the scores and the probabilities.
 template <int HD, int CDT, int QDT, int NT, bool SMALL>
-__global__ void __launch_bounds__(kPagedWarps * 32, 1) paged_attention_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attention_kernel(AttnArgs a) {
   constexpr int EB = elem_bytes(CDT);
   constexpr int ROWB = HD * EB;
   constexpr int UNIT = 4096 / ROWB;  // positions
@@ -260,6 +268,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, 1) paged_attention_kernel(At
       uint32_t kr[RG][2][KC * 4];
       uint32_t vr[RG][4][VW];
       float ksc[RG][2], vsc[RG][2];
+      const int in_page = (1 << c.log2_page) - 1;
       // Page of a position that is attended, else -1.
       auto page_at = [&](int pos) {
         if (pos >= len) return -1;
@@ -267,16 +276,57 @@ __global__ void __launch_bounds__(kPagedWarps * 32, 1) paged_attention_kernel(At
         if (page < 0) report(a.status, ADP_ERR_INVALID_ARG);
         return page;
       };
-      const int in_page = (1 << c.log2_page) - 1;
-      int pg[RG];  // pages of the next unit's groups (pages of 16 positions and more: a group lies in one)
+      // Where the next unit's groups of 16 positions lie (pages of 16 positions and more: a group lies in one page),
+      // and whether all its positions are attended.
+      int pg[RG];
+      bool next_full = false;
       auto fetch_pages = [&](int ut) {
+        next_full = !SMALL && (ut + 1) * UNIT <= len;
         if constexpr (!SMALL) {
 #pragma unroll
-          for (int g = 0; g < RG; ++g) pg[g] = page_at(ut * UNIT + g * 16);
+          for (int g = 0; g < RG; ++g) {
+            pg[g] = page_at(ut * UNIT + g * 16);
+            next_full &= pg[g] >= 0;
+          }
         }
       };
-      uint32_t kmask = 0;  // bit 2 g + j: position row j of group g is attended
+      auto load_k16 = [&](int g, int j, const uint8_t* p) {
+#pragma unroll
+        for (int kc = 0; kc < KC; ++kc) {
+          const uint4 w = ldg16(p + kc * 64);
+          kr[g][j][kc * 4] = w.x, kr[g][j][kc * 4 + 1] = w.y, kr[g][j][kc * 4 + 2] = w.z, kr[g][j][kc * 4 + 3] = w.w;
+        }
+      };
+      auto load_v16 = [&](int g, int j, const uint8_t* p) {
+        if constexpr (VB >= 16) {
+#pragma unroll
+          for (int h = 0; h < VB / 16; ++h) {
+            const uint4 w = ldg16(p + h * 128);
+            vr[g][j][h * 4] = w.x, vr[g][j][h * 4 + 1] = w.y, vr[g][j][h * 4 + 2] = w.z, vr[g][j][h * 4 + 3] = w.w;
+          }
+        } else {
+          const uint2 w = ldg8(p);
+          vr[g][j][0] = w.x, vr[g][j][1] = w.y;
+        }
+      };
+      const int k_lane = r8 * ROWB + l4 * 16, v_lane = 2 * l4 * ROWB + r8 * (VB >= 16 ? 16 : 8);
+      uint32_t kmask = 0;  // bit 2 g + j: position row j of group g is attended (of a unit that is not full)
       auto load_k = [&](int ut) {
+        if (next_full) {
+#pragma unroll
+          for (int g = 0; g < RG; ++g) {
+            const int cell = (kvh << c.log2_page) + ((ut * UNIT + g * 16) & in_page);
+            const uint8_t* p = c.k + (int64_t)pg[g] * c.page_bytes + (int64_t)cell * ROWB + k_lane;
+            load_k16(g, 0, p);
+            load_k16(g, 1, p + 8 * ROWB);
+            if constexpr (Q8) {
+              const int64_t at = (int64_t)pg[g] * c.scale_stride + cell + r8;
+              ksc[g][0] = __ldg(c.k_scale + at), ksc[g][1] = __ldg(c.k_scale + at + 8);
+              vsc[g][0] = __ldg(c.v_scale + at), vsc[g][1] = __ldg(c.v_scale + at + 8);
+            }
+          }
+          return;
+        }
         kmask = 0;
 #pragma unroll
         for (int g = 0; g < RG; ++g) {
@@ -284,43 +334,45 @@ __global__ void __launch_bounds__(kPagedWarps * 32, 1) paged_attention_kernel(At
           for (int j = 0; j < 2; ++j) {
             const int pos = ut * UNIT + g * 16 + r8 + 8 * j;
             const int page = SMALL ? page_at(pos) : pg[g];
-            const bool on = page >= 0 && pos < len;
-            const int64_t cell = ((int64_t)kvh << c.log2_page) + (pos & in_page);
-            const uint8_t* p = c.k + (int64_t)page * c.page_bytes + cell * ROWB;
-            kmask |= (on ? 1u : 0u) << (2 * g + j);
-#pragma unroll
-            for (int kc = 0; kc < KC; ++kc) {
-              const uint4 w = on ? ldg16(p + kc * 64 + l4 * 16) : make_uint4(0, 0, 0, 0);
-              kr[g][j][kc * 4] = w.x, kr[g][j][kc * 4 + 1] = w.y, kr[g][j][kc * 4 + 2] = w.z, kr[g][j][kc * 4 + 3] = w.w;
-            }
-            if constexpr (Q8) {
-              ksc[g][j] = vsc[g][j] = 0.0f;
-              if (on) {
+            ksc[g][j] = vsc[g][j] = 0.0f;
+            if (page >= 0 && pos < len) {
+              const int cell = (kvh << c.log2_page) + (pos & in_page);
+              kmask |= 1u << (2 * g + j);
+              load_k16(g, j, c.k + (int64_t)page * c.page_bytes + (int64_t)cell * ROWB + l4 * 16);
+              if constexpr (Q8) {
                 ksc[g][j] = __ldg(c.k_scale + (int64_t)page * c.scale_stride + cell);
                 vsc[g][j] = __ldg(c.v_scale + (int64_t)page * c.scale_stride + cell);
               }
+            } else {
+#pragma unroll
+              for (int w = 0; w < KC * 4; ++w) kr[g][j][w] = 0;
             }
           }
         }
       };
-      auto load_v = [&](int ut) {
+      auto load_v = [&](int ut, bool full) {
+        if (full) {
+#pragma unroll
+          for (int g = 0; g < RG; ++g) {
+            const int cell = (kvh << c.log2_page) + ((ut * UNIT + g * 16) & in_page);
+            const uint8_t* p = c.v + (int64_t)pg[g] * c.page_bytes + (int64_t)cell * ROWB + v_lane;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) load_v16(g, j, p + ((j & 1) + 8 * (j >> 1)) * ROWB);
+          }
+          return;
+        }
 #pragma unroll
         for (int g = 0; g < RG; ++g) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int pos = ut * UNIT + g * 16 + 2 * l4 + (j & 1) + 8 * (j >> 1);
             const int page = SMALL ? page_at(pos) : pg[g];
-            const bool on = page >= 0 && pos < len;
-            const uint8_t* p = c.v + (int64_t)page * c.page_bytes + (((int64_t)kvh << c.log2_page) + (pos & in_page)) * ROWB;
-            if constexpr (VB >= 16) {
-#pragma unroll
-              for (int h = 0; h < VB / 16; ++h) {
-                const uint4 w = on ? ldg16(p + (h * 8 + r8) * 16) : make_uint4(0, 0, 0, 0);
-                vr[g][j][h * 4] = w.x, vr[g][j][h * 4 + 1] = w.y, vr[g][j][h * 4 + 2] = w.z, vr[g][j][h * 4 + 3] = w.w;
-              }
+            if (page >= 0 && pos < len) {
+              const int cell = (kvh << c.log2_page) + (pos & in_page);
+              load_v16(g, j, c.v + (int64_t)page * c.page_bytes + (int64_t)cell * ROWB + r8 * (VB >= 16 ? 16 : 8));
             } else {
-              const uint2 w = on ? ldg8(p + r8 * 8) : make_uint2(0, 0);
-              vr[g][j][0] = w.x, vr[g][j][1] = w.y;
+#pragma unroll
+              for (int w = 0; w < VW; ++w) vr[g][j][w] = 0;
             }
           }
         }
@@ -328,9 +380,9 @@ __global__ void __launch_bounds__(kPagedWarps * 32, 1) paged_attention_kernel(At
 
       fetch_pages(t);
       load_k(t);
-      load_v(t);
+      load_v(t, next_full);
       for (int i = 0; i < n; ++i) {
-        const bool more = i + 1 < n;
+        const bool more = i + 1 < n, full = next_full;
         if (more) fetch_pages(t + i + 1);
         // ---- S^T = K Q^T: rows are keys, columns heads
         float s[RG][NT][4];
@@ -342,9 +394,8 @@ __global__ void __launch_bounds__(kPagedWarps * 32, 1) paged_attention_kernel(At
           for (int ks = 0; ks < MT; ++ks) {
             uint32_t f[4];
             if constexpr (Q8) {
-              const uint32_t w0 = kr[g][0][ks], w1 = kr[g][1][ks];
-              f[0] = e4m3x2_to_f16x2(w0), f[1] = e4m3x2_to_f16x2(w1);
-              f[2] = e4m3x2_to_f16x2(w0 >> 16), f[3] = e4m3x2_to_f16x2(w1 >> 16);
+              e4m3x4_to_f16(kr[g][0][ks], f[0], f[2]);
+              e4m3x4_to_f16(kr[g][1][ks], f[1], f[3]);
             } else {
               f[0] = kr[g][0][2 * ks], f[1] = kr[g][1][2 * ks], f[2] = kr[g][0][2 * ks + 1], f[3] = kr[g][1][2 * ks + 1];
             }
@@ -361,60 +412,64 @@ __global__ void __launch_bounds__(kPagedWarps * 32, 1) paged_attention_kernel(At
             for (int j = 0; j < 2; ++j) ks_now[g][j] = ksc[g][j], vs_now[g][j] = vsc[g][j];
         }
         if (more) load_k(t + i + 1);
-        // ---- running maximum
-        float grow = 1.0f;  // e4m3: the old unit of O in the new one
+        // ---- scores in base-2 exponents; the running maximum (and e4m3's unit of O) are replaced only when some score
+        // exceeds the maximum by more than 8, decided per warp: till then the weights stay below 2^8, and the same
+        // stale maximum scales O and l alike
+        bool need = false;
+        float vtop = 0.0f;
         if constexpr (Q8) {
-          float top = 0.0f;
 #pragma unroll
-          for (int g = 0; g < RG; ++g) top = fmaxf(top, fmaxf(vs_now[g][0], vs_now[g][1]));
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-          if (top > vref) {
-            const float nref = __uint_as_float((__float_as_uint(top) + 0x7FFFFFu) & 0x7F800000u);
-            vinv = 1.0f / nref;
-            grow = vref * vinv;
-            vref = nref;
-          }
+          for (int g = 0; g < RG; ++g) vtop = fmaxf(vtop, fmaxf(vs_now[g][0], vs_now[g][1]));
+          need = vtop > vref;
         }
-        float alpha[NT][2];
-        bool change = grow != 1.0f;
+        float top[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float top = -INFINITY;
+            top[nt][j] = -INFINITY;
 #pragma unroll
             for (int g = 0; g < RG; ++g)
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
                 float x = s[g][nt][2 * r + j] * qs[nt][j];
                 if constexpr (Q8) x *= ks_now[g][r];
-                x = (on >> (2 * g + r)) & 1 ? x : -INFINITY;
+                if (!full) x = (on >> (2 * g + r)) & 1 ? x : -INFINITY;
                 s[g][nt][2 * r + j] = x;
-                top = fmaxf(top, x);
+                top[nt][j] = fmaxf(top[nt][j], x);
               }
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-            const float mn = fmaxf(m[nt][j], top);
-            change |= mn != m[nt][j];
-            alpha[nt][j] = exp2_fast(m[nt][j] - safe_max(mn));
-            m[nt][j] = mn;
+            need |= top[nt][j] > m[nt][j] + kStale;
           }
         }
-        if (__any_sync(0xFFFFFFFFu, change)) {
+        if (__any_sync(0xFFFFFFFFu, need)) {
+          float grow = 1.0f;  // e4m3: the old unit of O in the new one
+          if constexpr (Q8) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            l[nt][0] *= alpha[nt][0];
-            l[nt][1] *= alpha[nt][1];
-            const float f0 = alpha[nt][0] * grow, f1 = alpha[nt][1] * grow;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              o[mt][nt][0] *= f0, o[mt][nt][2] *= f0;
-              o[mt][nt][1] *= f1, o[mt][nt][3] *= f1;
+            for (int d = 4; d <= 16; d <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xFFFFFFFFu, vtop, d));
+            if (vtop > vref) {
+              const float nref = __uint_as_float((__float_as_uint(vtop) + 0x7FFFFFu) & 0x7F800000u);
+              vinv = 1.0f / nref;
+              grow = vref * vinv;
+              vref = nref;
             }
           }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float mn = top[nt][j];
+#pragma unroll
+              for (int d = 4; d <= 16; d <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, d));
+              mn = fmaxf(m[nt][j], mn);
+              const float f = exp2_fast(m[nt][j] - safe_max(mn));
+              m[nt][j] = mn;
+              l[nt][j] *= f;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                o[mt][nt][j] *= f * grow;
+                o[mt][nt][2 + j] *= f * grow;
+              }
+            }
         }
         // ---- P, and O^T += V^T P^T
 #pragma unroll
@@ -439,11 +494,11 @@ __global__ void __launch_bounds__(kPagedWarps * 32, 1) paged_attention_kernel(At
           for (int w = 0; w < VW; ++w) {
             const uint32_t x0 = vr[g][0][w], x1 = vr[g][1][w], x2 = vr[g][2][w], x3 = vr[g][3][w];
             if constexpr (Q8) {
-              const uint32_t ya = __byte_perm(x0, x1, 0x5140), yb = __byte_perm(x2, x3, 0x5140);
-              const uint32_t za = __byte_perm(x0, x1, 0x7362), zb = __byte_perm(x2, x3, 0x7362);
-              const uint32_t f[8] = {e4m3x2_to_f16x2(ya), e4m3x2_to_f16x2(ya >> 16), e4m3x2_to_f16x2(yb),
-                                     e4m3x2_to_f16x2(yb >> 16), e4m3x2_to_f16x2(za), e4m3x2_to_f16x2(za >> 16),
-                                     e4m3x2_to_f16x2(zb), e4m3x2_to_f16x2(zb >> 16)};
+              uint32_t f[8];
+              e4m3x4_to_f16(__byte_perm(x0, x1, 0x5140), f[0], f[1]);
+              e4m3x4_to_f16(__byte_perm(x2, x3, 0x5140), f[2], f[3]);
+              e4m3x4_to_f16(__byte_perm(x0, x1, 0x7362), f[4], f[5]);
+              e4m3x4_to_f16(__byte_perm(x2, x3, 0x7362), f[6], f[7]);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 mma16<BF>(o[2 * w][nt], f[0], f[1], f[2], f[3], pf[nt][0], pf[nt][1]);
@@ -457,7 +512,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, 1) paged_attention_kernel(At
             }
           }
         }
-        if (more) load_v(t + i + 1);
+        if (more) load_v(t + i + 1, next_full);
       }
 
       // ---- end of the piece: sums over the lanes that share a head
@@ -639,12 +694,13 @@ __global__ void __launch_bounds__(128) paged_attention_join_kernel(AttnArgs a) {
 // Query heads per KV head take tiles of 8 (a group of up to 8) or 16 columns of the tensor instruction.
 int head_tiles(int group) { return group <= 8 ? 1 : 2; }
 
-// CTAs of an attention call: one per SM, or fewer where even full tables would not fill them.
+// CTAs of an attention call: as many as can be resident, or fewer where even full tables would not fill them.
 int attention_ctas(const adp_paged_kv* kv, int group, int sms) {
   const int nt = head_tiles(group), tiles = (group + nt * 8 - 1) / (nt * 8);
   const int unit = 4096 / (kv->head_dim * elem_bytes(kv->dtype));
   const int64_t per_seq = ((int64_t)kv->table_width * kv->page_size + unit - 1) / unit;
-  return split_parts(per_seq * kv->n_kv_heads * tiles * (kv->n_seqs > 0 ? kv->n_seqs : 1), sms);
+  return split_parts(per_seq * kv->n_kv_heads * tiles * (kv->n_seqs > 0 ? kv->n_seqs : 1),
+                     sms * (nt == 1 ? kResident<1> : kResident<2>));
 }
 
 size_t attention_bytes(int ctas, int nt, int hd) {

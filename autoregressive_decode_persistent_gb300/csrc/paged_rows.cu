@@ -12,6 +12,7 @@ namespace adp {
 namespace {
 
 constexpr float kE4m3Max = 448.0f;
+constexpr float kScaleFast = 8.2718061e-25f;  // 2^-80: above it no remainder of a quotient over 2^-11 underflows
 
 // The sequence that packed row i belongs to: the number of entries of cu[1 .. n] that are at most i (n for
 // rows behind the last sequence).  A whole warp asks; 32 entries are compared at a time.
@@ -125,8 +126,20 @@ __global__ void __launch_bounds__(256)
         for (int d = LPR / 2; d >= 1; d >>= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
         const float s = max_nan(__fdiv_rn(top, kE4m3Max), kScaleMin);
         if (on[a]) {
+          if (s > kScaleFast) {
+            // x / s correctly rounded by one correction of x times the correctly rounded 1 / s (Markstein, "Computation
+            // of elementary functions on the IBM RISC System/6000", 1990); a remainder that underflows belongs to a
+            // quotient whose code is 0 either way
+            const float inv = __frcp_rn(s);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[a][e] = __fdiv_rn(x[a][e], s);
+            for (int e = 0; e < 8; ++e) {
+              const float y = __fmul_rn(x[a][e], inv);
+              x[a][e] = fmaf(fmaf(-y, s, x[a][e]), inv, y);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[a][e] = __fdiv_rn(x[a][e], s);
+          }
           store_row8<DT_E4M3>(cell[a], x[a]);
           if (lane % LPR == 0) *scale[a] = s;
         }

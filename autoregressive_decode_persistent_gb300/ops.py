@@ -20,73 +20,84 @@ def _refuse(where: str, what: str):
     raise adp.AdpError(adp.ADP_ERR_INVALID_ARG, f"{where}: {what}")
 
 
-def _indices(where: str, name: str, t: torch.Tensor, dims: int, device):
-    if t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous() or t.device != device:
-        _refuse(where, f"{name} must be a contiguous int32 tensor of {dims} dimension(s) on {device}")
+# The checks below read each tensor's properties once: on the host of a GB300 a property costs about 0.1 us, and a
+# call's marshalling is what its smallest uses wait for.
 
-
-def _rows(where: str, name: str, t: torch.Tensor, heads: int | None, hd: int, device):
-    """A [n, heads, head_dim] tensor whose rows may lie apart."""
-    if (t.dim() != 3 or t.shape[2] != hd or (heads is not None and t.shape[1] != heads) or t.device != device
-            or (t.numel() and (t.stride(2) != 1 or (t.stride(1) != hd and t.shape[1] > 1)))):
-        _refuse(where, f"{name} must be [rows, heads, head_dim] on {device} with contiguous heads")
-
-
-def _row_stride(t: torch.Tensor) -> int:
-    """Elements from one row to the next (of a single row the stride says nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-
-
-def _status(where: str, t: torch.Tensor | None, device):
-    if t is None:
-        return None
-    if t.dtype != torch.int32 or t.numel() != 1 or t.device != device:
-        _refuse(where, f"status must be one int32 on {device}")
+def _indices(where: str, name: str, t: torch.Tensor, n: int, device: int) -> int:
+    """Address of a contiguous int32 [n] tensor on the device."""
+    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous() or t.get_device() != device:
+        _refuse(where, f"{name} must be a contiguous int32 tensor [{n}] on device {device}")
     return t.data_ptr()
 
 
-def _stream(device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
+def _rows(where: str, name: str, t: torch.Tensor, shape, dtype, device: int) -> int:
+    """Elements from one row to the next of a [rows, heads, head_dim] tensor whose rows may lie apart."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        _refuse(where, f"{name} must be {tuple(shape)} of {dtype} on device {device}")
+    n, heads, hd = shape
+    if t.is_contiguous() or n == 0:
+        return heads * hd
+    rows, between, inner = t.stride()
+    if inner != 1 or (between != hd and heads > 1):
+        _refuse(where, f"{name} must have contiguous heads")
+    return rows if n > 1 else heads * hd  # (the stride of a single row says nothing)
 
 
-def _call(device, fn, *args):
+def _status(where: str, t: torch.Tensor | None, device: int):
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or t.numel() != 1 or t.get_device() != device:
+        _refuse(where, f"status must be one int32 on device {device}")
+    return t.data_ptr()
+
+
+def _call(device: int, fn, *args):
     """fn(*args, stream) with the tensors' device current."""
-    if device.index == torch.cuda.current_device():
-        fn(*args, _stream(device))
+    if device == torch._C._cuda_getDevice():
+        fn(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
         with torch.cuda.device(device):
-            fn(*args, _stream(device))
+            fn(*args, torch._C._cuda_getCurrentRawStream(device))
 
 
-def _paged(where: str, k_pages, v_pages, table, lens, k_scale, v_scale) -> adp.PagedKV:
-    shape, stride, device = k_pages.shape, k_pages.stride(), k_pages.device
-    if device.type != "cuda":
+def _paged(where: str, k_pages, v_pages, table, lens, k_scale, v_scale, device: int) -> adp.PagedKV:
+    if not k_pages.is_cuda:
         _refuse(where, "the tensors must be on a CUDA device")
-    dtype = _CACHE.get(k_pages.dtype)
-    if dtype is None or len(shape) != 4 or v_pages.dtype != k_pages.dtype or v_pages.shape != shape \
-            or v_pages.stride() != stride or v_pages.device != device:
+    shape, torch_dtype = k_pages.shape, k_pages.dtype
+    dtype = _CACHE.get(torch_dtype)
+    if dtype is None or len(shape) != 4 or v_pages.dtype is not torch_dtype or v_pages.shape != shape \
+            or v_pages.get_device() != device:
         _refuse(where, "k_pages and v_pages must be alike: [pages, kv_heads, page_size, head_dim], f16, bf16 or e4m3")
     n_pages, heads, ps, hd = shape
-    if (stride[3] != 1 or (stride[2] != hd and ps > 1) or (stride[1] != ps * hd and heads > 1)) and k_pages.numel():
-        _refuse(where, "a page must be contiguous")
-    _indices(where, "table", table, 2, device)
-    _indices(where, "lens", lens, 1, device)
+    page = heads * ps * hd
+    if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
+        stride = k_pages.stride()
+        if v_pages.stride() != stride:
+            _refuse(where, "k_pages and v_pages must have the same strides")
+        if page and (stride[3] != 1 or (stride[2] != hd and ps > 1) or (stride[1] != ps * hd and heads > 1)):
+            _refuse(where, "a page must be contiguous")
+        if n_pages > 1:  # (the stride of a single page says nothing)
+            page = stride[0]
+    if table.dtype is not torch.int32 or len(table.shape) != 2 or not table.is_contiguous() or table.get_device() != device:
+        _refuse(where, f"table must be a contiguous int32 tensor [seqs, width] on device {device}")
     n_seqs, width = table.shape
-    if lens.shape[0] != n_seqs:
-        _refuse(where, "table and lens must name the same sequences")
+    at = _indices(where, "lens", lens, n_seqs, device)
     ks = vs = None
-    ss = 0
+    scales = heads * ps
     if dtype == adp.ADP_E4M3:
-        if k_scale is None or v_scale is None or k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 \
-                or k_scale.shape != shape[:3] or v_scale.shape != shape[:3] or k_scale.device != device \
-                or v_scale.device != device or k_scale.stride() != v_scale.stride() \
-                or (k_scale.stride(2) != 1 and ps > 1) or (k_scale.stride(1) != ps and heads > 1):
-            _refuse(where, "e4m3 pages need k_scale and v_scale alike: fp32 [pages, kv_heads, page_size]")
-        ks, vs, ss = k_scale.data_ptr(), v_scale.data_ptr(), k_scale.stride(0)
-    # (the stride of a single page says nothing)
-    return adp.PagedKV(k_pages.data_ptr(), v_pages.data_ptr(), ks, vs, table.data_ptr(), lens.data_ptr(),
-                       stride[0] if n_pages > 1 else heads * ps * hd, ss if n_pages > 1 else heads * ps,
-                       n_pages, ps, heads, hd, dtype, n_seqs, width)
+        if k_scale is None or v_scale is None or k_scale.dtype is not torch.float32 \
+                or v_scale.dtype is not torch.float32 or k_scale.shape != shape[:3] or v_scale.shape != shape[:3] \
+                or k_scale.get_device() != device or v_scale.get_device() != device:
+            _refuse(where, "e4m3 pages need k_scale and v_scale: fp32 [pages, kv_heads, page_size]")
+        if not (k_scale.is_contiguous() and v_scale.is_contiguous()):
+            stride = k_scale.stride()
+            if v_scale.stride() != stride or (stride[2] != 1 and ps > 1) or (stride[1] != ps and heads > 1):
+                _refuse(where, "k_scale and v_scale must have the same strides, and contiguous pages")
+            if n_pages > 1:
+                scales = stride[0]
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    return adp.PagedKV(k_pages.data_ptr(), v_pages.data_ptr(), ks, vs, table.data_ptr(), at, page, scales, n_pages, ps, heads,
+                       hd, dtype, n_seqs, width)
 
 
 def paged_kv_write(k_pages, v_pages, table, lens, cu_rows, k, v, *, k_scale=None, v_scale=None, status=None):
@@ -95,9 +106,7 @@ def paged_kv_write(k_pages, v_pages, table, lens, cu_rows, k, v, *, k_scale=None
     k_pages, v_pages: [pages, kv_heads, page_size, head_dim] f16, bf16 or float8_e4m3fn (then with fp32
     k_scale, v_scale [pages, kv_heads, page_size]), changed in place.  table: int32 [seqs, width] page numbers;
     lens: int32 [seqs], the rows being written included; cu_rows: int32 [seqs + 1]."""
-    where = "paged_kv_write"
-    kv = _paged(where, k_pages, v_pages, table, lens, k_scale, v_scale)
-    _transfer(where, adp.adp_paged_kv_write, kv, k_pages.device, cu_rows, k, v, status)
+    _transfer("paged_kv_write", adp.adp_paged_kv_write, k_pages, v_pages, table, lens, cu_rows, k, v, k_scale, v_scale, status)
 
 
 def paged_kv_read(k_pages, v_pages, table, lens, cu_rows, n_rows: int, *, dtype=None, k_scale=None, v_scale=None,
@@ -106,31 +115,31 @@ def paged_kv_read(k_pages, v_pages, table, lens, cu_rows, n_rows: int, *, dtype=
 
     Returns (k, v) [n_rows, kv_heads, head_dim] of `dtype` (default: the pages' type, fp16 for e4m3 pages), or
     writes into out = (k, v); rows from cu_rows[-1] on are left as they were."""
-    where = "paged_kv_read"
-    kv = _paged(where, k_pages, v_pages, table, lens, k_scale, v_scale)
     if out is None:
         if dtype is None:
-            dtype = torch.float16 if kv.dtype == adp.ADP_E4M3 else k_pages.dtype
-        shape = (n_rows, kv.n_kv_heads, kv.head_dim)
-        out = (torch.empty(shape, dtype=dtype, device=k_pages.device), torch.empty(shape, dtype=dtype, device=k_pages.device))
-    k, v = out
-    if k.shape[0] != n_rows or (dtype is not None and k.dtype != dtype):
-        _refuse(where, "out must hold n_rows rows of dtype")
-    _transfer(where, adp.adp_paged_kv_read, kv, k_pages.device, cu_rows, k, v, status)
-    return k, v
+            dtype = torch.float16 if k_pages.dtype is torch.float8_e4m3fn else k_pages.dtype
+        _, heads, _, hd = k_pages.shape
+        like = dict(dtype=dtype, device=k_pages.device)
+        k, v = out = torch.empty((n_rows, heads, hd), **like), torch.empty((n_rows, heads, hd), **like)
+    else:
+        k, v = out
+        if k.shape[0] != n_rows or (dtype is not None and k.dtype is not dtype):
+            _refuse("paged_kv_read", "out must hold n_rows rows of dtype")
+    _transfer("paged_kv_read", adp.adp_paged_kv_read, k_pages, v_pages, table, lens, cu_rows, k, v, k_scale, v_scale, status)
+    return out
 
 
-def _transfer(where, call, kv, device, cu_rows, k, v, status):
-    _indices(where, "cu_rows", cu_rows, 1, device)
-    if cu_rows.shape[0] != kv.n_seqs + 1:
-        _refuse(where, "cu_rows must have one entry more than there are sequences")
-    _rows(where, "k", k, kv.n_kv_heads, kv.head_dim, device)
-    _rows(where, "v", v, kv.n_kv_heads, kv.head_dim, device)
-    dt = _ROWS.get(k.dtype)
-    if dt is None or v.dtype != k.dtype or v.shape != k.shape:
-        _refuse(where, "k and v rows must be alike, of f16, bf16 or f32")
-    _call(device, call, kv, k.data_ptr(), v.data_ptr(), dt, _row_stride(k), _row_stride(v), cu_rows.data_ptr(), k.shape[0],
-          _status(where, status, device))
+def _transfer(where, call, k_pages, v_pages, table, lens, cu_rows, k, v, k_scale, v_scale, status):
+    device = k_pages.get_device()
+    kv = _paged(where, k_pages, v_pages, table, lens, k_scale, v_scale, device)
+    cu = _indices(where, "cu_rows", cu_rows, kv.n_seqs + 1, device)
+    dtype, n = k.dtype, k.shape[0]
+    dt = _ROWS.get(dtype)
+    if dt is None:
+        _refuse(where, "k and v rows must be of f16, bf16 or f32")
+    shape = (n, kv.n_kv_heads, kv.head_dim)
+    ks, vs = _rows(where, "k", k, shape, dtype, device), _rows(where, "v", v, shape, dtype, device)
+    _call(device, call, kv, k.data_ptr(), v.data_ptr(), dt, ks, vs, cu, n, _status(where, status, device))
 
 
 def paged_attention(q, k_pages, v_pages, table, lens, *, scale: float | None = None, k_scale=None, v_scale=None,
@@ -140,32 +149,34 @@ def paged_attention(q, k_pages, v_pages, table, lens, *, scale: float | None = N
     scale: default 1 / sqrt(head_dim).  workspace: optional uint8 tensor of adp.adp_paged_attention_workspace
     bytes (not shared by calls that may run at the same time); by default one is allocated on the current stream."""
     where = "paged_attention"
-    kv = _paged(where, k_pages, v_pages, table, lens, k_scale, v_scale)
-    device, hd = k_pages.device, kv.head_dim
-    _rows(where, "q", q, None, hd, device)
-    dt = _HALF.get(q.dtype)
-    if dt is None or q.shape[0] != kv.n_seqs:
-        _refuse(where, "q must have one f16 or bf16 row per sequence")
-    n, heads, _ = q.shape
+    device = k_pages.get_device()
+    kv = _paged(where, k_pages, v_pages, table, lens, k_scale, v_scale, device)
+    dtype, shape = q.dtype, q.shape
+    dt = _HALF.get(dtype)
+    if dt is None or len(shape) != 3 or shape[0] != kv.n_seqs or shape[2] != kv.head_dim:
+        _refuse(where, "q must be [seqs, heads, head_dim] of f16 or bf16")
+    qs = _rows(where, "q", q, shape, dtype, device)
     if out is None:
-        out = torch.empty((n, heads, hd), dtype=q.dtype, device=device)
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+        os = shape[1] * shape[2]
     else:
-        _rows(where, "out", out, heads, hd, device)
-        if out.dtype != q.dtype or out.shape[0] != n:
-            _refuse(where, "out must be like q")
-    if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()
-                                  or workspace.device != device):
+        os = _rows(where, "out", out, shape, dtype, device)
+    if workspace is not None and (workspace.dtype is not torch.uint8 or not workspace.is_contiguous()
+                                  or workspace.get_device() != device):
         _refuse(where, "workspace must be a contiguous uint8 tensor on the tensors' device")
-    _call(device, _attention, kv, q, dt, heads, hd ** -0.5 if scale is None else scale, out, workspace,
+    _call(device, _attention, kv, q, dt, shape[1], qs, shape[2] ** -0.5 if scale is None else scale, out, os, workspace,
           _status(where, status, device))
     return out
 
 
-def _attention(kv, q, dt, heads, scale, out, workspace, status, stream):
+def _attention(kv, q, dt, heads, qs, scale, out, os, workspace, status, stream):
     if workspace is None:
-        workspace = torch.empty(adp.adp_paged_attention_workspace(kv, heads), dtype=torch.uint8, device=q.device)
-    adp.adp_paged_attention(kv, q.data_ptr(), dt, heads, _row_stride(q), scale, out.data_ptr(), _row_stride(out),
-                            workspace.data_ptr(), workspace.numel(), status, stream)
+        need = adp.adp_paged_attention_workspace(kv, heads)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    else:
+        need = workspace.numel()
+    adp.adp_paged_attention(kv, q.data_ptr(), dt, heads, qs, scale, out.data_ptr(), os, workspace.data_ptr(), need, status,
+                            stream)
 
 
 def packed_attention(q, k, v, cu_q, cu_k, *, scale: float | None = None, out=None, status=None):
@@ -175,28 +186,26 @@ def packed_attention(q, k, v, cu_q, cu_k, *, scale: float | None = None, out=Non
     i + lk - lq.  scale: default 1 / sqrt(head_dim).  Rows of q from cu_q[-1] on are padding: their rows of `out`
     are left as they were (unset where out is allocated here)."""
     where = "packed_attention"
-    device = q.device
-    if device.type != "cuda" or q.dim() != 3 or k.dim() != 3:
+    device = q.get_device()
+    if not q.is_cuda or len(q.shape) != 3 or len(k.shape) != 3:
         _refuse(where, "q, k and v must be [rows, heads, head_dim] on a CUDA device")
-    n_q, heads, hd = q.shape
-    n_k, kv_heads, _ = k.shape
-    _rows(where, "q", q, None, hd, device)
-    _rows(where, "k", k, kv_heads, hd, device)
-    _rows(where, "v", v, kv_heads, hd, device)
-    dt = _HALF.get(q.dtype)
-    if dt is None or k.dtype != q.dtype or v.dtype != q.dtype or v.shape[0] != n_k:
-        _refuse(where, "q, k and v must be alike, of f16 or bf16, with as many rows of v as of k")
-    _indices(where, "cu_q", cu_q, 1, device)
-    _indices(where, "cu_k", cu_k, 1, device)
-    if cu_q.shape[0] < 1 or cu_k.shape != cu_q.shape:
-        _refuse(where, "cu_q and cu_k must both have one entry more than there are sequences")
+    shape, kv_shape, dtype = q.shape, k.shape, q.dtype
+    n_q, heads, hd = shape
+    n_k, kv_heads, kd = kv_shape
+    dt = _HALF.get(dtype)
+    if dt is None or kd != hd:
+        _refuse(where, "q, k and v must be of f16 or bf16, with one head_dim")
+    qs = _rows(where, "q", q, shape, dtype, device)
+    ks, vs = _rows(where, "k", k, kv_shape, dtype, device), _rows(where, "v", v, kv_shape, dtype, device)
+    n = cu_q.numel()
+    if n < 1:
+        _refuse(where, "cu_q must have one entry more than there are sequences")
+    cq, ck = _indices(where, "cu_q", cu_q, n, device), _indices(where, "cu_k", cu_k, n, device)
     if out is None:
-        out = torch.empty((n_q, heads, hd), dtype=q.dtype, device=device)
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+        os = heads * hd
     else:
-        _rows(where, "out", out, heads, hd, device)
-        if out.dtype != q.dtype or out.shape[0] != n_q:
-            _refuse(where, "out must be like q")
-    _call(device, adp.adp_packed_attention, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, heads, kv_heads, hd, _row_stride(q),
-          _row_stride(k), _row_stride(v), cu_q.data_ptr(), cu_k.data_ptr(), cu_q.shape[0] - 1, n_q, n_k,
-          hd ** -0.5 if scale is None else scale, out.data_ptr(), _row_stride(out), _status(where, status, device))
+        os = _rows(where, "out", out, shape, dtype, device)
+    _call(device, adp.adp_packed_attention, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, heads, kv_heads, hd, qs, ks, vs,
+          cq, ck, n - 1, n_q, n_k, hd ** -0.5 if scale is None else scale, out.data_ptr(), os, _status(where, status, device))
     return out
