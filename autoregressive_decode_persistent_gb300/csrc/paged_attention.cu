@@ -1,6 +1,7 @@
 // Attention of one new token per sequence over the pages of a KV cache.
 #include <cuda_runtime.h>
 #include <math.h>
+#include <stddef.h>
 
 #include <type_traits>
 
@@ -79,7 +80,28 @@ struct AttnArgs {
   void* partials;                // Partial [2 ctas]
   SplitMeta* meta;               // [ctas]
   int32_t* status;
+  int32_t cluster;               // CTAs per segment (a cluster), 0: the line of all units is cut evenly
 };
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Loads from the shared memory of CTA `rank` of the cluster, at this CTA's address p.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
+  uint32_t d;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(smem_u32(p)), "r"(rank));
+  return d;
+}
+__device__ __forceinline__ float cluster_ld(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
 
 // CTAs per SM: 12 warps of 168 registers, or 8 of 255 for the wider tile of heads.
 template <int NT>
@@ -91,6 +113,9 @@ constexpr int kResident = NT == 1 ? 3 : 2;
 // A warp runs its range segment by segment (segment: one sequence and tile of heads) with its own running maximum,
 // sum and output in registers.  Segments that several warps share are joined in shared memory, segments that
 // several CTAs share in paged_attention_join_kernel.
+// Where every segment is short and there are few (a.cluster), each gets a cluster of 1 to 8 CTAs instead, whose warps
+// share its units and join through distributed shared memory: no sums over the lengths, no workspace and no second
+// launch, which is what small calls wait for.
 //
 // Bound by reading K and V once.  Both go from global memory straight into the registers of the 16 x 8 x 16 tensor
 // instruction: S^T = K Q^T takes a K row's 16-byte pieces as the A operand (the order of the contraction index is
@@ -124,58 +149,74 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
     const int len = paged_length(c.lens[b], c.table_width, c.log2_page);
     return (len + UNIT - 1) / UNIT;
   };
-  // ---- the line's length: units of every 32 sequences, and zeros for the sequences without any
   const int n_chunks = (c.n_seqs + 31) / 32;
-  for (int ch = warp; ch < n_chunks; ch += kPagedWarps) {
-    const int b = ch * 32 + lane;
-    int n = 0;
-    bool empty = false;
-    if (b < c.n_seqs) {
-      const int32_t raw = c.lens[b], len = paged_length(raw, c.table_width, c.log2_page);
-      if (raw > len) report(a.status, ADP_ERR_CONTEXT_OVERFLOW);
-      if (raw < 0) report(a.status, ADP_ERR_INVALID_ARG);
-      n = (len + UNIT - 1) / UNIT;
-      empty = n == 0 && b % gridDim.x == blockIdx.x;
-    }
-    for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, empty); todo; todo &= todo - 1) {
-      uint8_t* o = a.out + (int64_t)(ch * 32 + __ffs(todo) - 1) * a.out_stride;
-      const int words = c.n_kv_heads * a.group * HD / 8;
-      for (int w = lane; w < words; w += 32) reinterpret_cast<uint4*>(o)[w] = make_uint4(0, 0, 0, 0);
-    }
-    n = __reduce_add_sync(0xFFFFFFFFu, n);
-    if (lane == 0) s_chunk[ch] = n;
-  }
+  int64_t u, u_end, c0 = 0, c1 = 0, total = 0;
+  int parts = 1, b = 0, vt = 0, t = 0, seg_units = 0;
   if (threadIdx.x < kPagedWarps * 2) s_seg[threadIdx.x] = -1;
-  __syncthreads();
-  if (warp == 0) {  // running sums over the chunks, in place: s_chunk[i] = units before chunk i
-    int64_t run = 0;
-    for (int ch = 0; ch <= n_chunks; ch += 32) {
-      int64_t n = ch + lane < n_chunks ? s_chunk[ch + lane] : 0, sum = n;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int64_t o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
-        if (lane >= d) sum += o;
+  if (a.cluster) {
+    const int seg = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
+    b = seg / nvt;
+    vt = seg % nvt;
+    const int32_t raw = c.lens[b], len = paged_length(raw, c.table_width, c.log2_page);
+    if (raw > len) report(a.status, ADP_ERR_CONTEXT_OVERFLOW);
+    if (raw < 0) report(a.status, ADP_ERR_INVALID_ARG);
+    seg_units = (len + UNIT - 1) / UNIT;
+    const int w = rank * kPagedWarps + warp;
+    u = split_begin(seg_units, a.cluster * kPagedWarps, w);
+    u_end = split_begin(seg_units, a.cluster * kPagedWarps, w + 1);
+    t = (int)u;
+  } else {
+    // ---- the line's length: units of every 32 sequences, and zeros for the sequences without any
+    for (int ch = warp; ch < n_chunks; ch += kPagedWarps) {
+      const int b = ch * 32 + lane;
+      int n = 0;
+      bool empty = false;
+      if (b < c.n_seqs) {
+        const int32_t raw = c.lens[b], len = paged_length(raw, c.table_width, c.log2_page);
+        if (raw > len) report(a.status, ADP_ERR_CONTEXT_OVERFLOW);
+        if (raw < 0) report(a.status, ADP_ERR_INVALID_ARG);
+        n = (len + UNIT - 1) / UNIT;
+        empty = n == 0 && b % gridDim.x == blockIdx.x;
       }
-      if (ch + lane <= n_chunks) s_chunk[ch + lane] = run + sum - n;
-      run += __shfl_sync(0xFFFFFFFFu, sum, 31);
+      for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, empty); todo; todo &= todo - 1) {
+        uint8_t* o = a.out + (int64_t)(ch * 32 + __ffs(todo) - 1) * a.out_stride;
+        const int words = c.n_kv_heads * a.group * HD / 8;
+        for (int w = lane; w < words; w += 32) reinterpret_cast<uint4*>(o)[w] = make_uint4(0, 0, 0, 0);
+      }
+      n = __reduce_add_sync(0xFFFFFFFFu, n);
+      if (lane == 0) s_chunk[ch] = n;
     }
+    __syncthreads();
+    if (warp == 0) {  // running sums over the chunks, in place: s_chunk[i] = units before chunk i
+      int64_t run = 0;
+      for (int ch = 0; ch <= n_chunks; ch += 32) {
+        int64_t n = ch + lane < n_chunks ? s_chunk[ch + lane] : 0, sum = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int64_t o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+          if (lane >= d) sum += o;
+        }
+        if (ch + lane <= n_chunks) s_chunk[ch + lane] = run + sum - n;
+        run += __shfl_sync(0xFFFFFFFFu, sum, 31);
+      }
+    }
+    __syncthreads();
+    total = s_chunk[n_chunks] * nvt;
+    parts = split_parts(total, gridDim.x);
+    if ((int)blockIdx.x >= parts || total == 0) {
+      if (threadIdx.x == 0) a.meta[blockIdx.x].seg = -1;
+      return;
+    }
+    c0 = split_begin(total, parts, blockIdx.x);
+    c1 = split_begin(total, parts, blockIdx.x + 1);
+    u = c0 + split_begin(c1 - c0, kPagedWarps, warp);
+    u_end = c0 + split_begin(c1 - c0, kPagedWarps, warp + 1);
   }
-  __syncthreads();
-  const int64_t total = s_chunk[n_chunks] * nvt;
-  const int parts = split_parts(total, gridDim.x);
-  if ((int)blockIdx.x >= parts || total == 0) {
-    if (threadIdx.x == 0) a.meta[blockIdx.x].seg = -1;
-    return;
-  }
-  const int64_t c0 = split_begin(total, parts, blockIdx.x), c1 = split_begin(total, parts, blockIdx.x + 1);
-  int64_t u = c0 + split_begin(c1 - c0, kPagedWarps, warp);
-  const int64_t u_end = c0 + split_begin(c1 - c0, kPagedWarps, warp + 1);
   const int64_t u_first = u;
+  const int b0 = b, vt0 = vt;  // a cluster's segment
 
   if (u < u_end) {
-    // ---- the sequence, head tile and unit of u
-    int b, vt, t;
-    {
+    if (!a.cluster) {  // ---- the sequence, head tile and unit of u
       const int64_t seq_u = u / nvt;
       int ch = 0;
       for (int at = 0; at < n_chunks; at += 32) {
@@ -278,14 +319,20 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
       };
       // Where the next unit's groups of 16 positions lie (pages of 16 positions and more: a group lies in one page),
       // and whether all its positions are attended.
-      int pg[RG];
+      int pg[RG], ahead[RG];
       bool next_full = false;
       auto fetch_pages = [&](int ut) {
+        if constexpr (!SMALL) {
+#pragma unroll
+          for (int g = 0; g < RG; ++g) ahead[g] = page_at(ut * UNIT + g * 16);
+        }
+      };
+      auto take_pages = [&](int ut) {
         next_full = !SMALL && (ut + 1) * UNIT <= len;
         if constexpr (!SMALL) {
 #pragma unroll
           for (int g = 0; g < RG; ++g) {
-            pg[g] = page_at(ut * UNIT + g * 16);
+            pg[g] = ahead[g];
             next_full &= pg[g] >= 0;
           }
         }
@@ -379,11 +426,16 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
       };
 
       fetch_pages(t);
+      take_pages(t);
+      if (n > 1) fetch_pages(t + 1);
       load_k(t);
       load_v(t, next_full);
       for (int i = 0; i < n; ++i) {
         const bool more = i + 1 < n, full = next_full;
-        if (more) fetch_pages(t + i + 1);
+        if (more) {
+          take_pages(t + i + 1);
+          if (i + 2 < n) fetch_pages(t + i + 2);
+        }
         // ---- S^T = K Q^T: rows are keys, columns heads
         float s[RG][NT][4];
 #pragma unroll
@@ -571,7 +623,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
       }
       u += n;
       t = 0;
-      if (u < u_end && ++vt == nvt) {
+      if (u < u_end && ++vt == nvt) {  // (never in a cluster: its warps' units are of one segment)
         vt = 0;
         do {
           ++b;
@@ -579,6 +631,40 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
         if (b >= c.n_seqs) break;
       }
     }
+  }
+  if (a.cluster) {
+    // ---- join the cluster's pieces; every CTA takes a part of the output
+    const int parts_w = a.cluster * kPagedWarps, rank = blockIdx.x % a.cluster;
+    cluster_barrier();
+    if (seg_units != 1) {  // (a single unit was written by its warp)
+      const int kvh = vt0 / a.tiles, head0 = (vt0 % a.tiles) * (NT * 8);
+      const int heads = min(NT * 8, a.group - head0);
+      for (int x = rank * kPagedWarps * 32 + threadIdx.x; x < heads * (HD / 4); x += parts_w * 32) {
+        const int h = x / (HD / 4), d = (x % (HD / 4)) * 4;
+        float m = -INFINITY, sum = 0.0f;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int k = 0; k < parts_w; ++k) {
+          if (split_begin(seg_units, parts_w, k) == split_begin(seg_units, parts_w, k + 1)) continue;
+          const Part* p = slots + (k % kPagedWarps) * 2;
+          const uint32_t at = cluster_addr(p, k / kPagedWarps);
+          const float pm = cluster_ld(at + (uint32_t)offsetof(Part, m) + 4 * h);
+          const float pl = cluster_ld(at + (uint32_t)offsetof(Part, l) + 4 * h);
+          const float4 po = cluster_ld4(at + (uint32_t)(h * HD + d) * 4);
+          const float mn = fmaxf(m, pm);
+          const float f = exp2_fast(m - safe_max(mn)), g = exp2_fast(pm - safe_max(mn));
+          m = mn;
+          sum = fmaf(sum, f, g * pl);
+          acc.x = fmaf(acc.x, f, g * po.x), acc.y = fmaf(acc.y, f, g * po.y);
+          acc.z = fmaf(acc.z, f, g * po.z), acc.w = fmaf(acc.w, f, g * po.w);
+        }
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        uint8_t* po = a.out + (int64_t)b0 * a.out_stride + ((int64_t)(kvh * a.group + head0 + h) * HD + d) * 2;
+        *reinterpret_cast<uint2*>(po) = make_uint2(pack2(acc.x * inv, acc.y * inv, QDT), pack2(acc.z * inv, acc.w * inv, QDT));
+      }
+    }
+    cluster_barrier();  // no CTA leaves while another reads its shared memory
+    return;
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();
@@ -694,17 +780,37 @@ __global__ void __launch_bounds__(128) paged_attention_join_kernel(AttnArgs a) {
 // Query heads per KV head take tiles of 8 (a group of up to 8) or 16 columns of the tensor instruction.
 int head_tiles(int group) { return group <= 8 ? 1 : 2; }
 
-// CTAs of an attention call: as many as can be resident, or fewer where even full tables would not fill them.
-int attention_ctas(const adp_paged_kv* kv, int group, int sms) {
-  const int nt = head_tiles(group), tiles = (group + nt * 8 - 1) / (nt * 8);
+// How an attention call falls on the GPU: a cluster of CTAs per segment, or CTAs that share all units evenly.
+struct AttentionPlan {
+  int nt, tiles, cluster, ctas;
+  size_t bytes;  // workspace
+};
+
+// A cluster per segment while all of them can be resident and no warp gets more than kClusterUnits units even if every
+// sequence fills its table: then the uneven lengths cost less than the even split's sums, partial results and second
+// launch.  (Clusters take up to 8 CTAs, the portable size, and no more warps than there are units.)
+constexpr int kClusterUnits = 8;
+
+AttentionPlan attention_plan(const adp_paged_kv* kv, int group, int sms) {
+  AttentionPlan p{};
+  p.nt = head_tiles(group);
+  p.tiles = (group + p.nt * 8 - 1) / (p.nt * 8);
+  const int resident = sms * (p.nt == 1 ? kResident<1> : kResident<2>);
   const int unit = 4096 / (kv->head_dim * elem_bytes(kv->dtype));
   const int64_t per_seq = ((int64_t)kv->table_width * kv->page_size + unit - 1) / unit;
-  return split_parts(per_seq * kv->n_kv_heads * tiles * (kv->n_seqs > 0 ? kv->n_seqs : 1),
-                     sms * (nt == 1 ? kResident<1> : kResident<2>));
-}
-
-size_t attention_bytes(int ctas, int nt, int hd) {
-  return (size_t)ctas * 2 * (nt * 8) * (hd + 2) * sizeof(float) + (size_t)ctas * sizeof(SplitMeta);
+  const int64_t segs = (int64_t)kv->n_seqs * kv->n_kv_heads * p.tiles;
+  if (segs > 0 && segs <= resident) {
+    int cs = 1;
+    while (cs < 8 && segs * cs * 2 <= resident && cs * kPagedWarps < per_seq) cs *= 2;
+    if (per_seq <= (int64_t)cs * kPagedWarps * kClusterUnits) {
+      p.cluster = cs;
+      p.ctas = (int)segs * cs;
+      return p;
+    }
+  }
+  p.ctas = split_parts(per_seq * (segs > 0 ? segs : 1), resident);
+  p.bytes = (size_t)p.ctas * 2 * (p.nt * 8) * (kv->head_dim + 2) * sizeof(float) + (size_t)p.ctas * sizeof(SplitMeta);
+  return p;
 }
 
 template <int HD, int CDT, int QDT, int NT, bool SMALL>
@@ -716,8 +822,22 @@ cudaError_t attention_launch(const AttnArgs& a, int ctas, cudaStream_t st) {
   auto* kernel = paged_attention_kernel<HD, CDT, QDT, NT, SMALL>;
   cudaError_t e = allow_smem<AttentionKey<HD, CDT, QDT, NT, SMALL>>((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
+  if (a.cluster > 1) {
+    cudaLaunchAttribute together{};
+    together.id = cudaLaunchAttributeClusterDimension;
+    together.val.clusterDim.x = a.cluster;
+    together.val.clusterDim.y = together.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kPagedWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &together;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+  }
   kernel<<<ctas, kPagedWarps * 32, smem, st>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess || ctas == 1) return e;  // one CTA shares no segment
+  if ((e = cudaGetLastError()) != cudaSuccess || a.cluster || ctas == 1) return e;  // one CTA shares no segment
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
@@ -749,7 +869,7 @@ extern "C" int adp_paged_attention_workspace(const adp_paged_kv* kv, int32_t n_h
   int sms = 0;
   if (rc || (rc = sm_count(&sms))) return rc;
   const int group = n_heads / kv->n_kv_heads;
-  *bytes = attention_bytes(attention_ctas(kv, group, sms), head_tiles(group), kv->head_dim);
+  *bytes = attention_plan(kv, group, sms).bytes;
   return ADP_OK;
 }
 
@@ -768,20 +888,22 @@ extern "C" int adp_paged_attention(const adp_paged_kv* kv, const void* q, int32_
     return ADP_ERR_INVALID_ARG;
   int sms = 0;
   if ((rc = sm_count(&sms))) return rc;
-  const int group = n_heads / kv->n_kv_heads, nt = head_tiles(group);
-  const int ctas = attention_ctas(kv, group, sms);
-  if (!workspace || !aligned16(workspace) || workspace_bytes < attention_bytes(ctas, nt, kv->head_dim))
-    return ADP_ERR_INVALID_ARG;
+  const int group = n_heads / kv->n_kv_heads;
+  const AttentionPlan plan = attention_plan(kv, group, sms);
+  const int nt = plan.nt, ctas = plan.ctas;
+  if (plan.bytes && (!workspace || !aligned16(workspace) || workspace_bytes < plan.bytes)) return ADP_ERR_INVALID_ARG;
   a.q = static_cast<const uint8_t*>(q);
   a.out = static_cast<uint8_t*>(out);
   a.q_stride = q_stride * 2;
   a.out_stride = out_stride * 2;
   a.group = group;
-  a.tiles = (group + nt * 8 - 1) / (nt * 8);
+  a.tiles = plan.tiles;
+  a.cluster = plan.cluster;
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.partials = workspace;
-  a.meta = reinterpret_cast<SplitMeta*>(static_cast<uint8_t*>(workspace) +
-                                        (size_t)ctas * 2 * (nt * 8) * (kv->head_dim + 2) * sizeof(float));
+  if (plan.bytes) {
+    a.partials = workspace;
+    a.meta = reinterpret_cast<SplitMeta*>(static_cast<uint8_t*>(workspace) + plan.bytes - (size_t)ctas * sizeof(SplitMeta));
+  }
   a.status = dev_status;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const bool small = kv->page_size < 16;

@@ -51,13 +51,13 @@ def _status(where: str, t: torch.Tensor | None, device: int):
     return t.data_ptr()
 
 
-def _call(device: int, fn, *args):
-    """fn(*args, stream) with the tensors' device current."""
+def _call(device: int, name: str, *args):
+    """The C ABI's function `name` on the current stream, with the tensors' device current."""
     if device == torch._C._cuda_getDevice():
-        fn(*args, torch._C._cuda_getCurrentRawStream(device))
+        adp._check(getattr(adp.load_library(), name)(*args, torch._C._cuda_getCurrentRawStream(device)), name)
     else:
         with torch.cuda.device(device):
-            fn(*args, torch._C._cuda_getCurrentRawStream(device))
+            adp._check(getattr(adp.load_library(), name)(*args, torch._C._cuda_getCurrentRawStream(device)), name)
 
 
 def _paged(where: str, k_pages, v_pages, table, lens, k_scale, v_scale, device: int) -> adp.PagedKV:
@@ -106,7 +106,7 @@ def paged_kv_write(k_pages, v_pages, table, lens, cu_rows, k, v, *, k_scale=None
     k_pages, v_pages: [pages, kv_heads, page_size, head_dim] f16, bf16 or float8_e4m3fn (then with fp32
     k_scale, v_scale [pages, kv_heads, page_size]), changed in place.  table: int32 [seqs, width] page numbers;
     lens: int32 [seqs], the rows being written included; cu_rows: int32 [seqs + 1]."""
-    _transfer("paged_kv_write", adp.adp_paged_kv_write, k_pages, v_pages, table, lens, cu_rows, k, v, k_scale, v_scale, status)
+    _transfer("paged_kv_write", k_pages, v_pages, table, lens, cu_rows, k, v, k_scale, v_scale, status)
 
 
 def paged_kv_read(k_pages, v_pages, table, lens, cu_rows, n_rows: int, *, dtype=None, k_scale=None, v_scale=None,
@@ -125,11 +125,11 @@ def paged_kv_read(k_pages, v_pages, table, lens, cu_rows, n_rows: int, *, dtype=
         k, v = out
         if k.shape[0] != n_rows or (dtype is not None and k.dtype is not dtype):
             _refuse("paged_kv_read", "out must hold n_rows rows of dtype")
-    _transfer("paged_kv_read", adp.adp_paged_kv_read, k_pages, v_pages, table, lens, cu_rows, k, v, k_scale, v_scale, status)
+    _transfer("paged_kv_read", k_pages, v_pages, table, lens, cu_rows, k, v, k_scale, v_scale, status)
     return out
 
 
-def _transfer(where, call, k_pages, v_pages, table, lens, cu_rows, k, v, k_scale, v_scale, status):
+def _transfer(where, k_pages, v_pages, table, lens, cu_rows, k, v, k_scale, v_scale, status):
     device = k_pages.get_device()
     kv = _paged(where, k_pages, v_pages, table, lens, k_scale, v_scale, device)
     cu = _indices(where, "cu_rows", cu_rows, kv.n_seqs + 1, device)
@@ -139,7 +139,7 @@ def _transfer(where, call, k_pages, v_pages, table, lens, cu_rows, k, v, k_scale
         _refuse(where, "k and v rows must be of f16, bf16 or f32")
     shape = (n, kv.n_kv_heads, kv.head_dim)
     ks, vs = _rows(where, "k", k, shape, dtype, device), _rows(where, "v", v, shape, dtype, device)
-    _call(device, call, kv, k.data_ptr(), v.data_ptr(), dt, ks, vs, cu, n, _status(where, status, device))
+    _call(device, "adp_" + where, kv, k.data_ptr(), v.data_ptr(), dt, ks, vs, cu, n, _status(where, status, device))
 
 
 def paged_attention(q, k_pages, v_pages, table, lens, *, scale: float | None = None, k_scale=None, v_scale=None,
@@ -157,26 +157,25 @@ def paged_attention(q, k_pages, v_pages, table, lens, *, scale: float | None = N
         _refuse(where, "q must be [seqs, heads, head_dim] of f16 or bf16")
     qs = _rows(where, "q", q, shape, dtype, device)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
         os = shape[1] * shape[2]
     else:
         os = _rows(where, "out", out, shape, dtype, device)
-    if workspace is not None and (workspace.dtype is not torch.uint8 or not workspace.is_contiguous()
-                                  or workspace.get_device() != device):
-        _refuse(where, "workspace must be a contiguous uint8 tensor on the tensors' device")
-    _call(device, _attention, kv, q, dt, shape[1], qs, shape[2] ** -0.5 if scale is None else scale, out, os, workspace,
-          _status(where, status, device))
-    return out
-
-
-def _attention(kv, q, dt, heads, qs, scale, out, os, workspace, status, stream):
-    if workspace is None:
-        need = adp.adp_paged_attention_workspace(kv, heads)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    else:
+    if workspace is not None:
         need = workspace.numel()
-    adp.adp_paged_attention(kv, q.data_ptr(), dt, heads, qs, scale, out.data_ptr(), os, workspace.data_ptr(), need, status,
-                            stream)
+        if workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != device:
+            _refuse(where, "workspace must be a contiguous uint8 tensor on the tensors' device")
+    else:
+        if device == torch._C._cuda_getDevice():
+            need = adp.adp_paged_attention_workspace(kv, shape[1])
+        else:
+            with torch.cuda.device(device):
+                need = adp.adp_paged_attention_workspace(kv, shape[1])
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _call(device, "adp_paged_attention", kv, q.data_ptr(), dt, shape[1], qs, shape[2] ** -0.5 if scale is None else scale,
+          out.data_ptr(), os, workspace.data_ptr() if need else None, need, _status(where, status, device))
+    return out
 
 
 def packed_attention(q, k, v, cu_q, cu_k, *, scale: float | None = None, out=None, status=None):
@@ -202,10 +201,10 @@ def packed_attention(q, k, v, cu_q, cu_k, *, scale: float | None = None, out=Non
         _refuse(where, "cu_q must have one entry more than there are sequences")
     cq, ck = _indices(where, "cu_q", cu_q, n, device), _indices(where, "cu_k", cu_k, n, device)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
         os = heads * hd
     else:
         os = _rows(where, "out", out, shape, dtype, device)
-    _call(device, adp.adp_packed_attention, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, heads, kv_heads, hd, qs, ks, vs,
+    _call(device, "adp_packed_attention", q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, heads, kv_heads, hd, qs, ks, vs,
           cq, ck, n - 1, n_q, n_k, hd ** -0.5 if scale is None else scale, out.data_ptr(), os, _status(where, status, device))
     return out

@@ -403,8 +403,8 @@ int adp_paged_kv_read(const adp_paged_kv* kv, void* k, void* v, int32_t rows_dty
  *              16-byte aligned
  *  n_heads     a multiple of n_kv_heads, at most 4096; n_seqs at most 8192
  *  scale       finite
- *  workspace   DEVICE scratch of at least adp_paged_attention_workspace bytes, 16-byte aligned; its contents
- *              do not matter.  Calls that may run at the same time need one each.
+ *  workspace   DEVICE scratch of at least adp_paged_attention_workspace bytes, 16-byte aligned (may be NULL
+ *              where that is 0); its contents do not matter.  Calls that may run at the same time need one each.
  * Scores, softmax and sums are fp32; probabilities are rounded to the cache's 16-bit type (e4m3: fp16)
  * before they weigh V.  A sequence of length 0 gives zeros.  A position whose page number is outside the
  * pool is left out and reported as ADP_ERR_INVALID_ARG; a length behind the table is cut and reported as
@@ -413,8 +413,8 @@ int adp_paged_kv_read(const adp_paged_kv* kv, void* k, void* v, int32_t rows_dty
 int adp_paged_attention(const adp_paged_kv* kv, const void* q, int32_t q_dtype, int32_t n_heads, int64_t q_stride,
                         float scale, void* out, int64_t out_stride, void* workspace, uint64_t workspace_bytes,
                         int32_t* dev_status, void* cuda_stream);
-/* Bytes of scratch adp_paged_attention needs for this cache (a few MB at most; asks the current device for
- * its SM count). */
+/* Bytes of scratch adp_paged_attention needs for this cache's shape (0 for few short sequences, a few MB at most;
+ * asks the current device for its SM count). */
 int adp_paged_attention_workspace(const adp_paged_kv* kv, int32_t n_heads, uint64_t* bytes);
 
 /* Causal attention of packed prompts: query i of sequence s (row cu_q[s] + i) sees keys j <= i + (lk - lq) of

@@ -135,10 +135,15 @@ def test_long_and_ragged_contexts_are_split_and_joined(ops, dtype, q_dtype):
         out = paged(ops, q, c)
         check_attention(out, q, c)
         assert torch.equal(out, paged(ops, q, c))  # the same bits again
+        wide = torch.full((len(lens), 20000), -1, dtype=torch.int32, device="cuda")  # (the even split at any length)
+        wide[:, :c.table.shape[1]] = c.table
+        out = ops.paged_attention(q, c.k, c.v, wide, c.len_t, **c.scales)
+        check_attention(out, q, c)
+        assert torch.equal(out, ops.paged_attention(q, c.k, c.v, wide, c.len_t, **c.scales))
 
 
 def test_more_sequences_than_one_scan_of_a_warp_holds(ops):
-    lens = [(i * 7) % 5 for i in range(1100)]
+    lens = [(i * 7) % 5 for i in range(1100)]  # (more segments than can be resident: the even split)
     c, q = run(lens, (2, 1), 64, 4, F16, seed=1)
     check_attention(paged(ops, q, c), q, c)
 
@@ -385,3 +390,32 @@ def test_written_then_attended(ops):
             assert torch.equal(kr, k.float()) and torch.equal(vr, v.float())
         q = torch.randn(3, 8, hd, generator=g).to(F16).cuda()
         check_attention(paged(ops, q, c), q, c)
+
+
+@pytest.mark.parametrize("dtype,q_dtype", TYPES)
+@pytest.mark.parametrize("hd", [64, 128])
+def test_segments_of_a_cluster_and_of_the_even_split_agree(ops, dtype, q_dtype, hd):
+    """The same sequences with a table just wide enough (a cluster for each) and with a very wide one (the even split)."""
+    lens = [1, 16, 17, 31, 0, 33, 64, 65, 200, 500]
+    c, q = run(lens, (8, 2), hd, 16, dtype, q_dtype, seed=21)
+    check_attention(paged(ops, q, c), q, c)
+    wide = torch.full((len(lens), 20000), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c.table.shape[1]] = c.table
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    check_attention(ops.paged_attention(q, c.k, c.v, wide, c.len_t, status=status, **c.scales), q, c)
+    assert int(status) == 0
+
+
+def test_the_workspace_that_is_asked_for(ops):
+    from autoregressive_decode_persistent_gb300 import adp
+    c, q = run([6000, 10], (8, 2), 128, 16, F16, seed=22)
+    kv = ops._paged("test", c.k, c.v, c.table, c.len_t, None, None, 0)
+    need = adp.adp_paged_attention_workspace(kv, 8)
+    assert need > 0
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")  # its contents do not matter
+    check_attention(paged(ops, q, c, workspace=ws), q, c)
+    with pytest.raises(adp.AdpError):
+        paged(ops, q, c, workspace=ws[:need - 1])
+    c, q = run([300, 10], (8, 2), 128, 16, F16, seed=22)
+    kv = ops._paged("test", c.k, c.v, c.table, c.len_t, None, None, 0)
+    assert adp.adp_paged_attention_workspace(kv, 8) == 0
