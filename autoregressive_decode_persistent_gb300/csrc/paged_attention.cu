@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
   int64_t u, u_end, c0 = 0, c1 = 0, total = 0;
   int parts = 1, b = 0, vt = 0, t = 0, seg_units = 0;
   if (threadIdx.x < kPagedWarps * 2) s_seg[threadIdx.x] = -1;
+  __syncthreads();
   if (a.cluster) {
     const int seg = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
     b = seg / nvt;
@@ -162,9 +163,9 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
     if (raw < 0) report(a.status, ADP_ERR_INVALID_ARG);
     seg_units = (len + UNIT - 1) / UNIT;
     const int w = rank * kPagedWarps + warp;
-    u = split_begin(seg_units, a.cluster * kPagedWarps, w);
-    u_end = split_begin(seg_units, a.cluster * kPagedWarps, w + 1);
-    t = (int)u;
+    t = (int)((uint32_t)seg_units * w / (uint32_t)(a.cluster * kPagedWarps));  // (few units: no overflow)
+    u = t;
+    u_end = (uint32_t)seg_units * (w + 1) / (uint32_t)(a.cluster * kPagedWarps);
   } else {
     // ---- the line's length: units of every 32 sequences, and zeros for the sequences without any
     for (int ch = warp; ch < n_chunks; ch += kPagedWarps) {
@@ -633,35 +634,61 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
     }
   }
   if (a.cluster) {
-    // ---- join the cluster's pieces; every CTA takes a part of the output
-    const int parts_w = a.cluster * kPagedWarps, rank = blockIdx.x % a.cluster;
-    cluster_barrier();
+    // ---- join each CTA's pieces, then the cluster's; every CTA takes a part of the output
+    __syncthreads();
     if (seg_units != 1) {  // (a single unit was written by its warp)
       const int kvh = vt0 / a.tiles, head0 = (vt0 % a.tiles) * (NT * 8);
-      const int heads = min(NT * 8, a.group - head0);
-      for (int x = rank * kPagedWarps * 32 + threadIdx.x; x < heads * (HD / 4); x += parts_w * 32) {
+      const int heads = min(NT * 8, a.group - head0), rank = blockIdx.x % a.cluster;
+      for (int x = threadIdx.x; x < heads * (HD / 4); x += kPagedWarps * 32) {
         const int h = x / (HD / 4), d = (x % (HD / 4)) * 4;
         float m = -INFINITY, sum = 0.0f;
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int k = 0; k < parts_w; ++k) {
-          if (split_begin(seg_units, parts_w, k) == split_begin(seg_units, parts_w, k + 1)) continue;
-          const Part* p = slots + (k % kPagedWarps) * 2;
-          const uint32_t at = cluster_addr(p, k / kPagedWarps);
-          const float pm = cluster_ld(at + (uint32_t)offsetof(Part, m) + 4 * h);
-          const float pl = cluster_ld(at + (uint32_t)offsetof(Part, l) + 4 * h);
-          const float4 po = cluster_ld4(at + (uint32_t)(h * HD + d) * 4);
-          const float mn = fmaxf(m, pm);
-          const float f = exp2_fast(m - safe_max(mn)), g = exp2_fast(pm - safe_max(mn));
-          m = mn;
-          sum = fmaf(sum, f, g * pl);
-          acc.x = fmaf(acc.x, f, g * po.x), acc.y = fmaf(acc.y, f, g * po.y);
-          acc.z = fmaf(acc.z, f, g * po.z), acc.w = fmaf(acc.w, f, g * po.w);
+#pragma unroll
+        for (int w = 0; w < kPagedWarps; ++w)
+          if (s_seg[w * 2] >= 0) m = fmaxf(m, slots[w * 2].m[h]);
+#pragma unroll
+        for (int w = 0; w < kPagedWarps; ++w) {
+          if (s_seg[w * 2] < 0) continue;
+          const float4 p = *reinterpret_cast<const float4*>(&slots[w * 2].o[h][d]);
+          const float f = exp2_fast(slots[w * 2].m[h] - safe_max(m));
+          sum = fmaf(f, slots[w * 2].l[h], sum);
+          acc.x = fmaf(f, p.x, acc.x), acc.y = fmaf(f, p.y, acc.y), acc.z = fmaf(f, p.z, acc.z), acc.w = fmaf(f, p.w, acc.w);
+        }
+        // (into slots that no warp of a cluster uses)
+        *reinterpret_cast<float4*>(&slots[1].o[h][d]) = acc;
+        if (d == 0) slots[1].m[h] = m, slots[1].l[h] = sum;
+      }
+      cluster_barrier();
+      for (int x = rank * kPagedWarps * 32 + threadIdx.x; x < heads * (HD / 4); x += a.cluster * kPagedWarps * 32) {
+        const int h = x / (HD / 4), d = (x % (HD / 4)) * 4;
+        float pm[8], pl[8];
+        float4 po[8];
+        float m = -INFINITY, sum = 0.0f;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          pm[k] = -INFINITY;
+          if (k >= a.cluster) continue;
+          const uint32_t at = cluster_addr(&slots[1], k);
+          pm[k] = cluster_ld(at + (uint32_t)offsetof(Part, m) + 4 * h);
+          pl[k] = cluster_ld(at + (uint32_t)offsetof(Part, l) + 4 * h);
+          po[k] = cluster_ld4(at + (uint32_t)(h * HD + d) * 4);
+          m = fmaxf(m, pm[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (k >= a.cluster) continue;
+          const float f = exp2_fast(pm[k] - safe_max(m));
+          sum = fmaf(f, pl[k], sum);
+          acc.x = fmaf(f, po[k].x, acc.x), acc.y = fmaf(f, po[k].y, acc.y);
+          acc.z = fmaf(f, po[k].z, acc.z), acc.w = fmaf(f, po[k].w, acc.w);
         }
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        uint8_t* po = a.out + (int64_t)b0 * a.out_stride + ((int64_t)(kvh * a.group + head0 + h) * HD + d) * 2;
-        *reinterpret_cast<uint2*>(po) = make_uint2(pack2(acc.x * inv, acc.y * inv, QDT), pack2(acc.z * inv, acc.w * inv, QDT));
+        uint8_t* dst = a.out + (int64_t)b0 * a.out_stride + ((int64_t)(kvh * a.group + head0 + h) * HD + d) * 2;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(acc.x * inv, acc.y * inv, QDT), pack2(acc.z * inv, acc.w * inv, QDT));
       }
+    } else {
+      cluster_barrier();
     }
     cluster_barrier();  // no CTA leaves while another reads its shared memory
     return;

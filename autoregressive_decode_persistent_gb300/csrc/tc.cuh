@@ -161,22 +161,28 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) 
 // ---- 128-byte-swizzled operands, as the tensor copies below write them: rows of 128 bytes (64 16-bit elements), eight
 // rows to an atom of 1,024 bytes, the 16-byte piece p of row r of an atom at piece p ^ (r % 8).
 
-// Descriptor of such an operand.  K-major (rows are M or N, the row holds K): sbo 1024 between 8-row groups, lbo unused;
-// 16 elements of K further is 32 bytes.  MN-major (rows are K, the row holds 64 of M or N): sbo 1024 between 8-row
-// groups of K, lbo between the 64-wide blocks of M or N; 16 rows of K further is 2,048 bytes.
-__device__ __forceinline__ uint64_t tc_smem_desc_sw128(uint32_t smem_addr, uint32_t lbo, uint32_t sbo) {
-  return tc_smem_desc(smem_addr, lbo, sbo) | (2ull << 61);
-}
+// Their descriptors say swizzle mode 2 in bits 61-63.  K-major (rows are M or N, the row holds K): sbo 1024 between 8-row
+// groups, lbo unused; 16 elements of K further is 32 bytes.  MN-major (rows are K, the row holds 64 of M or N): sbo 1024
+// between 8-row groups of K, lbo between the 64-wide blocks of M or N; 16 rows of K further is 2,048 bytes.
 // The instruction descriptor's bit for an MN-major B operand.
 constexpr uint32_t kTcIdescBMn = 1u << 16;
 
-// D[tmem] (+)= A[tmem] * B[smem], issued by one thread.  A: lane = row, two 16-bit elements of K per 32-bit column.
-__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+// D[tmem] (+)= A[smem] * B[smem]^T with the descriptors' low words and their common high word.
+__device__ __forceinline__ void tc_mma_f16_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
                                               bool accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %5, 0;\n mov.b64 da, {%1, %3};\n mov.b64 db, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem], issued by one thread.  A: lane = row, two 16-bit elements of K per 32-bit column.
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                              bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %5, 0;\n mov.b64 db, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
 

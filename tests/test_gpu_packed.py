@@ -90,6 +90,20 @@ def test_long_prompts_and_many_short_ones(ops, dtype):
         assert torch.equal(out, ops.packed_attention(q, k, v, cumulative(lq), cumulative(lk)))
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_more_work_than_the_gpu_holds_at_once(ops, dtype, hd):
+    """Several pieces of work in a row on every SM, in both orders (up to 32 sequences and more), with sequences and
+    tiles that see nothing among them."""
+    rng = random.Random(4)
+    for lq, lk in (([1000, 0, 33, 700, 500], [1000, 40, 600, 300, 500]),
+                   ([rng.randint(0, 90) for _ in range(75)], [rng.randint(0, 200) for _ in range(75)])):
+        q, k, v = inputs(lq, lk, (64, 4), hd, dtype, seed=10)
+        out = ops.packed_attention(q, k, v, cumulative(lq), cumulative(lk))
+        check(out, q, k, v, lq, lk)
+        assert torch.equal(out, ops.packed_attention(q, k, v, cumulative(lq), cumulative(lk)))
+
+
 def test_scales_negative_zero_and_large_and_growing_scores(ops):
     lq = lk = [300]
     q, k, v = inputs(lq, lk, (4, 2), 64, BF16, seed=1)
