@@ -496,7 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], x[kKeys - 4 + e]);
         const float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
         const float mb = mx == -INFINITY ? -INFINITY : mx * a.scale_log2;
-        const bool grow = mb > m + kRescale || (m == -INFINITY && mb > -INFINITY);
+        // (only for rows of the sequence: what stands in the others must not decide how these are rounded)
+        const bool grow = live && (mb > m + kRescale || (m == -INFINITY && mb > -INFINITY));
         if (__any_sync(0xFFFFFFFFu, grow)) {
           const float mn = fmaxf(m, mb);
           const float f = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
