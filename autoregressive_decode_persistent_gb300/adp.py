@@ -159,6 +159,8 @@ _SIGS = [
                                            ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p]),
     ("adp_paged_attention_workspace", ctypes.c_int, [ctypes.POINTER(PagedKV), ctypes.c_int32,
                                                      ctypes.POINTER(ctypes.c_uint64)]),
+    ("adp_paged_forward", ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(PagedKV), ctypes.c_void_p, ctypes.c_void_p,
+                                         ctypes.c_void_p, ctypes.c_void_p]),
     ("adp_packed_attention", ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
                                             ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64,
                                             ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
@@ -476,6 +478,13 @@ def adp_paged_attention(kv: PagedKV, q, q_dtype: int, n_heads: int, q_stride: in
     _check(load_library().adp_paged_attention(kv, _ptr(q), q_dtype, n_heads, q_stride, scale, _ptr(out), out_stride,
                                               _ptr(workspace), workspace_bytes, _ptr(dev_status), stream),
            "adp_paged_attention")
+
+
+def adp_paged_forward(model, layers, tokens, cu_rows, lens, dev_logits):
+    """layers: a ctypes array of PagedKV, one per layer; tokens, cu_rows, lens: HOST sequences."""
+    t, c, n = (np.ascontiguousarray(x, dtype=np.int32) for x in (tokens, cu_rows, lens))
+    _check(load_library().adp_paged_forward(model, layers, _ptr(t), _ptr(c), _ptr(n), _ptr(dev_logits)),
+           "adp_paged_forward")
 
 
 def adp_packed_attention(q, k, v, dtype: int, n_heads: int, n_kv_heads: int, head_dim: int, q_stride: int, k_stride: int,

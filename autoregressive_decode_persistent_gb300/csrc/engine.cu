@@ -105,6 +105,15 @@ struct adp_model {
     uint8_t* Vt = nullptr;
     float* C = nullptr;     // fp32 QKV output (the timing hook's plain-store QKV GEMM only)
   } tc;
+  // Packed rows over a paged cache (adp_paged_forward): the LM head as GEMM operand tiles, and scratch that grows.
+  struct PagedFwd {
+    uint8_t* lm = nullptr;
+    int32_t *ints = nullptr, *status = nullptr;
+    float* xs = nullptr;
+    uint16_t *q = nullptr, *o = nullptr, *k = nullptr, *v = nullptr;
+    uint8_t* work = nullptr;
+    size_t n_ints = 0, n_xs = 0, n_q = 0, n_k = 0, n_work = 0;  // capacities
+  } pf;
   // Batched decode (set up at the first batched call): per-request buffers for kMaxBatch
   // requests, the per-request step state and KV cache tables, and the shared-memory layout of
   // each batch size.
@@ -1364,6 +1373,160 @@ extern "C" int adp_prefill_tc(adp_model* m, adp_kv* kv, const int32_t* host_toke
   }
   // the last token: one decode step (synchronises and reports any device error, the GEMMs' too)
   return adp_decode_step(m, kv, host_tokens[n - 1], sampling, next_token, dev_logits);
+}
+
+// A scratch buffer of at least n elements (the old one is freed behind the work that uses it).
+template <class T>
+static int reserve(adp_model* m, T** buf, size_t* cap, size_t n) {
+  if (n <= *cap) return ADP_OK;
+  if (*buf) {
+    CK(cudaStreamSynchronize(m->stream));
+    m->allocs.erase(std::remove(m->allocs.begin(), m->allocs.end(), (void*)*buf), m->allocs.end());
+    cudaFree(*buf);
+    *buf = nullptr;
+    *cap = 0;
+  }
+  const int rc = m->alloc(buf, n);
+  if (rc == ADP_OK) *cap = n;
+  return rc;
+}
+
+extern "C" int adp_paged_forward(adp_model* m, const adp_paged_kv* layers, const int32_t* host_tokens,
+                                 const int32_t* host_cu_rows, const int32_t* host_lens, float* dev_logits) {
+  if (!m || !layers || !host_cu_rows || !host_lens || !dev_logits) return ADP_ERR_INVALID_ARG;
+  if (m->sticky) return m->sticky;
+  const adp_config& c = m->cfg;
+  const int nb = layers[0].n_seqs;
+  if (nb < 1 || nb > 8192 || host_cu_rows[0] != 0) return ADP_ERR_INVALID_ARG;
+  for (int l = 0; l < c.n_layers; ++l) {
+    const adp_paged_kv& kv = layers[l];
+    if (kv.n_seqs != nb || kv.n_kv_heads != c.n_kv_heads || kv.head_dim != c.head_dim) return ADP_ERR_INVALID_ARG;
+    if (kv.dtype != c.kv_dtype && kv.dtype != ADP_E4M3) return ADP_ERR_UNSUPPORTED_CONFIG;
+  }
+  bool single = true;
+  int64_t keys = 0;
+  for (int s = 0; s < nb; ++s) {
+    const int64_t rows = (int64_t)host_cu_rows[s + 1] - host_cu_rows[s];
+    if (rows < 0 || host_lens[s] < rows) return ADP_ERR_INVALID_ARG;
+    if (host_lens[s] > c.max_ctx) return ADP_ERR_CONTEXT_OVERFLOW;
+    for (int l = 0; l < c.n_layers; ++l)
+      if ((int64_t)layers[l].table_width * layers[l].page_size < host_lens[s]) return ADP_ERR_CONTEXT_OVERFLOW;
+    single = single && rows == 1;
+    keys += host_lens[s];
+  }
+  const int P = host_cu_rows[nb];
+  if (P < 1 || !host_tokens || keys > 0x7FFFFFFF) return ADP_ERR_INVALID_ARG;
+  for (int i = 0; i < P; ++i)
+    if (host_tokens[i] < 0 || host_tokens[i] >= c.vocab) return ADP_ERR_INVALID_ARG;
+  if (tc_operand_bf16(c) != (c.kv_dtype == ADP_BF16 ? 1 : 0)) return ADP_ERR_UNSUPPORTED_CONFIG;
+  int rc = tc_init(m);
+  if (rc || (rc = tc_reserve(m, std::max(P, nb)))) return rc;
+  adp_model::PagedFwd& F = m->pf;
+  if (!F.lm) {
+    uint8_t* lm = nullptr;
+    for (const PhaseDesc& ph : m->phases) {
+      if (ph.kind != PK_LM) continue;
+      const size_t bytes = tc_tiled_bytes(c.vocab, ph.K, 256);
+      if ((rc = m->alloc(&lm, bytes))) return rc;
+      CK(cudaMemsetAsync(lm, 0, bytes, m->stream));
+      CK(tc_unpack(m->image, ph, m->G, c.head_dim, c.n_heads, c.n_kv_heads, c.d_ff, lm, tc_operand_bf16(c), m->stream));
+    }
+    if (!lm) return ADP_ERR_UNSUPPORTED_CONFIG;
+    F.lm = lm;
+  }
+  // tokens, positions, row and key offsets, lengths and last rows, in one copy
+  std::vector<int32_t> ints((size_t)2 * P + 4 * nb + 2);
+  int32_t *pos = ints.data() + P, *cu = pos + P, *lens = cu + nb + 1, *ck = lens + nb, *last = ck + nb + 1;
+  std::copy(host_tokens, host_tokens + P, ints.data());
+  ck[0] = 0;
+  for (int s = 0; s < nb; ++s) {
+    for (int i = host_cu_rows[s]; i < host_cu_rows[s + 1]; ++i) pos[i] = host_lens[s] - (host_cu_rows[s + 1] - i);
+    cu[s] = host_cu_rows[s];
+    lens[s] = host_lens[s];
+    ck[s + 1] = ck[s] + host_lens[s];
+    last[s] = host_cu_rows[s + 1] > host_cu_rows[s] ? host_cu_rows[s + 1] - 1 : -1;
+  }
+  cu[nb] = P;
+  uint64_t work = 0;
+  for (int l = 0; single && l < c.n_layers; ++l) {
+    uint64_t need = 0;
+    adp_paged_kv kv = layers[l];
+    kv.lens = kv.table;  // (only its shape counts here)
+    if ((rc = adp_paged_attention_workspace(&kv, c.n_heads, &need))) return rc;
+    work = std::max(work, need);
+  }
+  size_t one = F.status ? 1 : 0, o_cap = F.n_q, v_cap = F.n_k;
+  const size_t qn = (size_t)P * c.n_heads * c.head_dim, kn = single ? 0 : (size_t)keys * c.n_kv_heads * c.head_dim;
+  if ((rc = reserve(m, &F.status, &one, 1)) || (rc = reserve(m, &F.ints, &F.n_ints, ints.size())) ||
+      (rc = reserve(m, &F.xs, &F.n_xs, (size_t)nb * c.d_model)) || (rc = reserve(m, &F.o, &o_cap, qn)) ||
+      (rc = reserve(m, &F.q, &F.n_q, qn)) || (rc = reserve(m, &F.v, &v_cap, kn)) || (rc = reserve(m, &F.k, &F.n_k, kn)) ||
+      (rc = reserve(m, &F.work, &F.n_work, (size_t)work)))
+    return rc;
+  CK(cudaMemcpyAsync(F.ints, ints.data(), ints.size() * 4, cudaMemcpyHostToDevice, m->stream));
+  CK(cudaMemsetAsync(F.status, 0, 4, m->stream));
+  const int32_t* d = F.ints;
+  TcPaged a{};
+  a.P = P;
+  a.nb = nb;
+  a.n_layers = c.n_layers;
+  a.d = c.d_model;
+  a.hq = c.n_heads;
+  a.hkv = c.n_kv_heads;
+  a.hd = c.head_dim;
+  a.ff = c.d_ff;
+  a.vocab = c.vocab;
+  a.bf16 = tc_operand_bf16(c);
+  a.kvdt = c.kv_dtype;
+  a.single = single;
+  a.total_keys = (int)keys;
+  a.eps = c.rms_eps;
+  a.scale = m->p.attn_scale;
+  a.tokens = d;
+  a.pos = d + (pos - ints.data());
+  a.cu_rows = d + (cu - ints.data());
+  a.lens = d + (lens - ints.data());
+  a.cu_keys = d + (ck - ints.data());
+  a.last = d + (last - ints.data());
+  a.tok_emb = m->p.tok_emb;
+  a.attn_norm = m->h_attn_norm.data();
+  a.ffn_norm = m->h_ffn_norm.data();
+  a.final_norm = m->p.final_norm;
+  a.wqkv = m->tc.wqkv.data();
+  a.wo = m->tc.wo.data();
+  a.wgu = m->tc.wgu.data();
+  a.wdown = m->tc.wdown.data();
+  const bool scaled = !m->tc.sqkv.empty();
+  a.sqkv = scaled ? m->tc.sqkv.data() : nullptr;
+  a.swo = scaled ? m->tc.swo.data() : nullptr;
+  a.sgu = scaled ? m->tc.sgu.data() : nullptr;
+  a.sdown = scaled ? m->tc.sdown.data() : nullptr;
+  a.lm = F.lm;
+  a.rope_cos = m->p.rope_cos;
+  a.rope_sin = m->p.rope_sin;
+  a.layers = layers;
+  a.x = m->tc.x;
+  a.C = m->tc.C;
+  a.xs = F.xs;
+  a.A = m->tc.A;
+  a.A2 = m->tc.A2;
+  a.q = F.q;
+  a.o = F.o;
+  a.kbuf = F.k;
+  a.vbuf = F.v;
+  a.work = F.work;
+  a.work_bytes = F.n_work;
+  a.logits = dev_logits;
+  a.status = F.status;
+  a.err = m->p.err;
+  a.wait_ns = std::max<uint64_t>(m->p.wait_ns, 1000000000ull);
+  if ((rc = tc_paged(a, m->stream))) {
+    cudaStreamSynchronize(m->stream);
+    return rc == ADP_ERR_CUDA ? cuda_fail(cudaGetLastError(), "adp_paged_forward") : rc;
+  }
+  int32_t status = 0;
+  CK(cudaMemcpyAsync(&status, F.status, 4, cudaMemcpyDeviceToHost, m->stream));
+  if ((rc = finish(m))) return rc;
+  return status;
 }
 
 extern "C" int adp_sync(adp_model* m) {

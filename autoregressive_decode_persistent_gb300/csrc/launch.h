@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/adp.h"
 #include "plan.h"
 
 namespace adp {
@@ -98,6 +99,35 @@ struct TcPrefill {
   uint64_t wait_ns;
 };
 cudaError_t tc_prefill(const TcPrefill& a, cudaStream_t st);
+// One pass of P packed rows of several sequences through every layer over a paged cache (the operators of
+// paged_rows.cu, paged_attention.cu and packed_attention.cu between the prefill's GEMMs), and the logits of every
+// sequence's last row.
+struct TcPaged {
+  int P, nb, n_layers, d, hq, hkv, hd, ff, vocab, bf16, kvdt;
+  int single;                    // every sequence has one new row: attention of single tokens
+  int total_keys;                // sum of the lengths
+  float eps, scale;
+  const int32_t *tokens, *pos, *cu_rows, *lens, *cu_keys, *last;  // device: [P], [P], [nb+1], [nb], [nb+1], [nb] (-1: none)
+  const void* tok_emb;
+  const void* const* attn_norm;
+  const void* const* ffn_norm;
+  const void* final_norm;
+  const uint8_t *const *wqkv, *const *wo, *const *wgu, *const *wdown;
+  const float *const *sqkv, *const *swo, *const *sgu, *const *sdown;  // column scales, or null
+  const uint8_t* lm;             // device tiled LM head
+  const float *rope_cos, *rope_sin;
+  const adp_paged_kv* layers;    // host array [n_layers]
+  float *x, *C, *xs;             // device [P, d], [P, (hq + 2 hkv) hd], [nb, d]
+  uint8_t *A, *A2;
+  uint16_t *q, *o, *kbuf, *vbuf;  // device [P, hq hd] x2, [total_keys, hkv hd] x2 (not for single rows)
+  void* work;
+  uint64_t work_bytes;
+  float* logits;                 // device [nb, vocab]
+  int32_t* status;               // device: the operators' reports
+  int32_t* err;
+  uint64_t wait_ns;
+};
+int tc_paged(const TcPaged& a, cudaStream_t st);  // an ADP_* code
 // Phase P's tiles of the decode image -> one GEMM weight operand in 256-row tiles (dst cleared
 // beforehand; rows in the order of the caller's matrices, except gate|up: gate_i and up_i
 // interleaved as rows 2i and 2i + 1).

@@ -901,4 +901,88 @@ cudaError_t tc_flash(const TcPrefill& a, int qkv_n, int L, int kt_att, cudaStrea
   return a.hd == 128 ? tc_flash_launch<128, DT_F16>(a, kt_att, st) : tc_flash_launch<64, DT_F16>(a, kt_att, st);
 }
 
+// ---------------------------------------------------------------- packed rows over a paged cache
+
+// RoPE of the QKV GEMM's q and k columns at every row's position: q rounded for the attention, k in place (fp32; the
+// cache write rounds or quantises it).  One thread per row and rotated pair.
+__global__ void tc_paged_rope_kernel(float* C, int P, int hq, int hkv, int hd, const int32_t* __restrict__ pos,
+                                     const float* __restrict__ rope_cos, const float* __restrict__ rope_sin, int kvdt,
+                                     uint16_t* q) {
+  const int half = hd / 2, pairs = (hq + hkv) * half;
+  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= (long long)P * pairs) return;
+  const int row = (int)(i / pairs), h = (int)(i % pairs) / half, e = (int)(i % half);
+  float* x = C + (size_t)row * (hq + 2 * hkv) * hd + (size_t)h * hd + e;
+  const float c = rope_cos[(size_t)pos[row] * half + e], s = rope_sin[(size_t)pos[row] * half + e];
+  const float u = x[0], v = x[half];
+  const float ru = fmaf(u, c, -__fmul_rn(v, s)), rv = fmaf(v, c, __fmul_rn(u, s));
+  if (h < hq) {
+    uint16_t* o = q + (size_t)row * hq * hd + (size_t)h * hd + e;
+    o[0] = round_kv(ru, kvdt);
+    o[half] = round_kv(rv, kvdt);
+  } else {
+    x[0] = ru;
+    x[half] = rv;
+  }
+}
+
+// xs[s] = x[last[s]], zeros where the sequence has no new row.
+__global__ void tc_last_rows_kernel(const float* __restrict__ x, const int32_t* __restrict__ last, int d, float* xs) {
+  const int r = last[blockIdx.x];
+  for (int e = threadIdx.x; e < d; e += blockDim.x) xs[(size_t)blockIdx.x * d + e] = r < 0 ? 0.0f : x[(size_t)r * d + e];
+}
+
+int tc_paged(const TcPaged& a, cudaStream_t st) {
+  const int P = a.P, qkv_n = (a.hq + 2 * a.hkv) * a.hd;
+  const int kt_d = (a.d + kTcBK - 1) / kTcBK, kt_ff = (a.ff + kTcBK - 1) / kTcBK;
+#define TC_OK(call)                                \
+  do {                                             \
+    if ((call) != cudaSuccess) return ADP_ERR_CUDA; \
+  } while (0)
+  tc_embed_kernel<<<P, 256, 0, st>>>(a.tokens, (const uint16_t*)a.tok_emb, a.d, a.bf16, a.x);
+  TC_OK(cudaGetLastError());
+  for (int L = 0; L < a.n_layers; ++L) {
+    adp_paged_kv kv = a.layers[L];
+    kv.lens = a.lens;
+    tc_rmsnorm_kernel<<<(P + 7) / 8, 256, 0, st>>>(a.x, (const uint16_t*)a.attn_norm[L], P, a.d, a.eps, a.bf16, a.A, kt_d);
+    TC_OK(cudaGetLastError());
+    TC_OK(tc_gemm(a.bf16, TC_STORE, a.A, a.wqkv[L], a.C, qkv_n, P, qkv_n, a.d, a.err, a.wait_ns, st, nullptr,
+                  a.sqkv ? a.sqkv[L] : nullptr));
+    const long long n = (long long)P * (a.hq + a.hkv) * (a.hd / 2);
+    tc_paged_rope_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a.C, P, a.hq, a.hkv, a.hd, a.pos, a.rope_cos,
+                                                                      a.rope_sin, a.kvdt, a.q);
+    TC_OK(cudaGetLastError());
+    int rc = adp_paged_kv_write(&kv, a.C + (size_t)a.hq * a.hd, a.C + (size_t)(a.hq + a.hkv) * a.hd, ADP_F32, qkv_n, qkv_n,
+                                a.cu_rows, P, a.status, st);
+    if (rc) return rc;
+    const int64_t qw = (int64_t)a.hq * a.hd, kw = (int64_t)a.hkv * a.hd;
+    if (a.single) {
+      rc = adp_paged_attention(&kv, a.q, a.kvdt, a.hq, qw, a.scale, a.o, qw, a.work, a.work_bytes, a.status, st);
+    } else {
+      // the whole contexts in 16 bits (a cached prefix, and the rows just written), then all prompts at once
+      rc = adp_paged_kv_read(&kv, a.kbuf, a.vbuf, a.kvdt, kw, kw, a.cu_keys, a.total_keys, a.status, st);
+      if (!rc)
+        rc = adp_packed_attention(a.q, a.kbuf, a.vbuf, a.kvdt, a.hq, a.hkv, a.hd, qw, kw, kw, a.cu_rows, a.cu_keys, a.nb, P,
+                                  a.total_keys, a.scale, a.o, qw, a.status, st);
+    }
+    if (rc) return rc;
+    TC_OK(tc_tile(a.o, P, a.hq * a.hd, a.hq * a.hd, a.A, kTcBM, st));
+    TC_OK(tc_gemm(a.bf16, TC_ADD, a.A, a.wo[L], a.x, a.d, P, a.d, a.hq * a.hd, a.err, a.wait_ns, st, nullptr,
+                  a.swo ? a.swo[L] : nullptr));
+    tc_rmsnorm_kernel<<<(P + 7) / 8, 256, 0, st>>>(a.x, (const uint16_t*)a.ffn_norm[L], P, a.d, a.eps, a.bf16, a.A, kt_d);
+    TC_OK(cudaGetLastError());
+    TC_OK(tc_gemm(a.bf16, TC_SWIGLU, a.A, a.wgu[L], reinterpret_cast<float*>(a.A2), kt_ff, P, 2 * a.ff, a.d, a.err,
+                  a.wait_ns, st, nullptr, a.sgu ? a.sgu[L] : nullptr));
+    TC_OK(tc_gemm(a.bf16, TC_ADD, a.A2, a.wdown[L], a.x, a.d, P, a.d, a.ff, a.err, a.wait_ns, st, nullptr,
+                  a.sdown ? a.sdown[L] : nullptr));
+  }
+  tc_last_rows_kernel<<<a.nb, 256, 0, st>>>(a.x, a.last, a.d, a.xs);
+  TC_OK(cudaGetLastError());
+  tc_rmsnorm_kernel<<<(a.nb + 7) / 8, 256, 0, st>>>(a.xs, (const uint16_t*)a.final_norm, a.nb, a.d, a.eps, a.bf16, a.A, kt_d);
+  TC_OK(cudaGetLastError());
+  TC_OK(tc_gemm(a.bf16, TC_STORE, a.A, a.lm, a.logits, a.vocab, a.nb, a.vocab, a.d, a.err, a.wait_ns, st));
+#undef TC_OK
+  return ADP_OK;
+}
+
 }  // namespace adp

@@ -124,6 +124,51 @@ class DecodeModel:
         adp.adp_generate_batch_async(self.handle, [k.handle for k in kvs], tokens, n, temperatures, uniforms, out)
 
 
+class PagedCache:
+    """Pages of every layer of a model, shared by many requests (the caller owns the page numbers).
+
+    dtype: the model's KV type (default) or torch.float8_e4m3fn."""
+
+    def __init__(self, model: DecodeModel, n_pages: int, page_size: int = 16, dtype: torch.dtype | None = None):
+        c = model.cfg
+        self.model = model
+        own = torch.bfloat16 if c["kv_dtype"] == "bf16" else torch.float16
+        self.dtype = dtype or own
+        shape = (c["n_layers"], n_pages, c["n_kv_heads"], page_size, c["head_dim"])
+        self.k = torch.zeros(shape, dtype=self.dtype, device=model.device)
+        self.v = torch.zeros(shape, dtype=self.dtype, device=model.device)
+        self.k_scale = self.v_scale = None
+        if self.dtype == torch.float8_e4m3fn:
+            self.k_scale = torch.zeros(shape[:4], dtype=torch.float32, device=model.device)
+            self.v_scale = torch.zeros(shape[:4], dtype=torch.float32, device=model.device)
+
+    def forward(self, table, tokens, lens, logits: torch.Tensor | None = None) -> torch.Tensor:
+        """One pass over the new tokens of several requests: table [requests][pages] page numbers, tokens a list of
+        new tokens per request, lens their lengths with these.  Returns the logits [requests, vocab] of each
+        request's last new token."""
+        c = self.model.cfg
+        n_layers, n_pages, hkv, ps, hd = self.k.shape
+        table = torch.as_tensor(table, dtype=torch.int32).to(self.model.device).contiguous()
+        cu = np.cumsum([0] + [len(t) for t in tokens])
+        if logits is None:
+            logits = torch.empty((len(tokens), c["vocab"]), dtype=torch.float32, device=self.model.device)
+        if table.dim() != 2 or table.shape[0] != len(tokens) or len(lens) != len(tokens) or not logits.is_contiguous() \
+                or logits.dtype != torch.float32 or tuple(logits.shape) != (len(tokens), c["vocab"]):
+            raise adp.AdpError(adp.ADP_ERR_INVALID_ARG, "PagedCache.forward: table, tokens, lens and logits disagree")
+        dt = adp.ADP_E4M3 if self.k_scale is not None else adp.DTYPES[c["kv_dtype"]]
+        layers = (adp.PagedKV * n_layers)()
+        for i in range(n_layers):
+            ks = self.k_scale[i].data_ptr() if self.k_scale is not None else None
+            vs = self.v_scale[i].data_ptr() if self.v_scale is not None else None
+            layers[i] = adp.PagedKV(self.k[i].data_ptr(), self.v[i].data_ptr(), ks, vs, table.data_ptr(), table.data_ptr(),
+                                    hkv * ps * hd, hkv * ps, n_pages, ps, hkv, hd, dt, len(tokens), table.shape[1])
+        # the table and the pools were made on torch's stream, the pass runs on the model's
+        torch.cuda.current_stream(self.model.device).synchronize()
+        flat = [int(t) for ts in tokens for t in ts]
+        adp.adp_paged_forward(self.model.handle, layers, flat, cu, lens, logits)
+        return logits
+
+
 class KVCache:
     def __init__(self, model: DecodeModel):
         self.model = model

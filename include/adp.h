@@ -405,8 +405,8 @@ int adp_paged_kv_read(const adp_paged_kv* kv, void* k, void* v, int32_t rows_dty
  *  scale       finite
  *  workspace   DEVICE scratch of at least adp_paged_attention_workspace bytes, 16-byte aligned (may be NULL
  *              where that is 0); its contents do not matter.  Calls that may run at the same time need one each.
- * Scores, softmax and sums are fp32; probabilities are rounded to the cache's 16-bit type (e4m3: fp16)
- * before they weigh V.  A sequence of length 0 gives zeros.  A position whose page number is outside the
+ * Scores, softmax and sums are fp32; probabilities are rounded to fp16 (f16 and e4m3 caches) or to two bf16
+ * terms before they weigh V.  A sequence of length 0 gives zeros.  A position whose page number is outside the
  * pool is left out and reported as ADP_ERR_INVALID_ARG; a length behind the table is cut and reported as
  * ADP_ERR_CONTEXT_OVERFLOW; one below 0 counts as 0 and is reported as ADP_ERR_INVALID_ARG.  Equal inputs
  * give equal bits on one GPU. */
@@ -435,6 +435,24 @@ int adp_packed_attention(const void* q, const void* k, const void* v, int32_t dt
                          int32_t n_kv_heads, int32_t head_dim, int64_t q_stride, int64_t k_stride, int64_t v_stride,
                          const int32_t* cu_q, const int32_t* cu_k, int32_t n_seqs, int32_t n_q, int32_t n_k,
                          float scale, void* out, int64_t out_stride, int32_t* dev_status, void* cuda_stream);
+
+/* One pass of a dense model over packed new rows of several requests whose caches are paged: prompts (also behind a
+ * cached prefix), single tokens, or both together; the four operators above between the GEMMs of adp_prefill_tc.
+ * There is no limit of four requests as in adp_decode_batch, and the caches may be quantised.
+ *  layers        HOST array [n_layers]: one layer each, all with the same n_seqs; n_kv_heads and head_dim of the
+ *                model, dtype its kv_dtype or ADP_E4M3 (lens is not read: host_lens says them)
+ *  host_tokens   HOST [rows]: the new tokens, sequence by sequence
+ *  host_cu_rows  HOST [n_seqs + 1]: sequence s has rows host_cu_rows[s] .. host_cu_rows[s + 1] - 1 (possibly none), its
+ *                last positions
+ *  host_lens     HOST [n_seqs]: its length with the new rows, at most max_ctx
+ *  dev_logits    DEVICE float [n_seqs][vocab]: the logits of each sequence's last new row (zeros where it has none)
+ * Writes the new rows' K and V into their pages.  Like adp_prefill_tc it agrees with the oracle within the
+ * tolerances, not bit for bit (e4m3 pages add the cache's rounding).  head_dim 64 or 128 and a 16-bit operand
+ * type equal to kv_dtype, else ADP_ERR_UNSUPPORTED_CONFIG.  Runs on the model's stream and synchronises it; scratch grows with
+ * the most rows and keys seen.  Errors: as adp_prefill_tc, and what the operators report (ADP_ERR_INVALID_ARG: a
+ * page number outside the pool). */
+int adp_paged_forward(adp_model* m, const adp_paged_kv* layers, const int32_t* host_tokens,
+                      const int32_t* host_cu_rows, const int32_t* host_lens, float* dev_logits);
 
 /* Debug and ablation hooks ([H] §"標準推論スタックのボトルネックとKogの工夫": the launch
  * overhead the persistent kernel removes is measured by running the same device code as one

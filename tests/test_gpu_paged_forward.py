@@ -1,0 +1,138 @@
+"""adp_paged_forward: packed prompts, single tokens and both together over paged caches, against the oracle."""
+import numpy as np
+import pytest
+import torch
+
+import synth
+from gpu_common import ARGMAX_MARGIN, LOGIT_MAX_ABS, LOGIT_REL_L2, oracle_forced
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    assert torch.cuda.is_available(), "a CUDA GPU is required"
+    from autoregressive_decode_persistent_gb300 import adp, build
+    build.build()
+    return adp
+
+
+def _shapes():
+    tiny = synth.get_config("tiny")
+    big = synth.shrink(synth.get_config("dense-8b-bf16"))
+    e4m3 = synth.shrink(synth.get_config("dense-2.3b-e4m3"), head_dim=128)
+    return {"tiny-f16": tiny, "8b-bf16": big, "2.3b-e4m3-weights-hd128": e4m3}
+
+
+def _assert_close(cfg, got, ref):
+    """Logits against the oracle's plain mode: the stated tolerances for fp16 operands.  The path rounds six operands a
+    layer (both normalised inputs, q, the probabilities, the attention's output, h) and the last normalised input to
+    16 bits, each by at most u = finfo.eps / 2 of its value, independently of one another; a product with a random
+    matrix carries a rounding's share of the norm on as it carries the values.  So the logits' relative L2 error is at
+    most sqrt(6 L + 1) u: with 2 layers 1.8e-3 for fp16, within the stated 5e-3, and 1.4e-2 for bf16, where the three
+    stated bounds are scaled alike."""
+    u = 2.0 ** -8 if cfg["kv_dtype"] == "bf16" else 2.0 ** -11
+    f = max(1.0, np.sqrt(6 * cfg["n_layers"] + 1) * u / LOGIT_REL_L2)
+    for g, r in zip(got.astype(np.float64), ref.astype(np.float64)):
+        assert np.max(np.abs(g - r)) <= LOGIT_MAX_ABS * f, np.max(np.abs(g - r))
+        assert np.linalg.norm(g - r) <= LOGIT_REL_L2 * f * np.linalg.norm(r), np.linalg.norm(g - r) / np.linalg.norm(r)
+        top = np.sort(r)[-2:]
+        if top[1] - top[0] > ARGMAX_MARGIN * f:
+            assert np.argmax(g) == np.argmax(r)
+
+
+def _tables(lens, page):
+    """A page table for the requests' longest lengths, with pages in mixed order and some spare ones."""
+    need = [-(-n // page) for n in lens]
+    order = np.random.default_rng(5).permutation(sum(need) + 4).tolist()
+    table = -np.ones((len(lens), max(need)), dtype=np.int32)
+    for b, n in enumerate(need):
+        table[b, :n] = [order.pop() for _ in range(n)]
+    return table, sum(need) + 4
+
+
+@pytest.mark.parametrize("name", list(_shapes()))
+def test_prompts_then_steps_then_both_match_the_oracle(lib, name):
+    """Five requests (more than the batched step takes): their prompts in one pass, two steps of single tokens, a pass in
+    which one request continues with several tokens, one with a single one and one pauses; every logit row within the
+    tolerances of the oracle's plain mode on that request alone."""
+    from autoregressive_decode_persistent_gb300.model import DecodeModel, PagedCache
+    cfg = _shapes()[name]
+    W = synth.model_weights(cfg)
+    rng = np.random.default_rng(3)
+    lens = [3, 17, 1, 40, 33]
+    more = [[4, 1, 1], [1, 1, 5], [1, 1, 9], [1, 1, 0], [1, 1, 1]]
+    more[0][0] = 1
+    total = [n + sum(m) for n, m in zip(lens, more)]
+    seqs = [rng.integers(0, cfg["vocab"], n).tolist() for n in total]
+    refs = [oracle_forced(cfg, W, s)[0] for s in seqs]
+    model = DecodeModel(cfg, W)
+    table, n_pages = _tables(total, 16)
+    cache = PagedCache(model, n_pages, 16)
+    at = [0] * 5
+    passes = [lens] + [[m[i] for m in more] for i in range(3)]
+    for new in passes:
+        tokens = [s[a:a + n] for s, a, n in zip(seqs, at, new)]
+        at = [a + n for a, n in zip(at, new)]
+        logits = cache.forward(table, tokens, at).cpu().numpy()
+        for b in range(5):
+            if new[b]:
+                _assert_close(cfg, logits[b:b + 1], refs[b][at[b] - 1:at[b]])
+            else:
+                assert (logits[b] == 0).all()
+    model.close()
+
+
+def test_a_quantised_cache_holds_the_first_layers_rows(lib):
+    """Layer 0's keys and values do not depend on the cache: those of an e4m3 cache are the 16-bit cache's, off by half
+    a step of a code (2^-4 of the value, at least half the row's least step 2^-9 of its scale) and fp16's rounding."""
+    from autoregressive_decode_persistent_gb300.model import DecodeModel, PagedCache
+    from autoregressive_decode_persistent_gb300 import ops
+    cfg = synth.get_config("tiny")
+    W = synth.model_weights(cfg)
+    model = DecodeModel(cfg, W)
+    lens = [30, 7]
+    tokens = [np.random.default_rng(b).integers(0, cfg["vocab"], n).tolist() for b, n in enumerate(lens)]
+    table, n_pages = _tables(lens, 8)
+    t = torch.from_numpy(table).cuda()
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 30, 37], dtype=torch.int32, device="cuda")
+    rows = []
+    for dtype in (None, torch.float8_e4m3fn):
+        cache = PagedCache(model, n_pages, 8, dtype)
+        logits = cache.forward(table, tokens, lens)
+        assert torch.isfinite(logits).all()
+        scales = {} if dtype is None else dict(k_scale=cache.k_scale[0], v_scale=cache.v_scale[0])
+        rows.append(ops.paged_kv_read(cache.k[0], cache.v[0], t, n, cu, 37, dtype=torch.float32, **scales))
+    for exact, got in zip(*rows):
+        top = exact.abs().amax(-1, keepdim=True)
+        tol = exact.abs() * (2.0 ** -4 + 2.0 ** -10) + top / 448 * 2.0 ** -10 * 1.01 + top * 2.0 ** -11
+        assert ((got - exact).abs() <= tol).all()
+        assert (exact != 0).any()
+    model.close()
+
+
+def test_what_it_refuses(lib):
+    from autoregressive_decode_persistent_gb300.model import DecodeModel, PagedCache
+    cfg = synth.get_config("tiny")
+    model = DecodeModel(cfg, synth.model_weights(cfg))
+    cache = PagedCache(model, 40, 16)
+
+    def code(table, tokens, lens, c=cache):
+        with pytest.raises(lib.AdpError) as e:
+            c.forward(np.array(table, dtype=np.int32), tokens, lens)
+        return e.value.code
+
+    assert code([[0]], [[cfg["vocab"]]], [1]) == lib.ADP_ERR_INVALID_ARG
+    assert code([[0]], [[-1]], [1]) == lib.ADP_ERR_INVALID_ARG
+    assert code([[0]], [[1, 2]], [1]) == lib.ADP_ERR_INVALID_ARG       # fewer positions than rows
+    assert code([[0]], [[]], [1]) == lib.ADP_ERR_INVALID_ARG           # nothing to do
+    assert code([[0]], [[1]], [17]) == lib.ADP_ERR_CONTEXT_OVERFLOW    # behind the table
+    assert code([[0] * 30], [[1]], [cfg["max_ctx"] + 1]) == lib.ADP_ERR_CONTEXT_OVERFLOW
+    assert code([[40]], [[1]], [1]) == lib.ADP_ERR_INVALID_ARG         # no such page
+    cache.forward(np.array([[39]], dtype=np.int32), [[1]], [1])        # and the model still works
+    moe = synth.shrink(synth.get_config("moe-32x1408-top4-e4m3"))
+    m2 = DecodeModel(moe, synth.model_weights(moe))
+    assert code([[0]], [[1]], [1], PagedCache(m2, 4, 16)) == lib.ADP_ERR_UNSUPPORTED_CONFIG
+    m2.close()
+    model.close()
