@@ -29,16 +29,36 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int n, int i, in
   return lo + __popc(__ballot_sync(0xFFFFFFFFu, lane < n && cu[1 + lo + min(lane, max(n - 1, 0))] <= i));
 }
 
-// 8 consecutive elements in fp32 (exact).
+// 8 consecutive elements as they lie in memory.
 template <int DT>
-__device__ __forceinline__ void load_row8(const uint8_t* p, float (&x)[8]) {
-  if constexpr (DT == DT_F32) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 16);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
-    load8<DT>(p, x);
+struct Raw8 {
+  uint32_t w[2 * elem_bytes(DT)];
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    if constexpr (DT == DT_E4M3) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    } else {
+#pragma unroll
+      for (int q = 0; q < elem_bytes(DT) / 2; ++q) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p + 16 * q);
+        w[4 * q] = v.x, w[4 * q + 1] = v.y, w[4 * q + 2] = v.z, w[4 * q + 3] = v.w;
+      }
+    }
   }
-}
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int q = 0; q < 2 * elem_bytes(DT); ++q) w[q] = 0;
+  }
+  // In fp32 (exact).
+  __device__ __forceinline__ void expand(float (&x)[8]) const {
+    if constexpr (DT == DT_F32) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(w[e]);
+    } else {
+      load8<DT>(reinterpret_cast<const uint8_t*>(w), x);
+    }
+  }
+};
 
 template <int DT>
 __device__ __forceinline__ void store_row8(uint8_t* p, const float (&x)[8]) {
@@ -88,44 +108,50 @@ __global__ void __launch_bounds__(256)
   if (WRITE && page < 0) return;
   const int slot = (int)(pos & ((1 << c.log2_page) - 1));
   const int heads = 2 * c.n_kv_heads;
+  // this lane's piece of head 0 in the page and in the packed row, and the way from head to head (32 bits hold it)
+  const int piece = (lane % LPR) * 8, head_step = (HD * elem_bytes(CDT)) << c.log2_page;
+  const int64_t cell0 = (int64_t)page * c.page_bytes + ((int64_t)slot * HD + piece) * elem_bytes(CDT);
+  uint8_t *const ck = c.k + cell0, *const cv = c.v + cell0;
+  uint8_t *const rk = rows_k + (int64_t)i * k_stride + piece * elem_bytes(ROWDT);
+  uint8_t *const rv = rows_v + (int64_t)i * v_stride + piece * elem_bytes(ROWDT);
+  const int64_t scale0 = CDT == DT_E4M3 ? (int64_t)page * c.scale_stride + slot : 0;
   constexpr int kAhead = 4;  // pieces per lane in flight
+  constexpr int FROM = WRITE ? ROWDT : CDT;
   for (int h0 = 0; h0 < heads; h0 += kAhead * (32 / LPR)) {
-    float x[kAhead][8];
-    uint8_t* cell[kAhead];
-    uint8_t* row[kAhead];
-    float* scale[kAhead];
-    bool on[kAhead];
+    Raw8<FROM> raw[kAhead];
+    float sc[kAhead];  // reading e4m3
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       const int hh = h0 + a * (32 / LPR) + lane / LPR;
-      on[a] = hh < heads;
       const bool is_v = hh >= c.n_kv_heads;
       const int h = is_v ? hh - c.n_kv_heads : hh;
-      const int64_t at = ((int64_t)h << c.log2_page) + slot;
-      cell[a] = (is_v ? c.v : c.k) + (int64_t)page * c.page_bytes + (at * HD + (lane % LPR) * 8) * elem_bytes(CDT);
-      row[a] = (is_v ? rows_v + (int64_t)i * v_stride : rows_k + (int64_t)i * k_stride) +
-               (int64_t)(h * HD + (lane % LPR) * 8) * elem_bytes(ROWDT);
-      scale[a] = CDT == DT_E4M3 ? (is_v ? c.v_scale : c.k_scale) + (int64_t)page * c.scale_stride + at : nullptr;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[a][e] = 0.0f;
-      if (on[a]) {
-        if (WRITE) {
-          load_row8<ROWDT>(row[a], x[a]);
-        } else if (page >= 0) {
-          load_row8<CDT>(cell[a], x[a]);
-        }
+      if (hh < heads && page >= 0) {
+        raw[a].load(WRITE ? (is_v ? rv : rk) + h * (HD * elem_bytes(ROWDT)) : (is_v ? cv : ck) + h * head_step);
+        if constexpr (CDT == DT_E4M3 && !WRITE) sc[a] = (is_v ? c.v_scale : c.k_scale)[scale0 + (h << c.log2_page)];
+      } else {
+        raw[a].clear();
+        sc[a] = 0.0f;
       }
     }
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
+      if (h0 + a * (32 / LPR) >= heads) break;
+      const int hh = h0 + a * (32 / LPR) + lane / LPR;
+      const bool is_v = hh >= c.n_kv_heads, on = hh < heads;
+      const int h = is_v ? hh - c.n_kv_heads : hh;
+      uint8_t* cell = (is_v ? cv : ck) + h * head_step;
+      uint8_t* row = (is_v ? rv : rk) + h * (HD * elem_bytes(ROWDT));
+      float* scale = CDT == DT_E4M3 ? (is_v ? c.v_scale : c.k_scale) + scale0 + (h << c.log2_page) : nullptr;
+      float x[8];
+      raw[a].expand(x);
       if constexpr (CDT == DT_E4M3 && WRITE) {
         float top = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(x[a][e]));
+        for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(x[e]));
 #pragma unroll
         for (int d = LPR / 2; d >= 1; d >>= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
         const float s = max_nan(__fdiv_rn(top, kE4m3Max), kScaleMin);
-        if (on[a]) {
+        if (on) {
           if (s > kScaleFast) {
             // x / s correctly rounded by one correction of x times the correctly rounded 1 / s (Markstein, "Computation
             // of elementary functions on the IBM RISC System/6000", 1990); a remainder that underflows belongs to a
@@ -133,26 +159,25 @@ __global__ void __launch_bounds__(256)
             const float inv = __frcp_rn(s);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float y = __fmul_rn(x[a][e], inv);
-              x[a][e] = fmaf(fmaf(-y, s, x[a][e]), inv, y);
+              const float y = __fmul_rn(x[e], inv);
+              x[e] = fmaf(fmaf(-y, s, x[e]), inv, y);
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[a][e] = __fdiv_rn(x[a][e], s);
+            for (int e = 0; e < 8; ++e) x[e] = __fdiv_rn(x[e], s);
           }
-          store_row8<DT_E4M3>(cell[a], x[a]);
-          if (lane % LPR == 0) *scale[a] = s;
+          store_row8<DT_E4M3>(cell, x);
+          if (lane % LPR == 0) *scale = s;
         }
-      } else if (on[a]) {
+      } else if (on) {
         if constexpr (CDT == DT_E4M3) {
-          const float s = page >= 0 ? *scale[a] : 0.0f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[a][e] = __fmul_rn(x[a][e], s);
+          for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(x[e], sc[a]);
         }
         if (WRITE) {
-          store_row8<CDT>(cell[a], x[a]);
+          store_row8<CDT>(cell, x);
         } else {
-          store_row8<ROWDT>(row[a], x[a]);
+          store_row8<ROWDT>(row, x);
         }
       }
     }
