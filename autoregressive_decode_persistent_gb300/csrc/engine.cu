@@ -13,6 +13,7 @@
 #include <cstdio>
 #include <cstring>
 #include <string>
+#include <new>
 #include <vector>
 
 #include "../../include/adp.h"
@@ -1392,7 +1393,7 @@ static int reserve(adp_model* m, T** buf, size_t* cap, size_t n) {
 }
 
 extern "C" int adp_paged_forward(adp_model* m, const adp_paged_kv* layers, const int32_t* host_tokens,
-                                 const int32_t* host_cu_rows, const int32_t* host_lens, float* dev_logits) {
+                                 const int32_t* host_cu_rows, const int32_t* host_lens, float* dev_logits) try {
   if (!m || !layers || !host_cu_rows || !host_lens || !dev_logits) return ADP_ERR_INVALID_ARG;
   if (m->sticky) return m->sticky;
   const adp_config& c = m->cfg;
@@ -1527,6 +1528,9 @@ extern "C" int adp_paged_forward(adp_model* m, const adp_paged_kv* layers, const
   CK(cudaMemcpyAsync(&status, F.status, 4, cudaMemcpyDeviceToHost, m->stream));
   if ((rc = finish(m))) return rc;
   return status;
+} catch (const std::bad_alloc&) {  // the host's memory
+  adp::set_last_error("adp_paged_forward: out of host memory");
+  return ADP_ERR_CUDA;
 }
 
 extern "C" int adp_sync(adp_model* m) {

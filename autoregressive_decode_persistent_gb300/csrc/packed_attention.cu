@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 8) {
     if (warp == 10) {
       int index = blockIdx.x, published = 0, asked = 0, told = 0;
+      bool more = true;  // index and those behind it may be items
       while (true) {
         // (the next CTA is asked for before this item is found)
         if (index >= 0) {
@@ -279,7 +280,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           break;
         }
-        if (find_item(a, index, lane, &items[s])) {
+        // (the grid is an upper bound: behind the first index without an item there is none, and the rest is only taken
+        // over so that it is not launched)
+        more = more && find_item(a, index, lane, &items[s]);
+        if (more) {
           if (lane == 0) mbar_arrive(&ifull[s]);
           ++published;
         }

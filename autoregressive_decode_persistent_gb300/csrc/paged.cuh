@@ -54,7 +54,7 @@ inline int cuda_status(cudaError_t e, const char* where) {
 
 // Checks of a cache's description that need no device, and the kernels' view of it.
 inline int paged_view(const adp_paged_kv* c, PagedView* out) {
-  if (!c || !c->k || !c->v || !c->table || !c->lens) return ADP_ERR_INVALID_ARG;
+  if (!c || !c->k || !c->v || (c->n_seqs > 0 && (!c->table || !c->lens))) return ADP_ERR_INVALID_ARG;
   if (c->n_seqs < 0 || c->n_pages < 1 || c->table_width < 1 || c->n_kv_heads < 1 || c->page_size < 1)
     return ADP_ERR_INVALID_ARG;
   if (c->dtype != ADP_F16 && c->dtype != ADP_BF16 && c->dtype != ADP_E4M3) return ADP_ERR_UNSUPPORTED_CONFIG;

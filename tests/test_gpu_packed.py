@@ -219,3 +219,33 @@ def test_prompts_attend_through_a_quantised_cache(ops):
         assert ((got.double() - x).abs() <= x.abs() * (2.0 ** -4 + 2.0 ** -8) * 1.01 + x.abs().amax(-1, keepdim=True) / 448 * 2.0 ** -9).all()
     out = ops.packed_attention(q[cut:], kr, vr, torch.tensor([0, n - cut], **i32), torch.tensor([0, n], **i32))
     check(out, q[cut:], kr, vr, [n - cut], [n])
+
+
+def test_many_sequences(ops):
+    """500 short sequences: more than are sorted by cost, and a grid that is mostly an upper bound."""
+    rng = random.Random(8)
+    lq = [rng.randint(0, 6) for _ in range(500)]
+    lk = [n + rng.randint(0, 3) for n in lq]
+    q, k, v = inputs(lq, lk, (4, 2), 64, F16, seed=12)
+    out = torch.full_like(q, NAN)
+    ops.packed_attention(q, k, v, cumulative(lq), cumulative(lk), out=out)
+    check(out, q, k, v, lq, lk)
+
+
+def test_calls_at_once_and_the_result_in_the_queries_place(ops):
+    lq = [700, 90]
+    q, k, v = inputs(lq, lq, (16, 4), 128, BF16, seed=13)
+    cu = cumulative(lq)
+    want = ops.packed_attention(q, k, v, cu, cu)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(ops.packed_attention(q, k, v, cu, cu))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in got)
+    over = q.clone()
+    ops.packed_attention(over, k, v, cu, cu, out=over)
+    assert torch.equal(over, want)

@@ -236,11 +236,13 @@ def test_another_stream_and_captured_graphs_with_changing_lengths(ops):
         out = paged(ops, q, c)
     torch.cuda.current_stream().wait_stream(s)
     check_attention(out, q, c)
+    wide = torch.full((2, 20000), -1, dtype=torch.int32, device="cuda")  # (the even split, with its second launch)
+    wide[:, :c.table.shape[1]] = c.table
     graphs, outs = [], []
-    for _ in range(2):  # two graphs of one cache: each has a workspace of its own
+    for i in range(4):  # graphs of one cache: each has a workspace of its own
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            outs.append(paged(ops, q, c))
+            outs.append(paged(ops, q, c) if i < 2 else ops.paged_attention(q, c.k, c.v, wide, c.len_t))
         graphs.append(g)
     for lens in ([300, 10], [17, 0], [299, 5]):
         c.len_t.copy_(torch.tensor(lens, dtype=torch.int32))
@@ -419,3 +421,44 @@ def test_the_workspace_that_is_asked_for(ops):
     c, q = run([300, 10], (8, 2), 128, 16, F16, seed=22)
     kv = ops._paged("test", c.k, c.v, c.table, c.len_t, None, None, 0)
     assert adp.adp_paged_attention_workspace(kv, 8) == 0
+
+
+def test_calls_at_once_on_two_streams(ops):
+    """Two caches attended at the same time, each call with a workspace of its own, many times over."""
+    pairs = []
+    for seed in (31, 32):
+        c, q = run([6000, 300, 5], (8, 2), 64, 16, F16, seed=seed)  # (long enough for the even split)
+        pairs.append((c, q, paged(ops, q, c), torch.cuda.Stream()))
+        check_attention(pairs[-1][2], q, c)
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(30):
+        for c, q, _, s in pairs:
+            with torch.cuda.stream(s):
+                got.append((paged(ops, q, c), c))
+    torch.cuda.synchronize()
+    for out, c in got:
+        want = next(w for cc, _, w, _ in pairs if cc is c)
+        assert torch.equal(out, want)
+
+
+def test_no_sequences_and_no_rows(ops):
+    c = Cache([5], 2, 64, 16, F16, 1)
+    none = torch.zeros(0, 3, dtype=torch.int32, device="cuda")
+    no_lens = torch.zeros(0, dtype=torch.int32, device="cuda")
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = torch.zeros(0, 4, 64, dtype=F16, device="cuda")
+    assert ops.paged_attention(q, c.k, c.v, none, no_lens).shape == (0, 4, 64)
+    rows = torch.zeros(0, 2, 64, dtype=F16, device="cuda")
+    ops.paged_kv_write(c.k, c.v, none, no_lens, cu, rows, rows)
+    k, v = ops.paged_kv_read(c.k, c.v, none, no_lens, cu, 0)
+    assert k.shape == v.shape == (0, 2, 64)
+
+
+def test_the_result_in_the_queries_place(ops):
+    for lens in ([40, 3], [6000, 20]):
+        c, q = run(lens, (8, 2), 64, 16, F16, seed=33)
+        want = paged(ops, q, c)
+        got = q.clone()
+        paged(ops, got, c, out=got)
+        assert torch.equal(got, want)
