@@ -26,8 +26,7 @@ struct PackedArgs {
   uint8_t* out;
   int64_t v_stride, out_stride;  // bytes
   int32_t n_seqs, n_q, n_k, hkv, group, tok;
-  float scale_log2;              // of |scale|
-  int32_t negative;              // scale < 0
+  float scale_log2;              // of |scale|, and above 0
   int32_t* status;
 };
 
@@ -191,7 +190,7 @@ constexpr int kItems = 2;  // the item worked on and the next one: more known ah
 // Keys that a row does not see: their scores are replaced; their V must not meet the zero probabilities if it is not
 // finite, so blocks on the causal edge or the sequence's end are looked through in shared memory: rows behind the
 // sequence become zeros, non-finite elements too, and the (rare) latter are added to the rows that do see them at the end.
-template <int HD, bool BF16>
+template <int HD, bool BF16, bool NEG>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                             const __grid_constant__ CUtensorMap mv, const PackedArgs a) {
@@ -460,9 +459,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = w.t0 + t * a.tok + row_tok;
       const bool live = r < a.tok * a.group && tok < w.lq;
       const int lim = min(tok + w.lk - w.lq, w.lk - 1);  // the last key that this row sees
+      const int warp_lim = __reduce_min_sync(0xFFFFFFFFu, lim);
       // the first key that some row of the tiles with this block does not see: from its block on, blocks are edge blocks
       const int edge = w.t0 + w.lk - w.lq + 1 + (n0 > 0 ? 0 : a.tok);
-      float m = -INFINITY, l = 0.0f;
+      // the running maximum and sum, and the score above which the maximum is replaced (never by what stands in rows that
+      // are not the sequence's: it must not decide how the others are rounded)
+      float m = -INFINITY, l = 0.0f, limit = live ? -INFINITY : INFINITY;
       for (int j = 0; j < nk; ++j, ++ns) {
         const uint32_t buf = ns & 1;
         if (!wait_all(&sfull[2 * t + buf], (ns >> 1) & 1)) {
@@ -470,23 +472,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        if (j >= 2) {
-          if (!wait_all(&odone[2 * t + buf], ((ns >> 1) - 1) & 1)) {
-            ok = false;
-            break;
-          }
-          if (r == 0) mbar_arrive(&empty[(g + j - 2) % NS]);
-        }
+        // (S(j) was issued once the product of block j - 2 was done)
+        if (r == 0 && j >= 2) mbar_arrive(&empty[(g + j - 2) % NS]);
         __syncwarp();  // (the tensor-memory instructions want a warp in step)
         float x[kKeys];
         tmem_ld64(tS + buf * 64, x);
-        if (a.negative) {
+        if constexpr (NEG) {  // scale < 0
 #pragma unroll
           for (int c = 0; c < kKeys; ++c) x[c] = -x[c];
         }
         const int left = lim - j * kKeys;  // columns c <= left are seen
-        const bool all_seen = __all_sync(0xFFFFFFFFu, left >= kKeys - 1);
-        if (!all_seen) {
+        if (warp_lim - j * kKeys < kKeys - 1) {
 #pragma unroll
           for (int c = 0; c < kKeys; ++c) x[c] = c <= left ? x[c] : -INFINITY;
         }
@@ -499,14 +495,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], x[kKeys - 4 + e]);
         const float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
-        const float mb = mx == -INFINITY ? -INFINITY : mx * a.scale_log2;
-        // (only for rows of the sequence: what stands in the others must not decide how these are rounded)
-        const bool grow = live && (mb > m + kRescale || (m == -INFINITY && mb > -INFINITY));
+        const bool grow = mx > limit;
         if (__any_sync(0xFFFFFFFFu, grow)) {
-          const float mn = fmaxf(m, mb);
+          const float mn = live && mx > -INFINITY ? fmaxf(m, mx * a.scale_log2) : m;
           const float f = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
           m = mn;
           l *= f;
+          if (live && m > -INFINITY) limit = (m + kRescale) / a.scale_log2;
           if (j > 0) {
             // block j - 1's product must be in O
             if (!wait_all(&odone[2 * t + (buf ^ 1)], ((ns - 1) >> 1) & 1)) {
@@ -558,11 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             const float2 y = __ffma2_rn(make_float2(x[c0 + e], x[c0 + e + 1]), sc, nm);
-            float2 p = make_float2(exp2_fast(y.x), exp2_fast(y.y));
-            if (!all_seen) {
-              p.x = c0 + e <= left ? p.x : 0.0f;
-              p.y = c0 + e + 1 <= left ? p.y : 0.0f;
-            }
+            const float2 p = make_float2(exp2_fast(y.x), exp2_fast(y.y));  // (0 where x is -infinity: not seen)
             sum[(e >> 1) & 1] = __fadd2_rn(sum[(e >> 1) & 1], p);
             u[e >> 1] = pack2(p.x, p.y, BF16 ? DT_BF16 : DT_F16);
           }
@@ -574,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&pready[2 * t + buf]);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
-      // ---- O / l, behind the last two products
+      // ---- O / l, behind the last two products (S(nk - 1) was issued behind the others)
       if (ok && nk > 1) ok = wait_all(&odone[2 * t + (ns & 1)], ((ns - 2) >> 1) & 1);
       if (ok && nk > 0) ok = wait_all(&odone[2 * t + (~ns & 1)], ((ns - 1) >> 1) & 1);
       if (!ok) break;
@@ -668,13 +659,13 @@ bool encode(CUtensorMap* map, const void* base, bool bf16, int hd, int heads, in
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int HD, bool BF16>
+template <int HD, bool BF16, bool NEG>
 struct PackedKey {};
 
-template <int HD, bool BF16>
+template <int HD, bool BF16, bool NEG>
 cudaError_t packed_launch(const CUtensorMap (&m)[3], const PackedArgs& a, int64_t grid, cudaStream_t st) {
-  auto* kernel = packed_attention_kernel<HD, BF16>;
-  const cudaError_t e = allow_smem<PackedKey<HD, BF16>>((const void*)kernel, PackedSmem<HD>::kBytes);
+  auto* kernel = packed_attention_kernel<HD, BF16, NEG>;
+  const cudaError_t e = allow_smem<PackedKey<HD, BF16, NEG>>((const void*)kernel, PackedSmem<HD>::kBytes);
   if (e != cudaSuccess) return e;
   kernel<<<(unsigned)grid, kThreads, PackedSmem<HD>::kBytes, st>>>(m[0], m[1], m[2], a);
   return cudaGetLastError();
@@ -713,13 +704,25 @@ extern "C" int adp_packed_attention(const void* q, const void* k, const void* v,
       !encode(&m[2], n_k ? v : q, bf16, head_dim, n_kv_heads, n_k ? n_k : 1, n_k ? v_stride : kw, 1, kKeys))
     return ADP_ERR_INVALID_ARG;
   PackedArgs a{cu_q, cu_k, static_cast<const uint8_t*>(v), static_cast<uint8_t*>(out), v_stride * 2, out_stride * 2,
-               n_seqs, n_q, n_k, n_kv_heads, group, tok, fabsf(scale) * 1.4426950408889634f, scale < 0.0f, dev_status};
+               n_seqs, n_q, n_k, n_kv_heads, group, tok,
+               // (a scale of 0 becomes the least normal number: the scores' differences vanish all the same, and what is
+               // not seen stays at -infinity)
+               fmaxf(fabsf(scale) * 1.4426950408889634f, kScaleMin), dev_status};
   const int64_t pairs = (int64_t)n_q / (2 * tok) + n_seqs;  // at most: every sequence may end inside a pair
   const int64_t grid = pairs * n_kv_heads;
   if (grid > 0x7FFFFFFF) return ADP_ERR_UNSUPPORTED_CONFIG;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   cudaError_t e;
-  if (head_dim == 128) e = bf16 ? packed_launch<128, true>(m, a, grid, st) : packed_launch<128, false>(m, a, grid, st);
-  else e = bf16 ? packed_launch<64, true>(m, a, grid, st) : packed_launch<64, false>(m, a, grid, st);
+  auto by_sign = [&](auto hd, auto b) {
+    constexpr int H = decltype(hd)::value;
+    constexpr bool B = decltype(b)::value;
+    e = scale < 0.0f ? packed_launch<H, B, true>(m, a, grid, st) : packed_launch<H, B, false>(m, a, grid, st);
+  };
+  auto by_type = [&](auto hd) {
+    if (bf16) by_sign(hd, std::true_type());
+    else by_sign(hd, std::false_type());
+  };
+  if (head_dim == 128) by_type(std::integral_constant<int, 128>());
+  else by_type(std::integral_constant<int, 64>());
   return cuda_status(e, "adp_packed_attention");
 }
