@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int edge = w.t0 + w.lk - w.lq + 1 + (n0 > 0 ? 0 : a.tok);
       // the running maximum and sum, and the score above which the maximum is replaced (never by what stands in rows that
       // are not the sequence's: it must not decide how the others are rounded)
-      float m = -INFINITY, l = 0.0f, limit = live ? -INFINITY : INFINITY;
+      float m = -INFINITY, ms = 0.0f, l = 0.0f, limit = live ? -INFINITY : INFINITY;
       for (int j = 0; j < nk; ++j, ++ns) {
         const uint32_t buf = ns & 1;
         if (!wait_all(&sfull[2 * t + buf], (ns >> 1) & 1)) {
@@ -500,6 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float mn = live && mx > -INFINITY ? fmaxf(m, mx * a.scale_log2) : m;
           const float f = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
           m = mn;
+          ms = m == -INFINITY ? 0.0f : m;
           l *= f;
           if (live && m > -INFINITY) limit = (m + kRescale) / a.scale_log2;
           if (j > 0) {
@@ -524,27 +525,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         if ((j + 1) * kKeys > edge) {
           uint8_t* vt = ring + (g + j) % NS * L::kPair + L::kTile;
           const int key = r >> 1;  // two threads to a key
-          const bool outside = j * kKeys + key >= w.lk;
-#pragma unroll 1
-          for (int c = r & 1; c < HD / 8; c += 2) {
-            uint4* p = reinterpret_cast<uint4*>(vt + (c / 8) * L::kBlock + key * 128 + (((c & 7) ^ (key & 7)) * 16));
-            uint4 v = outside ? make_uint4(0, 0, 0, 0) : *p;
-            constexpr uint32_t kExp = BF16 ? 0x7F80u : 0x7C00u;
-            bool odd = false;
-            uint32_t* u = reinterpret_cast<uint32_t*>(&v);
+          auto piece = [&](int c) {
+            return reinterpret_cast<uint4*>(vt + (c / 8) * L::kBlock + key * 128 + (((c & 7) ^ (key & 7)) * 16));
+          };
+          constexpr uint32_t kExp = BF16 ? 0x7F80u : 0x7C00u, kExp2 = kExp * 0x10001u, kOne2 = (0x8000u - kExp) * 0x10001u;
+          if (j * kKeys + key >= w.lk) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const bool lo = (u[e] & kExp) == kExp, hi = (u[e] & (kExp << 16)) == (kExp << 16);
-              odd |= lo | hi;
-              u[e] = (lo ? 0u : u[e] & 0xFFFFu) | (hi ? 0u : u[e] & 0xFFFF0000u);
+            for (int c = 0; c < HD / 16; ++c) *piece(2 * c + (r & 1)) = make_uint4(0, 0, 0, 0);
+          } else {
+            // an exponent of all ones carries into its half's sign bit
+            uint32_t over = 0;
+#pragma unroll
+            for (int c = 0; c < HD / 16; ++c) {
+              const uint4 v = *piece(2 * c + (r & 1));
+              over |= ((v.x & kExp2) + kOne2) | ((v.y & kExp2) + kOne2) | ((v.z & kExp2) + kOne2) | ((v.w & kExp2) + kOne2);
             }
-            if (odd) *bad = 1;
-            if (odd || outside) *p = v;
+            if (over & 0x80008000u) {
+              *bad = 1;
+#pragma unroll 1
+              for (int c = r & 1; c < HD / 8; c += 2) {
+                uint4 v = *piece(c);
+                uint32_t* u = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  u[e] = ((u[e] & kExp) == kExp ? 0u : u[e] & 0xFFFFu) | ((u[e] & (kExp << 16)) == (kExp << 16) ? 0u : u[e] & 0xFFFF0000u);
+                *piece(c) = v;
+              }
+            }
           }
           fence_async_smem();
           __syncwarp();
         }
-        const float ms = m == -INFINITY ? 0.0f : m;
         const float2 sc = make_float2(a.scale_log2, a.scale_log2), nm = make_float2(-ms, -ms);
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
