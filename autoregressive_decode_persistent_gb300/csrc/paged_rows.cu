@@ -12,7 +12,7 @@ namespace adp {
 namespace {
 
 constexpr float kE4m3Max = 448.0f;
-constexpr float kScaleFast = 8.2718061e-25f;  // 2^-80: above it no remainder of a quotient over 2^-11 underflows
+constexpr float kTopFast = 3.7057691e-22f;  // 448 x 2^-80: above it no remainder of a quotient that counts underflows
 
 // The sequence that packed row i belongs to: the number of entries of cu[1 .. n] that are at most i (n for
 // rows behind the last sequence).  A whole warp asks; 32 entries are compared at a time.
@@ -27,6 +27,20 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int n, int i, in
     n = min(step, n - skip);
   }
   return lo + __popc(__ballot_sync(0xFFFFFFFFu, lane < n && cu[1 + lo + min(lane, max(n - 1, 0))] <= i));
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// x / s correctly rounded, from inv = the correctly rounded 1 / s: one correction of the product (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000", 1990).  A remainder that underflows belongs to a quotient whose
+// code is 0 either way.  (An infinity gives NaN.)
+__device__ __forceinline__ float divide(float x, float s, float inv) {
+  const float y = __fmul_rn(x, inv);
+  return fmaf(fmaf(-y, s, x), inv, y);
 }
 
 // 8 consecutive elements as they lie in memory.
@@ -48,6 +62,31 @@ struct Raw8 {
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int q = 0; q < 2 * elem_bytes(DT); ++q) w[q] = 0;
+  }
+  // The largest magnitude of the LPR lanes' elements (NaN if there is one); 16-bit types two at a time.
+  template <int LPR>
+  __device__ __forceinline__ float row_max() const {
+    if constexpr (DT == DT_F32) {
+      float top = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(__uint_as_float(w[e])));
+#pragma unroll
+      for (int d = LPR / 2; d >= 1; d >>= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+      return top;
+    } else {
+      uint32_t top = w[0] & 0x7FFF7FFFu;
+      auto larger = [](uint32_t a, uint32_t b) {
+        uint32_t r;
+        if constexpr (DT == DT_BF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+      };
+#pragma unroll
+      for (int e = 1; e < 4; ++e) top = larger(top, w[e] & 0x7FFF7FFFu);
+#pragma unroll
+      for (int d = LPR / 2; d >= 1; d >>= 1) top = larger(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+      return max_nan(kv_to_f32((uint16_t)top, DT), kv_to_f32((uint16_t)(top >> 16), DT));
+    }
   }
   // In fp32 (exact).
   __device__ __forceinline__ void expand(float (&x)[8]) const {
@@ -82,12 +121,6 @@ __device__ __forceinline__ void store_row8(uint8_t* p, const float (&x)[8]) {
   }
 }
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // Rows into pages (WRITE) or pages into rows, one warp per packed row.  Its K heads and then its V heads are one
 // line of 8-element pieces, a piece per lane, so that small rows fill a warp too.  Copying: bound by memory (45,000 bf16
 // rows of 8 x 128 read back in 92 us, 6.5 TB/s; 8 pieces in flight per lane instead of 4: the same, and 51 us instead of 47
@@ -102,6 +135,26 @@ __global__ void __launch_bounds__(256)
   const int lane = threadIdx.x & 31;
   const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (i >= n_rows) return;
+  const int heads = 2 * c.n_kv_heads, piece = (lane % LPR) * 8;
+  uint8_t *const rk = rows_k + (int64_t)i * k_stride + piece * elem_bytes(ROWDT);
+  uint8_t *const rv = rows_v + (int64_t)i * v_stride + piece * elem_bytes(ROWDT);
+  constexpr int kAhead = 4;  // pieces per lane in flight
+  constexpr int FROM = WRITE ? ROWDT : CDT;
+  Raw8<FROM> raw[kAhead];
+  auto row_piece = [&](int hh) {
+    const bool is_v = hh >= c.n_kv_heads;
+    return (is_v ? rv : rk) + (is_v ? hh - c.n_kv_heads : hh) * (HD * elem_bytes(ROWDT));
+  };
+  // the packed rows are asked for in front of the look-ups that say where they go
+  auto load_rows = [&](int h0) {
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int hh = h0 + a * (32 / LPR) + lane / LPR;
+      if (hh < heads) raw[a].load(row_piece(hh));
+      else raw[a].clear();
+    }
+  };
+  if constexpr (WRITE) load_rows(0);
   const int b = find_sequence(cu, c.n_seqs, i, lane);
   if (b >= c.n_seqs) return;  // behind the last sequence
   const int64_t pos = paged_position(c.lens[b], cu[b + 1], i);
@@ -109,30 +162,28 @@ __global__ void __launch_bounds__(256)
   if (page < 0 && lane == 0) report(status, ADP_ERR_INVALID_ARG);
   if (WRITE && page < 0) return;
   const int slot = (int)(pos & ((1 << c.log2_page) - 1));
-  const int heads = 2 * c.n_kv_heads;
-  // this lane's piece of head 0 in the page and in the packed row, and the way from head to head (32 bits hold it)
-  const int piece = (lane % LPR) * 8, head_step = (HD * elem_bytes(CDT)) << c.log2_page;
+  // this lane's piece of head 0 in the page, and the way from head to head (32 bits hold it)
+  const int head_step = (HD * elem_bytes(CDT)) << c.log2_page;
   const int64_t cell0 = (int64_t)page * c.page_bytes + ((int64_t)slot * HD + piece) * elem_bytes(CDT);
   uint8_t *const ck = c.k + cell0, *const cv = c.v + cell0;
-  uint8_t *const rk = rows_k + (int64_t)i * k_stride + piece * elem_bytes(ROWDT);
-  uint8_t *const rv = rows_v + (int64_t)i * v_stride + piece * elem_bytes(ROWDT);
   const int64_t scale0 = CDT == DT_E4M3 ? (int64_t)page * c.scale_stride + slot : 0;
-  constexpr int kAhead = 4;  // pieces per lane in flight
-  constexpr int FROM = WRITE ? ROWDT : CDT;
   for (int h0 = 0; h0 < heads; h0 += kAhead * (32 / LPR)) {
-    Raw8<FROM> raw[kAhead];
     float sc[kAhead];  // reading e4m3
+    if constexpr (WRITE) {
+      if (h0 > 0) load_rows(h0);
+    } else {
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int hh = h0 + a * (32 / LPR) + lane / LPR;
-      const bool is_v = hh >= c.n_kv_heads;
-      const int h = is_v ? hh - c.n_kv_heads : hh;
-      if (hh < heads && page >= 0) {
-        raw[a].load(WRITE ? (is_v ? rv : rk) + h * (HD * elem_bytes(ROWDT)) : (is_v ? cv : ck) + h * head_step);
-        if constexpr (CDT == DT_E4M3 && !WRITE) sc[a] = (is_v ? c.v_scale : c.k_scale)[scale0 + (h << c.log2_page)];
-      } else {
-        raw[a].clear();
-        sc[a] = 0.0f;
+      for (int a = 0; a < kAhead; ++a) {
+        const int hh = h0 + a * (32 / LPR) + lane / LPR;
+        const bool is_v = hh >= c.n_kv_heads;
+        const int h = is_v ? hh - c.n_kv_heads : hh;
+        if (hh < heads && page >= 0) {
+          raw[a].load((is_v ? cv : ck) + h * head_step);
+          if constexpr (CDT == DT_E4M3) sc[a] = (is_v ? c.v_scale : c.k_scale)[scale0 + (h << c.log2_page)];
+        } else {
+          raw[a].clear();
+          sc[a] = 0.0f;
+        }
       }
     }
 #pragma unroll
@@ -142,28 +193,22 @@ __global__ void __launch_bounds__(256)
       const bool is_v = hh >= c.n_kv_heads, on = hh < heads;
       const int h = is_v ? hh - c.n_kv_heads : hh;
       uint8_t* cell = (is_v ? cv : ck) + h * head_step;
-      uint8_t* row = (is_v ? rv : rk) + h * (HD * elem_bytes(ROWDT));
       float* scale = CDT == DT_E4M3 ? (is_v ? c.v_scale : c.k_scale) + scale0 + (h << c.log2_page) : nullptr;
       float x[8];
       raw[a].expand(x);
       if constexpr (CDT == DT_E4M3 && WRITE) {
-        float top = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(x[e]));
-#pragma unroll
-        for (int d = LPR / 2; d >= 1; d >>= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-        const float s = max_nan(__fdiv_rn(top, kE4m3Max), kScaleMin);
+        const float top = raw[a].template row_max<LPR>();
+        float s;
+        if (top > kTopFast) {
+          s = divide(top, kE4m3Max, 1.0f / kE4m3Max);
+        } else {
+          s = max_nan(__fdiv_rn(top, kE4m3Max), kScaleMin);
+        }
         if (on) {
-          if (s > kScaleFast) {
-            // x / s correctly rounded by one correction of x times the correctly rounded 1 / s (Markstein, "Computation
-            // of elementary functions on the IBM RISC System/6000", 1990); a remainder that underflows belongs to a
-            // quotient whose code is 0 either way
+          if (top > kTopFast) {
             const float inv = __frcp_rn(s);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float y = __fmul_rn(x[e], inv);
-              x[e] = fmaf(fmaf(-y, s, x[e]), inv, y);
-            }
+            for (int e = 0; e < 8; ++e) x[e] = divide(x[e], s, inv);
           } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = __fdiv_rn(x[e], s);
@@ -179,7 +224,7 @@ __global__ void __launch_bounds__(256)
         if (WRITE) {
           store_row8<CDT>(cell, x);
         } else {
-          store_row8<ROWDT>(row, x);
+          store_row8<ROWDT>(row_piece(hh), x);
         }
       }
     }
