@@ -1395,6 +1395,7 @@ static int reserve(adp_model* m, T** buf, size_t* cap, size_t n) {
 extern "C" int adp_paged_forward(adp_model* m, const adp_paged_kv* layers, const int32_t* host_tokens,
                                  const int32_t* host_cu_rows, const int32_t* host_lens, float* dev_logits) try {
   if (!m || !layers || !host_cu_rows || !host_lens || !dev_logits) return ADP_ERR_INVALID_ARG;
+  if ((uintptr_t)dev_logits & 15) return ADP_ERR_INVALID_ARG;  // the GEMM stores 16 bytes at a time
   if (m->sticky) return m->sticky;
   const adp_config& c = m->cfg;
   const int nb = layers[0].n_seqs;

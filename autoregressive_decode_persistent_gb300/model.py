@@ -145,7 +145,7 @@ class PagedCache:
     def forward(self, table, tokens, lens, logits: torch.Tensor | None = None) -> torch.Tensor:
         """One pass over the new tokens of several requests: table [requests][pages] page numbers, tokens a list of
         new tokens per request, lens their lengths with these.  Returns the logits [requests, vocab] of each
-        request's last new token."""
+        request's last new token (in `logits`: contiguous fp32 on the model's device, 16-byte aligned)."""
         c = self.model.cfg
         n_layers, n_pages, hkv, ps, hd = self.k.shape
         table = torch.as_tensor(table, dtype=torch.int32).to(self.model.device).contiguous()
@@ -153,7 +153,8 @@ class PagedCache:
         if logits is None:
             logits = torch.empty((len(tokens), c["vocab"]), dtype=torch.float32, device=self.model.device)
         if table.dim() != 2 or table.shape[0] != len(tokens) or len(lens) != len(tokens) or not logits.is_contiguous() \
-                or logits.dtype != torch.float32 or tuple(logits.shape) != (len(tokens), c["vocab"]):
+                or logits.dtype != torch.float32 or tuple(logits.shape) != (len(tokens), c["vocab"]) \
+                or logits.device != self.k.device or logits.data_ptr() % 16:
             raise adp.AdpError(adp.ADP_ERR_INVALID_ARG, "PagedCache.forward: table, tokens, lens and logits disagree")
         dt = adp.ADP_E4M3 if self.k_scale is not None else adp.DTYPES[c["kv_dtype"]]
         layers = (adp.PagedKV * n_layers)()

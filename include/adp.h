@@ -445,7 +445,8 @@ int adp_packed_attention(const void* q, const void* k, const void* v, int32_t dt
  *  host_cu_rows  HOST [n_seqs + 1]: sequence s has rows host_cu_rows[s] .. host_cu_rows[s + 1] - 1 (possibly none), its
  *                last positions
  *  host_lens     HOST [n_seqs]: its length with the new rows, at most max_ctx
- *  dev_logits    DEVICE float [n_seqs][vocab]: the logits of each sequence's last new row (zeros where it has none)
+ *  dev_logits    DEVICE float [n_seqs][vocab], 16-byte aligned: the logits of each sequence's last new row (zeros where
+ *                it has none)
  * Writes the new rows' K and V into their pages.  Like adp_prefill_tc it agrees with the oracle within the
  * tolerances, not bit for bit (e4m3 pages add the cache's rounding).  head_dim 64 or 128 and a 16-bit operand
  * type equal to kv_dtype, else ADP_ERR_UNSUPPORTED_CONFIG.  Runs on the model's stream and synchronises it; scratch grows with

@@ -136,3 +136,28 @@ def test_what_it_refuses(lib):
     assert code([[0]], [[1]], [1], PagedCache(m2, 4, 16)) == lib.ADP_ERR_UNSUPPORTED_CONFIG
     m2.close()
     model.close()
+
+
+def test_misaligned_logits_are_refused(lib):
+    """(The refusal of the C call itself; its stores are 16 bytes wide.)"""
+    from autoregressive_decode_persistent_gb300.model import DecodeModel, PagedCache
+    cfg = synth.get_config("tiny")
+    model = DecodeModel(cfg, synth.model_weights(cfg))
+    cache = PagedCache(model, 4, 16)
+    room = torch.zeros(cfg["vocab"] + 4, device="cuda")
+    assert room.data_ptr() % 16 == 0
+    hkv, hd = cfg["n_kv_heads"], cfg["head_dim"]
+    table = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    layers = (lib.PagedKV * cfg["n_layers"])()
+    for i in range(cfg["n_layers"]):
+        layers[i] = lib.PagedKV(cache.k[i].data_ptr(), cache.v[i].data_ptr(), None, None, table.data_ptr(), None,
+                                hkv * 16 * hd, 0, 4, 16, hkv, hd, lib.ADP_F16, 1, 1)
+    torch.cuda.synchronize()
+    for at in (1, 2, 3):
+        with pytest.raises(lib.AdpError) as e:
+            lib.adp_paged_forward(model.handle, layers, [1], [0, 1], [1], room[at:])
+        assert e.value.code == lib.ADP_ERR_INVALID_ARG
+    lib.adp_paged_forward(model.handle, layers, [1], [0, 1], [1], room[4:])
+    assert (room[:4] == 0).all() and room[4:].any()
+    assert torch.equal(room[4:], cache.forward([[0]], [[1]], [1])[0])
+    model.close()
