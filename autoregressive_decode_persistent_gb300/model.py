@@ -133,7 +133,9 @@ class PagedCache:
         c = model.cfg
         self.model = model
         own = torch.bfloat16 if c["kv_dtype"] == "bf16" else torch.float16
-        self.dtype = dtype or own
+        self.dtype = own if dtype is None else dtype
+        if self.dtype not in (own, torch.float8_e4m3fn):
+            raise adp.AdpError(adp.ADP_ERR_UNSUPPORTED_CONFIG, f"PagedCache: pages of {own} or float8_e4m3fn, not {dtype}")
         shape = (c["n_layers"], n_pages, c["n_kv_heads"], page_size, c["head_dim"])
         self.k = torch.zeros(shape, dtype=self.dtype, device=model.device)
         self.v = torch.zeros(shape, dtype=self.dtype, device=model.device)

@@ -43,3 +43,18 @@ def test_logits_that_the_engine_cannot_write_are_refused(calls):
     _refused(cache, calls, torch.zeros((2, VOCAB), dtype=torch.float16))
     _refused(cache, calls, torch.zeros((2, VOCAB + 1))[:, :VOCAB])
     _refused(cache, calls, torch.zeros((3, VOCAB)))
+
+
+@pytest.mark.parametrize("kv_dtype,own,other", [("f16", torch.float16, torch.bfloat16), ("bf16", torch.bfloat16, torch.float16)])
+def test_pages_of_a_type_that_the_engine_would_misread_are_refused(kv_dtype, own, other):
+    """The engine takes what is not e4m3 for the model's own 16-bit type: half a pool's bytes, or another type's bits."""
+    from autoregressive_decode_persistent_gb300 import adp
+    from autoregressive_decode_persistent_gb300.model import PagedCache
+    for dtype in (other, torch.float8_e5m2, torch.uint8, torch.int16, torch.float32):
+        with pytest.raises(adp.AdpError) as e:
+            PagedCache(_model(kv_dtype), 2, 16, dtype)
+        assert e.value.code == adp.ADP_ERR_UNSUPPORTED_CONFIG
+    for dtype in (None, own, torch.float8_e4m3fn):
+        cache = PagedCache(_model(kv_dtype), 2, 16, dtype)
+        assert cache.k.dtype == cache.v.dtype == (dtype or own)
+        assert (cache.k_scale is None) == (dtype != torch.float8_e4m3fn)
