@@ -27,6 +27,11 @@ ADP_INLINE int32_t paged_length(int32_t len, int32_t table_width, int log2_page)
 // positions.  Negative where it has fewer positions than rows.
 ADP_INLINE int64_t paged_position(int32_t len, int32_t next, int32_t i) { return (int64_t)len - ((int64_t)next - i); }
 
+// Whether packed row i is one of sequence b's rows [first, next) by its offsets: those of sequence 0 start at 0.
+ADP_INLINE bool paged_holds(int32_t b, int32_t first, int32_t next, int32_t i) {
+  return first <= i && i < next && (b == 0 ? first == 0 : first >= 0);
+}
+
 // The page of a position: an entry of the sequence's table row, or -1 where it has none or names no page.
 ADP_INLINE int32_t paged_page(const int32_t* table_row, int32_t table_width, int32_t n_pages, int log2_page, int64_t pos) {
   if (pos < 0 || (pos >> log2_page) >= table_width) return -1;

@@ -134,6 +134,9 @@ __global__ void __launch_bounds__(256)
   constexpr int LPR = HD / 8;  // lanes that hold one row of one head
   const int lane = threadIdx.x & 31;
   const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
+  // offsets that are wrong are reported, whichever rows they would move
+  for (int64_t s = (int64_t)blockIdx.x * 256 + threadIdx.x; s < c.n_seqs; s += (int64_t)gridDim.x * 256)
+    if (cu[s + 1] < cu[s] || (s == 0 && cu[0] != 0)) report(status, ADP_ERR_INVALID_ARG);
   if (i >= n_rows) return;
   const int heads = 2 * c.n_kv_heads, piece = (lane % LPR) * 8;
   uint8_t *const rk = rows_k + (int64_t)i * k_stride + piece * elem_bytes(ROWDT);
@@ -156,9 +159,16 @@ __global__ void __launch_bounds__(256)
   };
   if constexpr (WRITE) load_rows(0);
   const int b = find_sequence(cu, c.n_seqs, i, lane);
-  if (b >= c.n_seqs) return;  // behind the last sequence
-  const int64_t pos = paged_position(c.lens[b], cu[b + 1], i);
-  const int page = paged_page(c.table + (int64_t)b * c.table_width, c.table_width, c.n_pages, c.log2_page, pos);
+  int64_t pos = 0;
+  int page = -1;
+  if (b < c.n_seqs) {
+    const int first = cu[b], next = cu[b + 1], len = c.lens[b];
+    pos = paged_position(len, next, i);
+    if (paged_holds(b, first, next, i))  // else the position may lie behind the sequence's length
+      page = paged_page(c.table + (int64_t)b * c.table_width, c.table_width, c.n_pages, c.log2_page, pos);
+  } else if (cu[c.n_seqs] <= i) {
+    return;  // behind the last sequence
+  }
   if (page < 0 && lane == 0) report(status, ADP_ERR_INVALID_ARG);
   if (WRITE && page < 0) return;
   const int slot = (int)(pos & ((1 << c.log2_page) - 1));

@@ -380,8 +380,9 @@ typedef struct {
  *  cu_rows     DEVICE [n_seqs + 1], ascending from 0; rows from cu_rows[n_seqs] on are padding
  * 16-bit pages: rounded to nearest even.  e4m3 pages: per row and head the scale is max|x| / 448 (at least
  * 2^-126) and the codes are x / scale to nearest even; a row that holds an infinity or NaN reads back as NaN.
- * A row without a page (a position below 0 or behind the table, a page number outside the pool) is not
- * written, and reported as ADP_ERR_INVALID_ARG.  Two rows that name one slot leave it with either row's
+ * A row without a page (a position below 0 or behind the table, a page number outside the pool, or a row that no
+ * sequence's offsets hold) is not written, and reported as ADP_ERR_INVALID_ARG, as are offsets that descend or do not
+ * start at 0 (every row of the first sequence then has no page).  Two rows that name one slot leave it with either row's
  * values, per head and per 16 bytes: name each slot once.
  * Errors: ADP_ERR_INVALID_ARG, ADP_ERR_UNSUPPORTED_CONFIG, ADP_ERR_CUDA. */
 int adp_paged_kv_write(const adp_paged_kv* kv, const void* k, const void* v, int32_t rows_dtype, int64_t k_stride,

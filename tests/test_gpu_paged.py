@@ -462,3 +462,70 @@ def test_the_result_in_the_queries_place(ops):
         got = q.clone()
         paged(ops, got, c, out=got)
         assert torch.equal(got, want)
+
+
+WRONG_OFFSETS = [  # offsets of two sequences, rows, and by row: (sequence, rows behind it) or None; rows not named are padding
+    ([0, 50, 20], 30, {**{i: (0, 50 - i) for i in range(20)}, **dict.fromkeys(range(20, 30))}),
+    ([5, 10, 20], 20, {**dict.fromkeys(range(10)), **{i: (1, 20 - i) for i in range(10, 20)}}),
+    ([-5, 10, 20], 20, {**dict.fromkeys(range(10)), **{i: (1, 20 - i) for i in range(10, 20)}}),
+    ([0, -5, 20], 20, dict.fromkeys(range(20))),
+    ([0, 2 ** 31 - 1, -2 ** 31], 20, dict.fromkeys(range(20))),
+    ([20, 10, 0], 20, dict.fromkeys(range(10)))]
+
+
+@pytest.mark.parametrize("dtype", [F16, E4M3])
+@pytest.mark.parametrize("cu,n_rows,where", WRONG_OFFSETS)
+def test_row_offsets_that_are_wrong_are_reported(ops, dtype, cu, n_rows, where):
+    """Rows that no sequence's offsets hold are not written (read: zeros), whatever the tables hold behind the lengths."""
+    lens, page = [60, 40], 8
+    c = Cache(lens, 1, 64, page, dtype, 7)
+    stale = next(p for p in range(c.k.shape[0]) if p not in c.table.flatten().tolist())
+    c.table[c.table < 0] = stale  # entries behind the lengths name a page of somebody else's
+    offsets = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    was = [raw(c.k).clone(), raw(c.v).clone()]
+    x = torch.randn(n_rows, 1, 64, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ops.paged_kv_write(c.k, c.v, c.table, c.len_t, offsets, x, x, status=status, **c.scales)
+    assert int(status) == -1
+    at = {i: (s, lens[s] - n) for i, (s, n) in ((i, w) for i, w in where.items() if w)}
+    cells = torch.zeros(c.k.shape[0], page, dtype=torch.bool)
+    for s, p in at.values():
+        cells[int(c.table[s, p // page]), p % page] = True
+    for pool, before in zip((c.k, c.v), was):
+        changed = (raw(pool) != before).any(-1)[:, 0].cpu()
+        assert torch.equal(changed, cells)
+    status.zero_()
+    out = tuple(torch.full((n_rows, 1, 64), 7.0, device="cuda") for _ in range(2))
+    ops.paged_kv_read(c.k, c.v, c.table, c.len_t, offsets, n_rows, out=out, status=status, **c.scales)
+    assert int(status) == -1
+    for got, pool, name in ((out[0], c.k, "k_scale"), (out[1], c.v, "v_scale")):
+        for i in range(n_rows):
+            if i not in where:
+                assert (got[i] == 7).all()
+            elif i not in at:
+                assert (got[i] == 0).all()
+            else:
+                s, p = at[i]
+                cell = int(c.table[s, p // page]), 0, p % page
+                want = pool[cell[0]].cpu().float()[0, p % page]
+                if dtype == E4M3:
+                    want = want * c.scales[name][cell].cpu()
+                assert torch.equal(got[i, 0].cpu(), want)
+
+
+def test_a_descending_pair_among_many_row_offsets(ops):
+    """40 sequences (more than one comparison of a warp), two of whose offsets descend: no row lands behind a length."""
+    lens, page = [9] * 40, 4
+    c = Cache(lens, 1, 64, page, F16, 8, spare=2)
+    behind = (torch.arange(c.table.shape[1] * page)[None] >= 9).expand(40, -1)  # positions behind the lengths
+    cu = list(range(0, 3 * 41, 3))
+    cu[20], cu[21] = cu[21], cu[20]
+    x = torch.ones(120, 1, 64, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ops.paged_kv_write(c.k, c.v, c.table, c.len_t, torch.tensor(cu, dtype=torch.int32, device="cuda"), x, x, status=status)
+    assert int(status) == -1
+    one = (c.k == 1).all(-1)[:, 0].cpu()  # [pages, slots]
+    for b in range(40):
+        for p in range(c.table.shape[1] * page):
+            if behind[b, p]:
+                assert not one[int(c.table[b, p // page]), p % page], (b, p)

@@ -155,3 +155,18 @@ def test_the_split_covers_every_unit_once_and_owners_agree(index):
         for i in range(parts):
             for u in {edges[i], edges[i + 1] - 1, rng.randrange(edges[i], edges[i + 1])}:
                 assert index.t_owner(total, parts, u) == i
+
+
+def test_rows_that_no_offsets_hold(tmp_path):
+    """paged_holds (csrc/paged.h) against the sets of rows that the offsets name."""
+    src, lib = tmp_path / "holds.cpp", tmp_path / "holds.so"
+    src.write_text('#include "%s"\nextern "C" int t_holds(int32_t b, int32_t f, int32_t n, int32_t i) '
+                   "{ return adp::paged_holds(b, f, n, i); }\n"
+                   % os.path.join(ROOT, "autoregressive_decode_persistent_gb300", "csrc", "paged.h"))
+    subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", str(src), "-o", str(lib)], check=True)
+    L = ctypes.CDLL(str(lib))
+    for cu in ([0, 3, 3, 7], [0, 50, 20, 60], [5, 10, 20, 20], [-5, 10, 12, 14], [0, -5, 4, 9], [0, 2 ** 31 - 1, -2 ** 31, 3]):
+        for b in range(3):
+            rows = range(cu[b], cu[b + 1]) if cu[b] >= 0 and (b > 0 or cu[0] == 0) else ()
+            for i in list(range(70)) + [2 ** 31 - 2, 2 ** 31 - 1]:
+                assert bool(L.t_holds(b, cu[b], cu[b + 1], i)) == (i in rows)
