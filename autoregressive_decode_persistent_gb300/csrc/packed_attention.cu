@@ -169,6 +169,12 @@ struct PackedSmem {
   static constexpr size_t kBytes = 1024 + kBars + 768;
 };
 
+// fp16 weights are held 2^7 times larger (and so is their sum): up to 2^15 beside a maximum that is stale by 2^8, they stay
+// below fp16's 65,504, and a weight keeps all its bits down to 2^-21 of the largest and some down to 2^-32, where 2^-14 and
+// 2^-25 would let the tail of a long context vanish beside one dominating key.  (bf16 has fp32's range.)
+template <bool BF16>
+constexpr float kWeightUp = BF16 ? 0.0f : 7.0f;
+
 constexpr int kItems = 2;  // the item worked on and the next one: more known ahead would keep work from idle SMs
 
 // A persistent kernel: a CTA works on items (one KV head's group of query heads for 2 x tok consecutive tokens of one
@@ -464,8 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int warp_lim = __reduce_min_sync(0xFFFFFFFFu, lim);
       // the first key that some row of the tiles with this block does not see: from its block on, blocks are edge blocks
       const int edge = w.t0 + w.lk - w.lq + 1 + (n0 > 0 ? 0 : a.tok);
-      // the running maximum and sum, and the score above which the maximum is replaced (never by what stands in rows that
-      // are not the sequence's: it must not decide how the others are rounded)
+      // the running maximum (and ms, what is subtracted from scores) and sum, and the score above which the maximum is
+      // replaced (never by what stands in rows that are not the sequence's: it must not decide how the others are rounded)
       float m = -INFINITY, ms = 0.0f, l = 0.0f, limit = live ? -INFINITY : INFINITY;
       for (int j = 0; j < nk; ++j, ++ns) {
         const uint32_t buf = ns & 1;
@@ -502,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float mn = live && mx > -INFINITY ? fmaxf(m, mx * a.scale_log2) : m;
           const float f = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
           m = mn;
-          ms = m == -INFINITY ? 0.0f : m;
+          ms = m == -INFINITY ? 0.0f : m - kWeightUp<BF16>;
           l *= f;
           if (live && m > -INFINITY) limit = (m + kRescale) / a.scale_log2;
           if (j > 0) {

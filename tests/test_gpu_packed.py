@@ -249,3 +249,24 @@ def test_calls_at_once_and_the_result_in_the_queries_place(ops):
     over = q.clone()
     ops.packed_attention(over, k, v, cu, cu, out=over)
     assert torch.equal(over, want)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_a_dominating_key_leaves_the_others_their_weights(ops, hd):
+    """Key 0 outweighs every other one by 2^25.5 and its V is 0: the result is the others' share alone, whose fp16 weights
+    must not vanish beside it."""
+    lq, lk, bits = [300], [4096], 25.5
+    q, k, v = inputs(lq, lk, (4, 1), hd, F16, seed=20)
+    q, k, v = torch.zeros_like(q), torch.zeros_like(k), v.abs() + 0.5
+    q[:, :, 0] = bits * math.log(2)
+    k[0, 0, 0] = 1.0
+    v[0] = 0.0
+    out = ops.packed_attention(q, k, v, cumulative(lq), cumulative(lk), scale=1.0).double()
+    s = torch.einsum("ihd,jd->hij", q.double(), k[:, 0].double())
+    seen = torch.arange(lk[0], device="cuda")[None] <= torch.arange(lq[0], device="cuda")[:, None] + lk[0] - lq[0]
+    p = torch.softmax(s.masked_fill(~seen, -math.inf), 2)
+    o = torch.einsum("hij,jd->ihd", p, v[:, 0].double())
+    # as in check (V is positive), but fp16's least half step 2^-25 is one of weights that are held 2^7 times larger
+    ds = bits * math.log(2) * (hd + 8) * 2.0 ** -24
+    tol = o * (2 * half_step(F16) + 2 * ds + 2.0 ** -19 + lk[0] * 2.0 ** -24) + 2.0 ** -32 * v[:, 0].double().sum(0)
+    assert ((out - o).abs() <= tol).all(), float(((out - o).abs() / tol).max())
