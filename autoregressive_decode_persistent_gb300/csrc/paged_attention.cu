@@ -55,6 +55,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 constexpr float kStale = 8.0f;  // how far scores may exceed the maximum in use (base-2 exponents)
+// fp16 weights are held 2^7 times larger, and their sum alike: up to 2^15 beside a stale maximum they fit, and a weight has
+// all its bits down to 2^-21 of the largest and some down to 2^-32, so that a long context's tail does not vanish beside
+// one dominating position.  (bf16 has fp32's range.)
+template <int CDT>
+constexpr float kWeightUp = CDT == DT_BF16 ? 0.0f : 7.0f;
 
 __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.0f : m; }
 
@@ -537,8 +542,8 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
           for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              float p0 = exp2_fast(s[g][nt][2 * r] - safe_max(m[nt][0]));
-              float p1 = exp2_fast(s[g][nt][2 * r + 1] - safe_max(m[nt][1]));
+              float p0 = exp2_fast(s[g][nt][2 * r] - (safe_max(m[nt][0]) - kWeightUp<CDT>));
+              float p1 = exp2_fast(s[g][nt][2 * r + 1] - (safe_max(m[nt][1]) - kWeightUp<CDT>));
               l[nt][0] += p0;
               l[nt][1] += p1;
               if constexpr (Q8) {

@@ -529,3 +529,34 @@ def test_a_descending_pair_among_many_row_offsets(ops):
         for p in range(c.table.shape[1] * page):
             if behind[b, p]:
                 assert not one[int(c.table[b, p // page]), p % page], (b, p)
+
+
+@pytest.mark.parametrize("heads", [(4, 1), (16, 1)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_a_dominating_position_leaves_the_others_their_weights(ops, heads, wide):
+    """Position 0 outweighs every other one by 2^25.5 and its V is 0: the result is the others' share alone, whose fp16
+    weights must not vanish beside it."""
+    n, hd, bits = 4096, 64, 25.5
+    c = Cache([n], 1, hd, 16, F16, 40)
+    g = torch.Generator().manual_seed(41)
+    held = [torch.zeros(n, 1, hd), torch.rand(n, 1, hd, generator=g) + 0.5]
+    held[0][0, 0, 0] = 1.0
+    held[1][0] = 0.0
+    for pool, x in zip((c.k, c.v), held):
+        x = x.to(F16).cuda()
+        for p0 in range(0, n, 16):
+            pool[int(c.table[0, p0 // 16])] = x[p0:p0 + 16].transpose(0, 1)
+    k, v = (x.to(F16).double() for x in held)
+    q = torch.zeros(1, heads[0], hd)
+    q[:, :, 0] = bits * math.log(2)
+    q = q.to(F16).cuda()
+    table = c.table
+    if wide:  # (the even split)
+        table = torch.full((1, 20000), -1, dtype=torch.int32, device="cuda")
+        table[:, :c.table.shape[1]] = c.table
+    out = ops.paged_attention(q, c.k, c.v, table, c.len_t, scale=1.0)[0].double().cpu()
+    o, a, ds, _ = attend64(q[0].double().cpu(), k, v, 1.0)
+    # as in check_attention, but fp16's least half step 2^-25 is one of weights that are held 2^7 times larger
+    tol = half_step(F16) * o.abs() + a * (half_step(F16) + 2 * ds[:, None] + 2.0 ** -19 + n * 2.0 ** -24)
+    tol = tol + 2.0 ** -32 * v.abs().sum((0, 1))
+    assert ((out - o).abs() <= tol).all(), float(((out - o).abs() / tol).max())
