@@ -54,7 +54,18 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float log2_fast(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 constexpr float kStale = 8.0f;  // how far scores may exceed the maximum in use (base-2 exponents)
+constexpr float kFactorMax = 1.329227996e36f;  // 2^120, of a value scale relative to the largest product
 // fp16 weights are held 2^7 times larger, and their sum alike: up to 2^15 beside a stale maximum they fit, and a weight has
 // all its bits down to 2^-21 of the largest and some down to 2^-32, so that a long context's tail does not vanish beside
 // one dominating position.  (bf16 has fp32's range.)
@@ -127,7 +138,8 @@ constexpr int kResident = NT == 1 ? 3 : 2;
 // free, and Q's is chosen alike), O^T = V^T P^T takes V's with the 16-bit halves of two keys interleaved.  With the
 // query heads as the 8-wide side a group of up to 8 heads costs one instruction per 16 x 16 of K; nothing is staged
 // in shared memory.  e4m3 codes become fp16 (exact), their scales multiply the scores and the probabilities.
-// Measured: 131,011 bf16 positions of 8 KV heads 91.5 us (5.9 TB/s), 64 ragged e4m3 sequences 87 us (5.2 TB/s); with an
+// Measured: 131,011 bf16 positions of 8 KV heads 91.5 us (5.9 TB/s), 64 ragged e4m3 sequences 89 us (5.1 TB/s; 87 with one unit
+// of O for a warp, the largest value scale: it took bits from the others whatever its own weight); with an
 // L2 prefetch of one unit more 96 and 93.  The first form (8 warps, every load predicated, a maximum updated every unit)
 // took 124 us for the latter.
 template <int HD, int CDT, int QDT, int NT, bool SMALL>
@@ -304,10 +316,14 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
 
       float o[MT][NT][4];
       float m[NT][2], l[NT][2];
-      float vref = kScaleMin, vinv = 1.0f / kScaleMin;  // e4m3: O is held in units of vref, a power of two
+      // e4m3: what weighs V's codes are the products weight x value scale.  They have a running maximum of their own, mo
+      // (base-2 exponents: score + log2 of the scale), O is relative to it, and vc = 2^(m - mo) brings them there: a large
+      // scale counts only with its weight, so that one beside a negligible weight takes no bits from the others.
+      float mo[NT][2], vc[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        m[nt][0] = m[nt][1] = -INFINITY;
+        m[nt][0] = m[nt][1] = mo[nt][0] = mo[nt][1] = -INFINITY;
+        vc[nt][0] = vc[nt][1] = 1.0f;
         l[nt][0] = l[nt][1] = 0.0f;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -473,22 +489,23 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
             for (int j = 0; j < 2; ++j) ks_now[g][j] = ksc[g][j], vs_now[g][j] = vsc[g][j];
         }
         if (more) load_k(t + i + 1);
-        // ---- scores in base-2 exponents; the running maximum (and e4m3's unit of O) are replaced only when some score
-        // exceeds the maximum by more than 8, decided per warp: till then the weights stay below 2^8, and the same
-        // stale maximum scales O and l alike
+        // ---- scores in base-2 exponents; the running maxima are replaced only when some score (or e4m3's score + log2 of
+        // the value scale) exceeds its maximum by more than 8, decided per warp: till then the weights stay below 2^8, and
+        // the same stale maximum scales O and l alike
         bool need = false;
-        float vtop = 0.0f;
-        if constexpr (Q8) {
+        float lv[RG][2];
+        if constexpr (Q8) {  // (2^-126 is the least scale that a row is given: the logarithm is finite for 0, too)
 #pragma unroll
-          for (int g = 0; g < RG; ++g) vtop = fmaxf(vtop, fmaxf(vs_now[g][0], vs_now[g][1]));
-          need = vtop > vref;
+          for (int g = 0; g < RG; ++g)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) lv[g][r] = fmaxf(log2_fast(fabsf(vs_now[g][r])), -126.0f);
         }
-        float top[NT][2];
+        float top[NT][2], topo[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            top[nt][j] = -INFINITY;
+            top[nt][j] = topo[nt][j] = -INFINITY;
 #pragma unroll
             for (int g = 0; g < RG; ++g)
 #pragma unroll
@@ -498,22 +515,13 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
                 if (!full) x = (on >> (2 * g + r)) & 1 ? x : -INFINITY;
                 s[g][nt][2 * r + j] = x;
                 top[nt][j] = fmaxf(top[nt][j], x);
+                if constexpr (Q8) topo[nt][j] = fmaxf(topo[nt][j], x + lv[g][r]);
               }
             need |= top[nt][j] > m[nt][j] + kStale;
+            if constexpr (Q8) need |= topo[nt][j] > mo[nt][j] + kStale;
           }
         }
         if (__any_sync(0xFFFFFFFFu, need)) {
-          float grow = 1.0f;  // e4m3: the old unit of O in the new one
-          if constexpr (Q8) {
-#pragma unroll
-            for (int d = 4; d <= 16; d <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xFFFFFFFFu, vtop, d));
-            if (vtop > vref) {
-              const float nref = __uint_as_float((__float_as_uint(vtop) + 0x7FFFFFu) & 0x7F800000u);
-              vinv = 1.0f / nref;
-              grow = vref * vinv;
-              vref = nref;
-            }
-          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -522,13 +530,22 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
 #pragma unroll
               for (int d = 4; d <= 16; d <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, d));
               mn = fmaxf(m[nt][j], mn);
-              const float f = exp2_fast(m[nt][j] - safe_max(mn));
+              float f = exp2_fast(m[nt][j] - safe_max(mn));
               m[nt][j] = mn;
               l[nt][j] *= f;
+              if constexpr (Q8) {  // (both maxima at once: mo is m - 126 at least, and vc finite)
+                float mw = topo[nt][j];
+#pragma unroll
+                for (int d = 4; d <= 16; d <<= 1) mw = fmaxf(mw, __shfl_xor_sync(0xFFFFFFFFu, mw, d));
+                mw = fmaxf(mo[nt][j], mw);
+                f = exp2_fast(mo[nt][j] - safe_max(mw));
+                mo[nt][j] = mw;
+                vc[nt][j] = mw == -INFINITY ? 1.0f : exp2_fast(mn - mw);
+              }
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
-                o[mt][nt][j] *= f * grow;
-                o[mt][nt][2 + j] *= f * grow;
+                o[mt][nt][j] *= f;
+                o[mt][nt][2 + j] *= f;
               }
             }
         }
@@ -546,9 +563,9 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
               float p1 = exp2_fast(s[g][nt][2 * r + 1] - (safe_max(m[nt][1]) - kWeightUp<CDT>));
               l[nt][0] += p0;
               l[nt][1] += p1;
-              if constexpr (Q8) {
-                const float f = vs_now[g][r] * vinv;
-                p0 *= f, p1 *= f;
+              if constexpr (Q8) {  // (cut where the weight is 0 next to it, or as good as: 0 times infinity is none)
+                p0 *= min_nan(vs_now[g][r] * vc[nt][0], kFactorMax);
+                p1 *= min_nan(vs_now[g][r] * vc[nt][1], kFactorMax);
               }
               const uint32_t hi = pack2(p0, p1, BF ? DT_BF16 : DT_F16);
               pf[nt][r] = transpose8x8(hi);
@@ -591,6 +608,19 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int d = 4; d <= 16; d <<= 1) l[nt][j] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][j], d);
+      if constexpr (Q8) {  // O relative to m (in two steps, so that the factor does not leave fp32's range)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float f = mo[nt][j] == -INFINITY ? 0.0f : exp2_fast(0.5f * (mo[nt][j] - m[nt][j]));
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              o[mt][nt][j] = o[mt][nt][j] * f * f;
+              o[mt][nt][2 + j] = o[mt][nt][2 + j] * f * f;
+            }
+          }
+      }
       // Element d of this lane's head 2 l4 + j: tile mt, register j (even d) and 2 + j (odd d).
       auto elem = [&](int mt) { return Q8 ? r8 * VB + 2 * mt : ((mt / 4) * 8 + r8) * 8 + 2 * (mt % 4); };
       const bool whole = t == 0 && n == n_units;
@@ -607,10 +637,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
             for (int mt = 0; mt < MT; mt += 4) {
               uint32_t w[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float f = Q8 ? vref : 1.0f;
-                w[e] = pack2(o[mt + e][nt][j] * inv * f, o[mt + e][nt][2 + j] * inv * f, QDT);
-              }
+              for (int e = 0; e < 4; ++e) w[e] = pack2(o[mt + e][nt][j] * inv, o[mt + e][nt][2 + j] * inv, QDT);
               *reinterpret_cast<uint4*>(po + elem(mt) * 2) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
@@ -623,10 +650,8 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
           for (int j = 0; j < 2; ++j) {
             const int h = nt * 8 + 2 * l4 + j;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              const float f = Q8 ? vref : 1.0f;
-              *reinterpret_cast<float2*>(&P.o[h][elem(mt)]) = make_float2(o[mt][nt][j] * f, o[mt][nt][2 + j] * f);
-            }
+            for (int mt = 0; mt < MT; ++mt)
+              *reinterpret_cast<float2*>(&P.o[h][elem(mt)]) = make_float2(o[mt][nt][j], o[mt][nt][2 + j]);
             if (r8 == 0) {
               P.m[h] = m[nt][j];
               P.l[h] = l[nt][j];

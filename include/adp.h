@@ -406,8 +406,9 @@ int adp_paged_kv_read(const adp_paged_kv* kv, void* k, void* v, int32_t rows_dty
  *  scale       finite
  *  workspace   DEVICE scratch of at least adp_paged_attention_workspace bytes, 16-byte aligned (may be NULL
  *              where that is 0); its contents do not matter.  Calls that may run at the same time need one each.
- * Scores, softmax and sums are fp32; probabilities are rounded to fp16 (f16 and e4m3 caches) or to two bf16
- * terms before they weigh V.  A sequence of length 0 gives zeros.  A position whose page number is outside the
+ * Scores, softmax and sums are fp32; before they weigh V, probabilities are rounded to two bf16 terms, or to fp16 (f16
+ * caches; e4m3 caches: probability x value scale), to 11 bits down to 2^-21 of the largest and to a step of 2^-31 of it
+ * below.  A sequence of length 0 gives zeros.  A position whose page number is outside the
  * pool is left out and reported as ADP_ERR_INVALID_ARG; a length behind the table is cut and reported as
  * ADP_ERR_CONTEXT_OVERFLOW; one below 0 counts as 0 and is reported as ADP_ERR_INVALID_ARG.  Equal inputs
  * give equal bits on one GPU. */

@@ -560,3 +560,66 @@ def test_a_dominating_position_leaves_the_others_their_weights(ops, heads, wide)
     tol = half_step(F16) * o.abs() + a * (half_step(F16) + 2 * ds[:, None] + 2.0 ** -19 + n * 2.0 ** -24)
     tol = tol + 2.0 ** -32 * v.abs().sum((0, 1))
     assert ((out - o).abs() <= tol).all(), float(((out - o).abs() / tol).max())
+
+
+@pytest.mark.parametrize("q_dtype", [F16, BF16])
+@pytest.mark.parametrize("heads,hd,wide", [((4, 1), 128, False), ((16, 1), 64, True), ((8, 2), 64, False)])
+def test_a_large_value_scale_that_hardly_counts_leaves_the_others_theirs(ops, q_dtype, heads, hd, wide):
+    """One position's V scale is 2^26 times the others', and its score so low that it weighs next to nothing: the others'
+    values keep their bits.  Another one's V is all zeros, at the least scale there is, and weighs the most."""
+    n = 200
+    c, q = run([n], heads, hd, 16, E4M3, q_dtype, seed=42)
+    hkv, group = heads[1], heads[0] // heads[1]
+    q = (q.float() + 1.0).to(q_dtype)  # (every query has a good part along the vector of ones)
+    at = lambda p: (int(c.table[0, p // 16]), slice(None), p % 16)
+    for p, sign, f in ((70, -1.0, 2.0 ** 26), (130, 1.0, None)):
+        c.k.view(torch.uint8)[at(p)] = torch.full((hkv, hd), sign, device="cuda").to(E4M3).view(torch.uint8)
+        c.scales["k_scale"][at(p)] = (60.0 if sign < 0 else 20.0) / hd ** 0.5
+        c.kv[0][0][p] = sign * float(c.scales["k_scale"][at(p)][0])
+        if f is None:
+            c.v.view(torch.uint8)[at(p)] = 0
+            c.scales["v_scale"][at(p)] = 2.0 ** -126
+            c.kv[1][0][p] = 0
+        else:
+            c.scales["v_scale"][at(p)] *= f
+            c.kv[1][0][p] *= f
+    table = c.table
+    if wide:  # (the even split)
+        table = torch.full((1, 20000), -1, dtype=torch.int32, device="cuda")
+        table[:, :c.table.shape[1]] = c.table
+    out = ops.paged_attention(q, c.k, c.v, table, c.len_t, **c.scales)[0].double().cpu()
+    qd, k, v = q[0].double().cpu(), c.kv[0][0], c.kv[1][0]
+    o, a, ds, _ = attend64(qd, k, v, hd ** -0.5)
+    s = torch.einsum("hd,nhd->hn", qd, k.repeat_interleave(group, 1)) * hd ** -0.5
+    p = torch.softmax(s, 1)
+    assert float(p[:, 70].max()) < 2.0 ** -60 and float(p[:, 130].min()) > 0.1
+    # as in check_attention; fp16's least half step is one of the products weight x value scale, held so that the largest of
+    # them is 2^7 at least, times codes of at most 448
+    largest = (p * c.scales["v_scale"].double().cpu()[c.table[0].long().cpu()].transpose(1, 2).reshape(-1, hkv)[:n].T
+               .repeat_interleave(group, 0)).amax(1)
+    tol = half_step(q_dtype) * o.abs() + a * (half_step(F16) + 2 * ds[:, None] + 2.0 ** -19 + n * 2.0 ** -24)
+    tol = tol + (n * 448 * 2.0 ** -32 * largest)[:, None] + torch.finfo(q_dtype).smallest_normal * half_step(q_dtype)
+    assert ((out - o).abs() <= tol).all(), float(((out - o).abs() / tol).max())
+
+
+@pytest.mark.parametrize("q_dtype", [F16, BF16])
+def test_value_scales_at_both_ends_of_fp32(ops, q_dtype):
+    """Positions of zeros (the least scale), of tiny and of huge scales in one sequence, in units of their own and
+    mixed: the result is the huge ones' sum, or the tiny ones' where there are no others, and always finite."""
+    n = 96
+    for scales in ([2.0 ** -126] * 96, [2.0 ** -100] * 96, [2.0 ** -126] * 64 + [1.0] * 32, [2.0 ** 100] * 32 + [2.0 ** -100] * 64,
+                   [2.0 ** (5 * (i % 40) - 100) for i in range(96)]):
+        c, q = run([n], (4, 1), 64, 16, E4M3, q_dtype, seed=43)
+        for p, f in enumerate(scales):
+            was = float(c.scales["v_scale"][c.table[0, p // 16], 0, p % 16])
+            c.scales["v_scale"][c.table[0, p // 16], 0, p % 16] = f
+            c.kv[1][0][p] *= f / was
+        out = paged(ops, q, c)[0].double().cpu()
+        o, a, ds, _ = attend64(q[0].double().cpu(), c.kv[0][0], c.kv[1][0], 64 ** -0.5)
+        p = torch.softmax(torch.einsum("hd,nd->hn", q[0].double().cpu(), c.kv[0][0][:, 0]) * 64 ** -0.5, 1)
+        largest = (p * torch.tensor(scales, dtype=torch.float64)).amax(1)[:, None]
+        tol = half_step(q_dtype) * o.abs() + a * (half_step(F16) + 2 * ds[:, None] + 2.0 ** -19 + n * 2.0 ** -24)
+        tol = tol + n * 448 * 2.0 ** -32 * largest + torch.finfo(q_dtype).smallest_normal * half_step(q_dtype) * 2
+        big = o.abs() > torch.finfo(q_dtype).max  # (what the result's type cannot hold becomes an infinity)
+        assert torch.isinf(out[big]).all()
+        assert ((out - o).abs() <= tol)[~big].all(), (scales[0], float(((out - o).abs() / tol)[~big].max()))
