@@ -142,7 +142,10 @@ struct adp_model {
   int alloc(T** ptr, size_t count) {
     void* q = nullptr;
     cudaError_t e = cudaMalloc(&q, std::max<size_t>(count * sizeof(T), 16));
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc");
+    if (e != cudaSuccess) {
+      cudaGetLastError();  // told here: the next launch's check must not find it
+      return cuda_fail(e, "cudaMalloc");
+    }
     allocs.push_back(q);
     *ptr = static_cast<T*>(q);
     return ADP_OK;

@@ -161,3 +161,18 @@ def test_misaligned_logits_are_refused(lib):
     assert (room[:4] == 0).all() and room[4:].any()
     assert torch.equal(room[4:], cache.forward([[0]], [[1]], [1])[0])
     model.close()
+
+
+def test_an_allocation_that_failed_is_reported_once(lib):
+    """The runtime's error of a failed allocation (2 TB of residual rows) is not taken for one of the next launches."""
+    from autoregressive_decode_persistent_gb300.model import DecodeModel, PagedCache
+    cfg = synth.get_config("tiny")
+    model = DecodeModel(cfg, synth.model_weights(cfg))
+    cache = PagedCache(model, 4, 16)
+    small = dict(table=[[0], [1]], tokens=[[5, 6, 7], [1]], lens=[3, 1])
+    first = cache.forward(**small).clone()
+    with pytest.raises(lib.AdpError) as e:
+        lib.adp_debug_tc_gemm_time(model.handle, 0, 2 ** 31 - 1, 1)
+    assert e.value.code == lib.ADP_ERR_CUDA and "out of memory" in str(e.value)
+    assert torch.equal(cache.forward(**small), first)
+    model.close()
