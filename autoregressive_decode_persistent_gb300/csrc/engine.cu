@@ -17,6 +17,7 @@
 #include <vector>
 
 #include "../../include/adp.h"
+#include "grow.h"
 #include "launch.h"
 #include "plan.h"
 #include "scratch.h"
@@ -109,11 +110,10 @@ struct adp_model {
   // Packed rows over a paged cache (adp_paged_forward): the LM head as GEMM operand tiles, and scratch that grows.
   struct PagedFwd {
     uint8_t* lm = nullptr;
-    int32_t *ints = nullptr, *status = nullptr;
-    float* xs = nullptr;
-    uint16_t *q = nullptr, *o = nullptr, *k = nullptr, *v = nullptr;
-    uint8_t* work = nullptr;
-    size_t n_ints = 0, n_xs = 0, n_q = 0, n_k = 0, n_work = 0;  // capacities
+    Grown<int32_t> ints, status;
+    Grown<float> xs;
+    Grown<uint16_t> q, o, k, v;
+    Grown<uint8_t> work;
   } pf;
   // Batched decode (set up at the first batched call): per-request buffers for kMaxBatch
   // requests, the per-request step state and KV cache tables, and the shared-memory layout of
@@ -1381,18 +1381,15 @@ extern "C" int adp_prefill_tc(adp_model* m, adp_kv* kv, const int32_t* host_toke
 
 // A scratch buffer of at least n elements (the old one is freed behind the work that uses it).
 template <class T>
-static int reserve(adp_model* m, T** buf, size_t* cap, size_t n) {
-  if (n <= *cap) return ADP_OK;
-  if (*buf) {
-    CK(cudaStreamSynchronize(m->stream));
-    m->allocs.erase(std::remove(m->allocs.begin(), m->allocs.end(), (void*)*buf), m->allocs.end());
-    cudaFree(*buf);
-    *buf = nullptr;
-    *cap = 0;
-  }
-  const int rc = m->alloc(buf, n);
-  if (rc == ADP_OK) *cap = n;
-  return rc;
+static int reserve(adp_model* m, Grown<T>* buf, size_t n) {
+  return grow(
+      buf, n, [&](T** p, size_t count) { return m->alloc(p, count); },
+      [&](T* p) -> int {
+        CK(cudaStreamSynchronize(m->stream));
+        m->allocs.erase(std::remove(m->allocs.begin(), m->allocs.end(), (void*)p), m->allocs.end());
+        cudaFree(p);
+        return ADP_OK;
+      });
 }
 
 extern "C" int adp_paged_forward(adp_model* m, const adp_paged_kv* layers, const int32_t* host_tokens,
@@ -1460,12 +1457,10 @@ extern "C" int adp_paged_forward(adp_model* m, const adp_paged_kv* layers, const
     if ((rc = adp_paged_attention_workspace(&kv, c.n_heads, &need))) return rc;
     work = std::max(work, need);
   }
-  size_t one = F.status ? 1 : 0, o_cap = F.n_q, v_cap = F.n_k;
   const size_t qn = (size_t)P * c.n_heads * c.head_dim, kn = single ? 0 : (size_t)keys * c.n_kv_heads * c.head_dim;
-  if ((rc = reserve(m, &F.status, &one, 1)) || (rc = reserve(m, &F.ints, &F.n_ints, ints.size())) ||
-      (rc = reserve(m, &F.xs, &F.n_xs, (size_t)nb * c.d_model)) || (rc = reserve(m, &F.o, &o_cap, qn)) ||
-      (rc = reserve(m, &F.q, &F.n_q, qn)) || (rc = reserve(m, &F.v, &v_cap, kn)) || (rc = reserve(m, &F.k, &F.n_k, kn)) ||
-      (rc = reserve(m, &F.work, &F.n_work, (size_t)work)))
+  if ((rc = reserve(m, &F.status, 1)) || (rc = reserve(m, &F.ints, ints.size())) ||
+      (rc = reserve(m, &F.xs, (size_t)nb * c.d_model)) || (rc = reserve(m, &F.o, qn)) || (rc = reserve(m, &F.q, qn)) ||
+      (rc = reserve(m, &F.v, kn)) || (rc = reserve(m, &F.k, kn)) || (rc = reserve(m, &F.work, (size_t)work)))
     return rc;
   CK(cudaMemcpyAsync(F.ints, ints.data(), ints.size() * 4, cudaMemcpyHostToDevice, m->stream));
   CK(cudaMemsetAsync(F.status, 0, 4, m->stream));
@@ -1519,7 +1514,7 @@ extern "C" int adp_paged_forward(adp_model* m, const adp_paged_kv* layers, const
   a.kbuf = F.k;
   a.vbuf = F.v;
   a.work = F.work;
-  a.work_bytes = F.n_work;
+  a.work_bytes = F.work.n;
   a.logits = dev_logits;
   a.status = F.status;
   a.err = m->p.err;

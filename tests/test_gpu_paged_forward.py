@@ -176,3 +176,21 @@ def test_an_allocation_that_failed_is_reported_once(lib):
     assert e.value.code == lib.ADP_ERR_CUDA and "out of memory" in str(e.value)
     assert torch.equal(cache.forward(**small), first)
     model.close()
+
+
+def test_scratch_that_could_not_grow_leaves_the_model_working(lib):
+    """A pass whose gathered contexts would take 550 GB is refused by the allocator; the passes behind it run as before."""
+    from autoregressive_decode_persistent_gb300.model import DecodeModel, PagedCache
+    cfg = synth.shrink(synth.get_config("dense-2.3b-fp16"), head_dim=128, n_kv_heads=8, n_heads=8, max_ctx=32768)
+    model = DecodeModel(cfg, synth.model_weights(cfg))
+    cache = PagedCache(model, 4, 1024)
+    small = dict(table=[[0], [1]], tokens=[[5, 6, 7], []], lens=[3, 0])
+    first = cache.forward(**small).clone()
+    n = 8192
+    for _ in range(2):
+        with pytest.raises(lib.AdpError) as e:
+            cache.forward(np.zeros((n, 32), dtype=np.int32), [[1]] + [[]] * (n - 1), [32768] * n)
+        assert e.value.code == lib.ADP_ERR_CUDA and "out of memory" in str(e.value)
+        for _ in range(2):
+            assert torch.equal(cache.forward(**small), first)
+    model.close()
