@@ -1400,10 +1400,17 @@ extern "C" int adp_paged_forward(adp_model* m, const adp_paged_kv* layers, const
   const adp_config& c = m->cfg;
   const int nb = layers[0].n_seqs;
   if (nb < 1 || nb > 8192 || host_cu_rows[0] != 0) return ADP_ERR_INVALID_ARG;
+  int rc;
+  uint64_t work = 0;  // of attention of single tokens
   for (int l = 0; l < c.n_layers; ++l) {
-    const adp_paged_kv& kv = layers[l];
+    adp_paged_kv kv = layers[l];
     if (kv.n_seqs != nb || kv.n_kv_heads != c.n_kv_heads || kv.head_dim != c.head_dim) return ADP_ERR_INVALID_ARG;
     if (kv.dtype != c.kv_dtype && kv.dtype != ADP_E4M3) return ADP_ERR_UNSUPPORTED_CONFIG;
+    // every layer's description is checked before the first layer's pages are written
+    uint64_t need = 0;
+    kv.lens = kv.table;  // (not the caller's, and not read)
+    if ((rc = adp_paged_attention_workspace(&kv, c.n_heads, &need))) return rc;
+    work = std::max(work, need);
   }
   bool single = true;
   int64_t keys = 0;
@@ -1421,8 +1428,7 @@ extern "C" int adp_paged_forward(adp_model* m, const adp_paged_kv* layers, const
   for (int i = 0; i < P; ++i)
     if (host_tokens[i] < 0 || host_tokens[i] >= c.vocab) return ADP_ERR_INVALID_ARG;
   if (tc_operand_bf16(c) != (c.kv_dtype == ADP_BF16 ? 1 : 0)) return ADP_ERR_UNSUPPORTED_CONFIG;
-  int rc = tc_init(m);
-  if (rc || (rc = tc_reserve(m, std::max(P, nb)))) return rc;
+  if ((rc = tc_init(m)) || (rc = tc_reserve(m, std::max(P, nb)))) return rc;
   adp_model::PagedFwd& F = m->pf;
   if (!F.lm) {
     uint8_t* lm = nullptr;
@@ -1449,14 +1455,7 @@ extern "C" int adp_paged_forward(adp_model* m, const adp_paged_kv* layers, const
     last[s] = host_cu_rows[s + 1] > host_cu_rows[s] ? host_cu_rows[s + 1] - 1 : -1;
   }
   cu[nb] = P;
-  uint64_t work = 0;
-  for (int l = 0; single && l < c.n_layers; ++l) {
-    uint64_t need = 0;
-    adp_paged_kv kv = layers[l];
-    kv.lens = kv.table;  // (only its shape counts here)
-    if ((rc = adp_paged_attention_workspace(&kv, c.n_heads, &need))) return rc;
-    work = std::max(work, need);
-  }
+  if (!single) work = 0;
   const size_t qn = (size_t)P * c.n_heads * c.head_dim, kn = single ? 0 : (size_t)keys * c.n_kv_heads * c.head_dim;
   if ((rc = reserve(m, &F.status, 1)) || (rc = reserve(m, &F.ints, ints.size())) ||
       (rc = reserve(m, &F.xs, (size_t)nb * c.d_model)) || (rc = reserve(m, &F.o, qn)) || (rc = reserve(m, &F.q, qn)) ||

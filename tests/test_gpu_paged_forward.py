@@ -194,3 +194,41 @@ def test_scratch_that_could_not_grow_leaves_the_model_working(lib):
         for _ in range(2):
             assert torch.equal(cache.forward(**small), first)
     model.close()
+
+
+def test_a_wrong_later_layer_is_refused_before_anything_is_written(lib):
+    from autoregressive_decode_persistent_gb300.model import DecodeModel, PagedCache
+    cfg = synth.get_config("tiny")
+    model = DecodeModel(cfg, synth.model_weights(cfg))
+    cache = PagedCache(model, 4, 16)
+    table = torch.tensor([[0], [1]], dtype=torch.int32, device="cuda")
+    logits = torch.empty((2, cfg["vocab"]), device="cuda")
+    hkv, hd = cfg["n_kv_heads"], cfg["head_dim"]
+
+    def layers(**last):
+        out = (lib.PagedKV * cfg["n_layers"])()
+        for i in range(cfg["n_layers"]):
+            f = dict(k=cache.k[i].data_ptr(), v=cache.v[i].data_ptr(), table=table.data_ptr(), lens=None,
+                     page_stride=hkv * 16 * hd, scale_stride=0, n_pages=4, page_size=16, n_kv_heads=hkv, head_dim=hd,
+                     dtype=lib.DTYPES[cfg["kv_dtype"]], n_seqs=2, table_width=1)
+            f.update(last if i + 1 == cfg["n_layers"] else {})
+            for k, x in f.items():
+                setattr(out[i], k, x)
+        return out
+
+    torch.cuda.synchronize()
+    for tokens, cu in (([1, 2, 3], [0, 2, 3]), ([1, 2], [0, 1, 2])):  # prompts, single tokens
+        lens = [cu[1], cu[2] - cu[1]]
+        for wrong, code in ((dict(k=None), -1), (dict(v=cache.v[-1].data_ptr() + 8), -1), (dict(table=None), -1),
+                            (dict(page_stride=hkv * 16 * hd - 8), -1), (dict(n_pages=0), -1), (dict(page_size=24), -2),
+                            (dict(dtype=lib.ADP_E4M3), -1), (dict(n_seqs=1), -1)):
+            with pytest.raises(lib.AdpError) as e:
+                lib.adp_paged_forward(model.handle, layers(**wrong), tokens, cu, lens, logits)
+            assert e.value.code == code, wrong
+            torch.cuda.synchronize()
+            assert not cache.k.any() and not cache.v.any()
+        lib.adp_paged_forward(model.handle, layers(), tokens, cu, lens, logits)
+        assert cache.k.any() and torch.isfinite(logits).all()
+        cache.k.zero_(), cache.v.zero_()
+        torch.cuda.synchronize()
+    model.close()
