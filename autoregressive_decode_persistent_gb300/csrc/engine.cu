@@ -1520,7 +1520,7 @@ extern "C" int adp_paged_forward(adp_model* m, const adp_paged_kv* layers, const
   a.wait_ns = std::max<uint64_t>(m->p.wait_ns, 1000000000ull);
   if ((rc = tc_paged(a, m->stream))) {
     cudaStreamSynchronize(m->stream);
-    return rc == ADP_ERR_CUDA ? cuda_fail(cudaGetLastError(), "adp_paged_forward") : rc;
+    return rc;
   }
   int32_t status = 0;
   CK(cudaMemcpyAsync(&status, F.status, 4, cudaMemcpyDeviceToHost, m->stream));

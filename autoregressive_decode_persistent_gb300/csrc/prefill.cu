@@ -22,6 +22,7 @@
 #include <algorithm>
 
 #include "launch.h"
+#include "paged.cuh"
 #include "tc.cuh"
 
 namespace adp {
@@ -935,9 +936,9 @@ __global__ void tc_last_rows_kernel(const float* __restrict__ x, const int32_t* 
 int tc_paged(const TcPaged& a, cudaStream_t st) {
   const int P = a.P, qkv_n = (a.hq + 2 * a.hkv) * a.hd;
   const int kt_d = (a.d + kTcBK - 1) / kTcBK, kt_ff = (a.ff + kTcBK - 1) / kTcBK;
-#define TC_OK(call)                                \
-  do {                                             \
-    if ((call) != cudaSuccess) return ADP_ERR_CUDA; \
+#define TC_OK(call)                                                         \
+  do {                                                                      \
+    if (const int rc_ = cuda_status((call), "adp_paged_forward")) return rc_; \
   } while (0)
   tc_embed_kernel<<<P, 256, 0, st>>>(a.tokens, (const uint16_t*)a.tok_emb, a.d, a.bf16, a.x);
   TC_OK(cudaGetLastError());
