@@ -118,12 +118,16 @@ def paged_kv_read(k_pages, v_pages, table, lens, cu_rows, n_rows: int, *, dtype=
     if out is None:
         if dtype is None:
             dtype = torch.float16 if k_pages.dtype is torch.float8_e4m3fn else k_pages.dtype
+        if len(k_pages.shape) != 4 or n_rows < 0 or dtype not in _ROWS:
+            _refuse("paged_kv_read", "pages [pages, kv_heads, page_size, head_dim] are read as n_rows >= 0 rows of f16, bf16 or f32")
         _, heads, _, hd = k_pages.shape
         like = dict(dtype=dtype, device=k_pages.device)
         k, v = out = torch.empty((n_rows, heads, hd), **like), torch.empty((n_rows, heads, hd), **like)
     else:
+        if len(out) != 2:
+            _refuse("paged_kv_read", "out must be (k, v)")
         k, v = out
-        if k.shape[0] != n_rows or (dtype is not None and k.dtype is not dtype):
+        if len(k.shape) != 3 or k.shape[0] != n_rows or (dtype is not None and k.dtype is not dtype):
             _refuse("paged_kv_read", "out must hold n_rows rows of dtype")
     _transfer("paged_kv_read", k_pages, v_pages, table, lens, cu_rows, k, v, k_scale, v_scale, status)
     return out
@@ -133,10 +137,11 @@ def _transfer(where, k_pages, v_pages, table, lens, cu_rows, k, v, k_scale, v_sc
     device = k_pages.get_device()
     kv = _paged(where, k_pages, v_pages, table, lens, k_scale, v_scale, device)
     cu = _indices(where, "cu_rows", cu_rows, kv.n_seqs + 1, device)
-    dtype, n = k.dtype, k.shape[0]
+    dtype, shape = k.dtype, k.shape
     dt = _ROWS.get(dtype)
-    if dt is None:
-        _refuse(where, "k and v rows must be of f16, bf16 or f32")
+    if dt is None or len(shape) != 3:
+        _refuse(where, "k and v rows must be [rows, kv_heads, head_dim] of f16, bf16 or f32")
+    n = shape[0]
     shape = (n, kv.n_kv_heads, kv.head_dim)
     ks, vs = _rows(where, "k", k, shape, dtype, device), _rows(where, "v", v, shape, dtype, device)
     _call(device, "adp_" + where, kv, k.data_ptr(), v.data_ptr(), dt, ks, vs, cu, n, _status(where, status, device))
@@ -153,7 +158,7 @@ def paged_attention(q, k_pages, v_pages, table, lens, *, scale: float | None = N
     kv = _paged(where, k_pages, v_pages, table, lens, k_scale, v_scale, device)
     dtype, shape = q.dtype, q.shape
     dt = _HALF.get(dtype)
-    if dt is None or len(shape) != 3 or shape[0] != kv.n_seqs or shape[2] != kv.head_dim:
+    if dt is None or len(shape) != 3 or shape[0] != kv.n_seqs or shape[2] != kv.head_dim or shape[2] < 1:
         _refuse(where, "q must be [seqs, heads, head_dim] of f16 or bf16")
     qs = _rows(where, "q", q, shape, dtype, device)
     if out is None:
@@ -192,7 +197,7 @@ def packed_attention(q, k, v, cu_q, cu_k, *, scale: float | None = None, out=Non
     n_q, heads, hd = shape
     n_k, kv_heads, kd = kv_shape
     dt = _HALF.get(dtype)
-    if dt is None or kd != hd:
+    if dt is None or kd != hd or hd < 1:
         _refuse(where, "q, k and v must be of f16 or bf16, with one head_dim")
     qs = _rows(where, "q", q, shape, dtype, device)
     ks, vs = _rows(where, "k", k, kv_shape, dtype, device), _rows(where, "v", v, kv_shape, dtype, device)

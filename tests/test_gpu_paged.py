@@ -623,3 +623,34 @@ def test_value_scales_at_both_ends_of_fp32(ops, q_dtype):
         big = o.abs() > torch.finfo(q_dtype).max  # (what the result's type cannot hold becomes an infinity)
         assert torch.isinf(out[big]).all()
         assert ((out - o).abs() <= tol)[~big].all(), (scales[0], float(((out - o).abs() / tol)[~big].max()))
+
+
+def test_ranks_and_empty_heads_are_refused(ops):
+    from autoregressive_decode_persistent_gb300 import adp
+    c = Cache([5], 2, 64, 16, F16, 1)
+    cu = torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+    rows = torch.zeros(5, 2, 64, dtype=F16, device="cuda")
+    none = torch.zeros(3, 2, 16, 0, dtype=F16, device="cuda")
+    q = torch.zeros(1, 2, 0, dtype=F16, device="cuda")
+    for call in (lambda: ops.paged_kv_write(c.k, c.v, c.table, c.len_t, cu, rows[0, 0, 0], rows),
+                 lambda: ops.paged_kv_write(c.k, c.v, c.table, c.len_t, cu, rows[0], rows[0]),
+                 lambda: ops.paged_kv_write(c.k, c.v, c.table, c.len_t, cu, rows, rows[:, :1]),
+                 lambda: ops.paged_attention(rows[0], c.k, c.v, c.table, c.len_t),
+                 lambda: ops.paged_attention(q, none, none, c.table, c.len_t),
+                 lambda: ops.packed_attention(q, q, q, cu, cu),
+                 lambda: ops.packed_attention(rows, rows[0], rows, cu, cu)):
+        with pytest.raises(adp.AdpError) as e:
+            call()
+        assert e.value.code == adp.ADP_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("q_dtype", [F16, BF16])
+def test_a_quantised_row_with_a_non_finite_value_makes_the_attention_nan(ops, q_dtype):
+    c, q = run([40], (4, 2), 64, 16, E4M3, q_dtype, seed=45)
+    x = torch.randn(1, 2, 64, device="cuda")
+    for which in (0, 1):  # K, V of the last position, head 0
+        k, v = x.clone(), x.clone()
+        (k, v)[which][0, 0, 9] = math.inf
+        ops.paged_kv_write(c.k, c.v, c.table, c.len_t, torch.tensor([0, 1], dtype=torch.int32, device="cuda"), k, v, **c.scales)
+        out = paged(ops, q, c)
+        assert torch.isnan(out[0, :2]).all() and torch.isfinite(out[0, 2:]).all()

@@ -170,3 +170,16 @@ def test_rows_that_no_offsets_hold(tmp_path):
             rows = range(cu[b], cu[b + 1]) if cu[b] >= 0 and (b > 0 or cu[0] == 0) else ()
             for i in list(range(70)) + [2 ** 31 - 2, 2 ** 31 - 1]:
                 assert bool(L.t_holds(b, cu[b], cu[b + 1], i)) == (i in rows)
+
+
+def test_shapes_that_name_no_rows_are_refused():
+    import torch
+    from autoregressive_decode_persistent_gb300 import adp, ops
+    pages, table, lens = torch.zeros(2, 1, 16, 64, dtype=torch.float16), torch.zeros(1, 1, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    cu, rows = torch.tensor([0, 1], dtype=torch.int32), torch.zeros(1, 1, 64, dtype=torch.float16)
+    for bad, n, more in ((pages[0], 1, {}), (pages[0, 0, 0, 0], 1, {}), (pages, -1, {}), (pages, 1, dict(dtype=torch.int32)),
+                         (pages, 1, dict(out=(rows,))), (pages, 1, dict(out=(rows, rows, rows))), (pages, 2, dict(out=(rows, rows))),
+                         (pages, 1, dict(out=(rows[0, 0, 0], rows))), (pages, 1, dict(out=(rows, rows), dtype=torch.float32))):
+        with pytest.raises(adp.AdpError) as e:
+            ops.paged_kv_read(bad, bad, table, lens, cu, n, **more)
+        assert e.value.code == adp.ADP_ERR_INVALID_ARG
