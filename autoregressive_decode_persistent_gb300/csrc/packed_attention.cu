@@ -16,7 +16,6 @@ namespace {
 constexpr int kRows = 128;            // rows of a query tile (M of the MMA)
 constexpr int kKeys = 64;             // keys of a block
 constexpr int kThreads = 384;         // 8 softmax warps, the copying and the issuing warp, two idle ones
-constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kRescale = 8.0f;      // base-2 growth of a row's maximum that rescales its output
 
 struct PackedArgs {
@@ -28,6 +27,7 @@ struct PackedArgs {
   int32_t n_seqs, n_q, n_k, hkv, group, tok;
   float scale_log2;              // of |scale|, and above 0
   int32_t* status;
+  uint64_t wait_ns;              // limit of every wait
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -52,6 +52,10 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// The limit of a wait lies 12 bytes behind the abort word in shared memory (8,192 tokens: 0.7% more time than a constant; as an
+// argument of every wait 1.1%).
+__device__ __forceinline__ uint64_t wait_limit(volatile int32_t* abort) { return *reinterpret_cast<volatile uint64_t*>(abort + 3); }
+
 // A whole warp's wait with one answer for all of it.  What is not over at the first look is waited for in a function of
 // its own: between the warps of different roles the instruction caches hold little, and a long wait loop in line cost
 // 200 cycles even when there was nothing to wait for.
@@ -59,7 +63,7 @@ __device__ __noinline__ bool mbar_wait_warp_slow(uint64_t* b, uint32_t parity, v
   const uint64_t t0 = globaltimer();
   for (uint32_t it = 1;; ++it) {
     if (__all_sync(0xFFFFFFFFu, mbar_try_wait(b, parity))) return true;
-    if ((it & 63) == 0 && __any_sync(0xFFFFFFFFu, *abort != 0 || globaltimer() - t0 > kWaitNs)) return false;
+    if ((it & 63) == 0 && __any_sync(0xFFFFFFFFu, *abort != 0 || globaltimer() - t0 > wait_limit(abort))) return false;
   }
 }
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* b, uint32_t parity, volatile int32_t* abort) {
@@ -250,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(done, 2);
     *ab = 0;
     *bad = 0;
+    *reinterpret_cast<uint64_t*>(ctl + 4) = a.wait_ns;
     mbar_fence_init();
   }
   if (warp == 9) {
@@ -303,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         fence_async_smem();  // the answer has been read before the next one is written
       }
-      if (told < asked) mbar_wait(taken, told & 1, &never, kWaitNs);  // no answer may arrive behind the CTA's end
+      if (told < asked) mbar_wait(taken, told & 1, &never, a.wait_ns);  // no answer may arrive behind the CTA's end
     } else if (warp == 8) {
       if (lane == 0) {
         const uint32_t qbytes = (uint32_t)(a.tok * a.group) * 128 * (HD / 64);
@@ -311,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         auto block = [&](const Item& w, int j) {
           const int s = g % NS;
-          if (g >= NS && !mbar_wait(&empty[s], (g / NS - 1) & 1, ab, kWaitNs)) return false;
+          if (g >= NS && !mbar_wait(&empty[s], (g / NS - 1) & 1, ab, a.wait_ns)) return false;
           mbar_arrive_expect_tx(&full[s], L::kPair);
           for (int c = 0; c < 2 * (HD / 64); ++c)
             tma_load_3d(ring + s * L::kPair + c * L::kBlock, c < HD / 64 ? &mk : &mv, c % (HD / 64) * 64, w.h, w.k0 + j * kKeys, &full[s]);
@@ -320,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         for (int it = 0; ok; ++it) {
           const int s = it % kItems;
-          if (!(ok = mbar_wait(&ifull[s], (it / kItems) & 1, ab, kWaitNs))) break;
+          if (!(ok = mbar_wait(&ifull[s], (it / kItems) & 1, ab, a.wait_ns))) break;
           const Item w = items[s];
           mbar_arrive(&iempty[s]);
           if (w.stop) break;
@@ -330,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (j > 0) continue;
             for (int t = 0; ok && t < 2; ++t) {
               if ((t ? n1 : n0) == 0) continue;
-              if (nq[t] > 0 && !(ok = mbar_wait(&qempty[t], (nq[t] - 1) & 1, ab, kWaitNs))) break;
+              if (nq[t] > 0 && !(ok = mbar_wait(&qempty[t], (nq[t] - 1) & 1, ab, a.wait_ns))) break;
               mbar_arrive_expect_tx(&qfull[t], qbytes);
               for (int c = 0; c < HD / 64; ++c)
                 tma_load_3d(Qs + t * L::kQTile + c * L::kQBlock, &mq, c * 64, w.h * a.group, w.q0 + w.t0 + t * a.tok, &qfull[t]);
@@ -341,8 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) *ab = 1;
         // no copy may still be writing this CTA's shared memory when it exits
         for (int t = 0; t < 2; ++t)
-          if (nq[t] > 0) mbar_wait(&qfull[t], (nq[t] - 1) & 1, &never, kWaitNs);
-        for (int i = g > NS ? g - NS : 0; i < g; ++i) mbar_wait(&full[i % NS], (i / NS) & 1, &never, kWaitNs);
+          if (nq[t] > 0) mbar_wait(&qfull[t], (nq[t] - 1) & 1, &never, a.wait_ns);
+        for (int i = g > NS ? g - NS : 0; i < g; ++i) mbar_wait(&full[i % NS], (i / NS) & 1, &never, a.wait_ns);
       }
       __syncwarp();
     } else {
@@ -592,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = max(n0, n1);
       if (r == 0)  // the last two blocks, and (each once it is there) those that only the other tile sees
         for (int j = max(0, nk - 2); j < n; ++j) {
-          if (j >= nk && !mbar_wait(&full[(g + j) % NS], ((g + j) / NS) & 1, ab, kWaitNs)) *ab = 1;
+          if (j >= nk && !mbar_wait(&full[(g + j) % NS], ((g + j) / NS) & 1, ab, a.wait_ns)) *ab = 1;
           mbar_arrive(&empty[(g + j) % NS]);
         }
       g += n;
@@ -641,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   // no MMA may be in flight (nor TMEM in use) when the accumulators are freed
-  if (warp == 9) mbar_wait(done, 0, &never, kWaitNs);
+  if (warp == 9) mbar_wait(done, 0, &never, a.wait_ns);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -726,7 +731,7 @@ extern "C" int adp_packed_attention(const void* q, const void* k, const void* v,
                n_seqs, n_q, n_k, n_kv_heads, group, tok,
                // (a scale of 0 becomes the least normal number: the scores' differences vanish all the same, and what is
                // not seen stays at -infinity)
-               fmaxf(fabsf(scale) * 1.4426950408889634f, kScaleMin), dev_status};
+               fmaxf(fabsf(scale) * 1.4426950408889634f, kScaleMin), dev_status, packed_wait_ns(n_k, n_seqs)};
   const int64_t pairs = (int64_t)n_q / (2 * tok) + n_seqs;  // at most: every sequence may end inside a pair
   const int64_t grid = pairs * n_kv_heads;
   if (grid > 0x7FFFFFFF) return ADP_ERR_UNSUPPORTED_CONFIG;

@@ -50,4 +50,10 @@ ADP_INLINE int32_t split_parts(int64_t total, int32_t ctas) {
   return want < 1 ? 1 : (want > ctas ? ctas : (int32_t)want);
 }
 
+// How long a wait inside packed attention may take: some wait for a whole piece of work, which sees up to n_k keys (13 ns a
+// key, measured), and some for the search of the next one, which looks through up to n_seqs sequences (about 2 us for 32).
+ADP_INLINE uint64_t packed_wait_ns(int32_t n_k, int32_t n_seqs) {
+  return 1000000000ull + 100ull * (uint64_t)n_k + 1000ull * (uint64_t)n_seqs;
+}
+
 }  // namespace adp

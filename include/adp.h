@@ -432,7 +432,8 @@ int adp_paged_attention_workspace(const adp_paged_kv* kv, int32_t n_heads, uint6
  * Scores, softmax and sums are fp32; probabilities are rounded to dtype before they weigh V.  A query that sees
  * no key gives zeros.  Keys and values that a query does not see do not reach it, whatever they hold.  Offsets
  * that descend or lie outside [0, n_q] / [0, n_k] are cut to it and reported as ADP_ERR_INVALID_ARG; a wait
- * inside the kernel that ran out is reported as ADP_ERR_PIPELINE_TIMEOUT.  Needs no workspace. */
+ * inside the kernel that ran out (1 s and more, with the keys and sequences) is reported as ADP_ERR_PIPELINE_TIMEOUT, and
+ * leaves rows of out unset: only dev_status tells.  Needs no workspace. */
 int adp_packed_attention(const void* q, const void* k, const void* v, int32_t dtype, int32_t n_heads,
                          int32_t n_kv_heads, int32_t head_dim, int64_t q_stride, int64_t k_stride, int64_t v_stride,
                          const int32_t* cu_q, const int32_t* cu_k, int32_t n_seqs, int32_t n_q, int32_t n_k,

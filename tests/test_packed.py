@@ -43,3 +43,25 @@ def test_tensors_off_the_gpu_are_refused():
     x, cu = torch.zeros(4, 2, 64, dtype=torch.float16), torch.tensor([0, 4], dtype=torch.int32)
     with pytest.raises(adp.AdpError):
         ops.packed_attention(x, x, x, cu, cu)
+
+
+def test_the_wait_limit_grows_with_the_work(tmp_path):
+    """packed_wait_ns (csrc/paged.h): a wait may last for a whole piece of work, 13 ns a key, or for the search through
+    the sequences, under 100 ns each; a quarter of the limit holds either, beyond a second for everything else."""
+    import ctypes
+    import os
+    import subprocess
+    src, lib = tmp_path / "wait.cpp", tmp_path / "wait.so"
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "autoregressive_decode_persistent_gb300", "csrc")
+    src.write_text('#include "%s/paged.h"\nextern "C" uint64_t t_wait(int32_t k, int32_t s) { return adp::packed_wait_ns(k, s); }\n' % csrc)
+    subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", str(src), "-o", str(lib)], check=True)
+    wait = ctypes.CDLL(str(lib)).t_wait
+    wait.restype = ctypes.c_uint64
+    top = 2 ** 31 - 1
+    for keys in (0, 1, 8192, 10 ** 8, top):
+        for seqs in (0, 1, 8192, 10 ** 7, top):
+            assert wait(keys, seqs) >= 10 ** 9 + 4 * max(13 * keys, 100 * seqs)
+            assert wait(keys, seqs) <= wait(top, top) < 2 ** 43  # (and ends)
+    # the kernel takes its limits from there alone
+    text = open(os.path.join(csrc, "packed_attention.cu")).read()
+    assert "packed_wait_ns(n_k, n_seqs)" in text and "kWaitNs" not in text and "1000000000" not in text
