@@ -731,7 +731,7 @@ extern "C" int adp_packed_attention(const void* q, const void* k, const void* v,
                n_seqs, n_q, n_k, n_kv_heads, group, tok,
                // (a scale of 0 becomes the least normal number: the scores' differences vanish all the same, and what is
                // not seen stays at -infinity)
-               fmaxf(fabsf(scale) * 1.4426950408889634f, kScaleMin), dev_status, packed_wait_ns(n_k, n_seqs)};
+               fmaxf(log2_scale(fabsf(scale)), kScaleMin), dev_status, packed_wait_ns(n_k, n_seqs)};
   const int64_t pairs = (int64_t)n_q / (2 * tok) + n_seqs;  // at most: every sequence may end inside a pair
   const int64_t grid = pairs * n_kv_heads;
   if (grid > 0x7FFFFFFF) return ADP_ERR_UNSUPPORTED_CONFIG;

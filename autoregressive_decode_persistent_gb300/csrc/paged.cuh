@@ -52,6 +52,12 @@ inline int cuda_status(cudaError_t e, const char* where) {
   return ADP_ERR_CUDA;
 }
 
+// A finite scale for scores in base-2 exponents, kept finite: scores of 0 are 0 under the largest, too.
+inline float log2_scale(float scale) {
+  const float s = scale * 1.4426950408889634f;
+  return s > 3.40282347e38f ? 3.40282347e38f : s < -3.40282347e38f ? -3.40282347e38f : s;
+}
+
 // Checks of a cache's description that need no device, and the kernels' view of it.
 inline int paged_view(const adp_paged_kv* c, PagedView* out) {
   if (!c || !c->k || !c->v || (c->n_seqs > 0 && (!c->table || !c->lens))) return ADP_ERR_INVALID_ARG;

@@ -970,7 +970,7 @@ extern "C" int adp_paged_attention(const adp_paged_kv* kv, const void* q, int32_
   a.group = group;
   a.tiles = plan.tiles;
   a.cluster = plan.cluster;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = log2_scale(scale);
   if (plan.bytes) {
     a.partials = workspace;
     a.meta = reinterpret_cast<SplitMeta*>(static_cast<uint8_t*>(workspace) + plan.bytes - (size_t)ctas * sizeof(SplitMeta));

@@ -270,3 +270,11 @@ def test_a_dominating_key_leaves_the_others_their_weights(ops, hd):
     ds = bits * math.log(2) * (hd + 8) * 2.0 ** -24
     tol = o * (2 * half_step(F16) + 2 * ds + 2.0 ** -19 + lk[0] * 2.0 ** -24) + 2.0 ** -32 * v[:, 0].double().sum(0)
     assert ((out - o).abs() <= tol).all(), float(((out - o).abs() / tol).max())
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_a_scale_near_the_largest_float(ops, dtype):
+    """Scores of 0 stay 0 under any finite scale: the mean of the values."""
+    q, k, v = inputs([70], [70], (4, 2), 64, dtype, seed=21)
+    for scale in (3e38, -3e38):
+        check(ops.packed_attention(q * 0, k, v, cumulative([70]), cumulative([70]), scale=scale), q * 0, k, v, [70], [70], scale=scale)

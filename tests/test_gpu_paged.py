@@ -654,3 +654,11 @@ def test_a_quantised_row_with_a_non_finite_value_makes_the_attention_nan(ops, q_
         ops.paged_kv_write(c.k, c.v, c.table, c.len_t, torch.tensor([0, 1], dtype=torch.int32, device="cuda"), k, v, **c.scales)
         out = paged(ops, q, c)
         assert torch.isnan(out[0, :2]).all() and torch.isfinite(out[0, 2:]).all()
+
+
+@pytest.mark.parametrize("dtype,q_dtype", TYPES)
+def test_a_scale_near_the_largest_float(ops, dtype, q_dtype):
+    """Scores of 0 stay 0 under any finite scale: the mean of the values."""
+    for scale in (3e38, -3e38):
+        c, q = run([33], (4, 2), 64, 16, dtype, q_dtype, seed=44)
+        check_attention(paged(ops, q * 0, c, scale=scale), q * 0, c, scale=scale)
