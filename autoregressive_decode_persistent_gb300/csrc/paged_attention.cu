@@ -862,13 +862,18 @@ struct AttentionPlan {
 // of 8 (8 units a warp) 14.7 and 17.6; 57 x 500 of 8 18.5 and 21.0; the worst, 14 x 1,000 of 8, 17.8 and 16.3.
 constexpr int kClusterUnits = 8;
 
+// Units of a sequence that fills its table.
+int64_t full_units(const adp_paged_kv* kv) {
+  const int unit = 4096 / (kv->head_dim * elem_bytes(kv->dtype));
+  return ((int64_t)kv->table_width * kv->page_size + unit - 1) / unit;
+}
+
 AttentionPlan attention_plan(const adp_paged_kv* kv, int group, int sms) {
   AttentionPlan p{};
   p.nt = head_tiles(group);
   p.tiles = (group + p.nt * 8 - 1) / (p.nt * 8);
   const int resident = sms * (p.nt == 1 ? kResident<1> : kResident<2>);
-  const int unit = 4096 / (kv->head_dim * elem_bytes(kv->dtype));
-  const int64_t per_seq = ((int64_t)kv->table_width * kv->page_size + unit - 1) / unit;
+  const int64_t per_seq = full_units(kv);
   const int64_t segs = (int64_t)kv->n_seqs * kv->n_kv_heads * p.tiles;
   if (segs > 0 && segs <= resident) {
     int cs = 1;
@@ -926,6 +931,8 @@ int attention_check(const adp_paged_kv* kv, int32_t n_heads, PagedView* c) {
   if (rc) return rc;
   if (n_heads < 1 || n_heads % kv->n_kv_heads) return ADP_ERR_INVALID_ARG;
   if (n_heads > 4096 || kv->n_seqs > kPagedMaxSeqs) return ADP_ERR_UNSUPPORTED_CONFIG;
+  // (the units of 32 sequences are added in 32 bits)
+  if ((kv->n_seqs < 32 ? kv->n_seqs : 32) * full_units(kv) > 0x7FFFFFFF) return ADP_ERR_UNSUPPORTED_CONFIG;
   return ADP_OK;
 }
 

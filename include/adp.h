@@ -402,7 +402,7 @@ int adp_paged_kv_read(const adp_paged_kv* kv, void* k, void* v, int32_t rows_dty
  *  q, out      DEVICE [n_seqs][n_heads][head_dim] of q_dtype (ADP_F16 or ADP_BF16; the cache's own type
  *              where that is a 16-bit one), rows q_stride / out_stride elements apart (multiples of 8),
  *              16-byte aligned
- *  n_heads     a multiple of n_kv_heads, at most 4096; n_seqs at most 8192
+ *  n_heads     a multiple of n_kv_heads, at most 4096; n_seqs at most 8192; tables of less than 2^30 positions a sequence
  *  scale       finite
  *  workspace   DEVICE scratch of at least adp_paged_attention_workspace bytes, 16-byte aligned (may be NULL
  *              where that is 0); its contents do not matter.  Calls that may run at the same time need one each.

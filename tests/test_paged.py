@@ -183,3 +183,20 @@ def test_shapes_that_name_no_rows_are_refused():
         with pytest.raises(adp.AdpError) as e:
             ops.paged_kv_read(bad, bad, table, lens, cu, n, **more)
         assert e.value.code == adp.ADP_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("head_dim,dtype,unit", [(128, 0, 16), (64, 0, 32), (128, 2, 32), (64, 2, 64)])
+def test_tables_whose_units_do_not_fit_32_bits_are_refused(adp, head_dim, dtype, unit):
+    """32 sequences' units (`unit` positions each) are added in 32 bits."""
+    most = 2 ** 31 - 1024 - 1  # positions that a table may name at all
+    for n_seqs, width in ((1, 2 ** 21 - 2), (31, 2 ** 20), (32, 2 ** 20 - 1), (32, 2 ** 20), (32, 2 ** 20 + 1), (8192, 2 ** 21 - 2)):
+        assert width * 1024 <= most
+        kv = _kv(adp, n_seqs=n_seqs, table_width=width, page_size=1024, head_dim=head_dim, dtype=dtype,
+                 page_stride=4 * 1024 * head_dim, scale_stride=4 * 1024)
+        code = 0
+        try:
+            adp.adp_paged_attention_workspace(kv, 20)
+        except adp.AdpError as e:
+            code = e.code
+        fits = min(n_seqs, 32) * -(-width * 1024 // unit) < 2 ** 31
+        assert code in ((0, adp.ADP_ERR_CUDA) if fits else (adp.ADP_ERR_UNSUPPORTED_CONFIG,))  # (CUDA: no GPU here)
