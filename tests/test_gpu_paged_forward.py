@@ -232,3 +232,50 @@ def test_a_wrong_later_layer_is_refused_before_anything_is_written(lib):
         cache.k.zero_(), cache.v.zero_()
         torch.cuda.synchronize()
     model.close()
+
+
+def test_an_nvfp4_model_matches_the_oracle(lib):
+    from autoregressive_decode_persistent_gb300.model import DecodeModel, PagedCache
+    cfg = synth.shrink(synth.get_config("dense-2.3b-nvfp4"))
+    W = synth.model_weights(cfg)
+    rng = np.random.default_rng(8)
+    seqs = [rng.integers(0, cfg["vocab"], n).tolist() for n in (21, 6)]
+    refs = [oracle_forced(cfg, W, s)[0] for s in seqs]
+    model = DecodeModel(cfg, W)
+    table, n_pages = _tables([21, 6], 16)
+    cache = PagedCache(model, n_pages, 16)
+    for at in ([20, 5], [21, 6]):  # prompts, then one token each
+        tokens = [s[at[b] - 1:at[b]] if at == [21, 6] else s[:at[b]] for b, s in enumerate(seqs)]
+        logits = cache.forward(table, tokens, at).cpu().numpy()
+        for b in range(2):
+            _assert_close(cfg, logits[b:b + 1], refs[b][at[b] - 1:at[b]])
+    model.close()
+
+
+@pytest.mark.parametrize("name", ["tiny-f16", "8b-bf16"])
+def test_one_token_steps_over_a_quantised_cache(lib, name):
+    """Steps of single tokens over e4m3 pages (codes attended as they are) and the same steps beside a request without a new
+    row (every context read back to 16 bits, then attended as prompts) are two ways to one result: each is within the
+    stated tolerances of the other.  They differ by the 16-bit roundings that _assert_close counts, and by codes of the new
+    rows that these turn to a neighbour: a rounding u of the value crosses a border of codes (steps of 2^-3 of the value)
+    for a share of 2^4 u of the elements at most and then changes one by 2^-3; of one row among the contexts' 30 and more."""
+    from autoregressive_decode_persistent_gb300.model import DecodeModel, PagedCache
+    cfg = _shapes()[name]
+    model = DecodeModel(cfg, synth.model_weights(cfg))
+    rng = np.random.default_rng(9)
+    lens = [40, 31, 65]
+    seqs = [rng.integers(0, cfg["vocab"], n + 3).tolist() for n in lens]
+    table, n_pages = _tables([n + 3 for n in lens], 16)
+    idle = np.concatenate([table, np.full((1, table.shape[1]), -1, dtype=np.int32)])
+    caches = [PagedCache(model, n_pages, 16, torch.float8_e4m3fn) for _ in range(2)]
+    for c in caches:
+        c.forward(table, [s[:n] for s, n in zip(seqs, lens)], lens)
+    for step in range(3):
+        tokens = [[s[n + step]] for s, n in zip(seqs, lens)]
+        at = [n + step + 1 for n in lens]
+        alone = caches[0].forward(table, tokens, at).cpu().numpy()
+        beside = caches[1].forward(idle, tokens + [[]], at + [0]).cpu().numpy()
+        assert (beside[3] == 0).all()
+        _assert_close(cfg, alone, beside[:3])
+        assert np.abs(alone).max() > 0.1
+    model.close()
