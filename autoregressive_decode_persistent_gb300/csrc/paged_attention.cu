@@ -138,8 +138,9 @@ constexpr int kResident = NT == 1 ? 3 : 2;
 // free, and Q's is chosen alike), O^T = V^T P^T takes V's with the 16-bit halves of two keys interleaved.  With the
 // query heads as the 8-wide side a group of up to 8 heads costs one instruction per 16 x 16 of K; nothing is staged
 // in shared memory.  e4m3 codes become fp16 (exact), their scales multiply the scores and the probabilities.
-// Measured: 131,011 bf16 positions of 8 KV heads 91.5 us (5.9 TB/s), 64 ragged e4m3 sequences 89 us (5.1 TB/s; 87 with one unit
-// of O for a warp, the largest value scale: it took bits from the others whatever its own weight); with an
+// Measured: 131,011 bf16 positions of 8 KV heads 91.5 us (5.9 TB/s), 64 ragged e4m3 sequences 87 us (5.2 TB/s; the same
+// with one unit of O for a warp, the largest value scale, which took bits from the others whatever its own weight; head_dim 64
+// 65 us instead of 61); with an
 // L2 prefetch of one unit more 96 and 93.  The first form (8 warps, every load predicated, a maximum updated every unit)
 // took 124 us for the latter.
 template <int HD, int CDT, int QDT, int NT, bool SMALL>
@@ -490,22 +491,23 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
         }
         if (more) load_k(t + i + 1);
         // ---- scores in base-2 exponents; the running maxima are replaced only when some score (or e4m3's score + log2 of
-        // the value scale) exceeds its maximum by more than 8, decided per warp: till then the weights stay below 2^8, and
-        // the same stale maximum scales O and l alike
+        // the value scale, taken for the lane's largest score with its largest scale) exceeds its maximum by more than 8,
+        // decided per warp: till then the weights stay below 2^8, and the same stale maximum scales O and l alike
         bool need = false;
-        float lv[RG][2];
-        if constexpr (Q8) {  // (2^-126 is the least scale that a row is given: the logarithm is finite for 0, too)
+        auto log2_scale = [](float s) { return fmaxf(log2_fast(fabsf(s)), -126.0f); };  // (2^-126: the least one)
+        float lvtop = 0.0f;
+        if constexpr (Q8) {
+          float vtop = 0.0f;
 #pragma unroll
-          for (int g = 0; g < RG; ++g)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) lv[g][r] = fmaxf(log2_fast(fabsf(vs_now[g][r])), -126.0f);
+          for (int g = 0; g < RG; ++g) vtop = fmaxf(vtop, fmaxf(fabsf(vs_now[g][0]), fabsf(vs_now[g][1])));
+          lvtop = log2_scale(vtop);
         }
-        float top[NT][2], topo[NT][2];
+        float top[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            top[nt][j] = topo[nt][j] = -INFINITY;
+            top[nt][j] = -INFINITY;
 #pragma unroll
             for (int g = 0; g < RG; ++g)
 #pragma unroll
@@ -515,10 +517,9 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
                 if (!full) x = (on >> (2 * g + r)) & 1 ? x : -INFINITY;
                 s[g][nt][2 * r + j] = x;
                 top[nt][j] = fmaxf(top[nt][j], x);
-                if constexpr (Q8) topo[nt][j] = fmaxf(topo[nt][j], x + lv[g][r]);
               }
             need |= top[nt][j] > m[nt][j] + kStale;
-            if constexpr (Q8) need |= topo[nt][j] > mo[nt][j] + kStale;
+            if constexpr (Q8) need |= top[nt][j] + lvtop > mo[nt][j] + kStale;
           }
         }
         if (__any_sync(0xFFFFFFFFu, need)) {
@@ -534,7 +535,11 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
               m[nt][j] = mn;
               l[nt][j] *= f;
               if constexpr (Q8) {  // (both maxima at once: mo is m - 126 at least, and vc finite)
-                float mw = topo[nt][j];
+                float mw = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < RG; ++g)
+#pragma unroll
+                  for (int r = 0; r < 2; ++r) mw = fmaxf(mw, s[g][nt][2 * r + j] + log2_scale(vs_now[g][r]));
 #pragma unroll
                 for (int d = 4; d <= 16; d <<= 1) mw = fmaxf(mw, __shfl_xor_sync(0xFFFFFFFFu, mw, d));
                 mw = fmaxf(mo[nt][j], mw);
