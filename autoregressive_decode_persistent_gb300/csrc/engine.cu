@@ -1421,7 +1421,7 @@ extern "C" int adp_paged_forward(adp_model* m, const adp_paged_kv* layers, const
     for (int l = 0; l < c.n_layers; ++l)
       if ((int64_t)layers[l].table_width * layers[l].page_size < host_lens[s]) return ADP_ERR_CONTEXT_OVERFLOW;
     single = single && rows == 1;
-    keys += host_lens[s];
+    keys += rows ? host_lens[s] : 0;  // (a context that nothing attends to is not read)
   }
   const int P = host_cu_rows[nb];
   if (P < 1 || !host_tokens || keys > 0x7FFFFFFF) return ADP_ERR_INVALID_ARG;
@@ -1451,7 +1451,7 @@ extern "C" int adp_paged_forward(adp_model* m, const adp_paged_kv* layers, const
     for (int i = host_cu_rows[s]; i < host_cu_rows[s + 1]; ++i) pos[i] = host_lens[s] - (host_cu_rows[s + 1] - i);
     cu[s] = host_cu_rows[s];
     lens[s] = host_lens[s];
-    ck[s + 1] = ck[s] + host_lens[s];
+    ck[s + 1] = ck[s] + (host_cu_rows[s + 1] > host_cu_rows[s] ? host_lens[s] : 0);
     last[s] = host_cu_rows[s + 1] > host_cu_rows[s] ? host_cu_rows[s + 1] - 1 : -1;
   }
   cu[nb] = P;

@@ -105,7 +105,7 @@ cudaError_t tc_prefill(const TcPrefill& a, cudaStream_t st);
 struct TcPaged {
   int P, nb, n_layers, d, hq, hkv, hd, ff, vocab, bf16, kvdt;
   int single;                    // every sequence has one new row: attention of single tokens
-  int total_keys;                // sum of the lengths
+  int total_keys;                // sum of the lengths of the sequences with a new row
   float eps, scale;
   const int32_t *tokens, *pos, *cu_rows, *lens, *cu_keys, *last;  // device: [P], [P], [nb+1], [nb], [nb+1], [nb] (-1: none)
   const void* tok_emb;

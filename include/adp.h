@@ -445,8 +445,8 @@ int adp_packed_attention(const void* q, const void* k, const void* v, int32_t dt
  *  layers        HOST array [n_layers]: one layer each, all with the same n_seqs; n_kv_heads and head_dim of the
  *                model, dtype its kv_dtype or ADP_E4M3 (lens is not read: host_lens says them)
  *  host_tokens   HOST [rows]: the new tokens, sequence by sequence
- *  host_cu_rows  HOST [n_seqs + 1]: sequence s has rows host_cu_rows[s] .. host_cu_rows[s + 1] - 1 (possibly none), its
- *                last positions
+ *  host_cu_rows  HOST [n_seqs + 1]: sequence s has rows host_cu_rows[s] .. host_cu_rows[s + 1] - 1 (possibly none: its
+ *                pages are not read then), its last positions
  *  host_lens     HOST [n_seqs]: its length with the new rows, at most max_ctx
  *  dev_logits    DEVICE float [n_seqs][vocab], 16-byte aligned: the logits of each sequence's last new row (zeros where
  *                it has none)

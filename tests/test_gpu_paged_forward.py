@@ -189,7 +189,7 @@ def test_scratch_that_could_not_grow_leaves_the_model_working(lib):
     n = 8192
     for _ in range(2):
         with pytest.raises(lib.AdpError) as e:
-            cache.forward(np.zeros((n, 32), dtype=np.int32), [[1]] + [[]] * (n - 1), [32768] * n)
+            cache.forward(np.zeros((n, 32), dtype=np.int32), [[1, 2]] + [[3]] * (n - 1), [32768] * n)
         assert e.value.code == lib.ADP_ERR_CUDA and "out of memory" in str(e.value)
         for _ in range(2):
             assert torch.equal(cache.forward(**small), first)
@@ -278,4 +278,20 @@ def test_one_token_steps_over_a_quantised_cache(lib, name):
         assert (beside[3] == 0).all()
         _assert_close(cfg, alone, beside[:3])
         assert np.abs(alone).max() > 0.1
+    model.close()
+
+
+def test_a_request_without_a_new_row_is_not_read(lib):
+    """Its context may be anywhere (here: no page at all, so that reading it would be reported), and the others' logits are
+    what they are without it."""
+    from autoregressive_decode_persistent_gb300.model import DecodeModel, PagedCache
+    cfg = synth.get_config("tiny")
+    model = DecodeModel(cfg, synth.model_weights(cfg))
+    cache = PagedCache(model, 8, 16)
+    table = [[0, 1], [-1, -1], [2, 3]]
+    for tokens, lens in (([[1, 2, 3], [], [4]], [3, 30, 1]), ([[5], [], [6, 7]], [4, 32, 3])):
+        beside = cache.forward(table, tokens, lens).clone()
+        others = [[tokens[0], tokens[2]], [lens[0], lens[2]]]
+        assert torch.equal(beside[[0, 2]], cache.forward([table[0], table[2]], *others))
+        assert (beside[1] == 0).all() and beside[0].any()
     model.close()
