@@ -15,7 +15,7 @@ namespace {
 
 constexpr int kRows = 128;            // rows of a query tile (M of the MMA)
 constexpr int kKeys = 64;             // keys of a block
-constexpr int kThreads = 384;         // 8 softmax warps, the copying and the issuing warp, two idle ones
+constexpr int kThreads = 384;         // 8 softmax warps, one that copies, two that issue MMAs, one that finds the work
 constexpr float kRescale = 8.0f;      // base-2 growth of a row's maximum that rescales its output
 
 struct PackedArgs {
@@ -197,7 +197,7 @@ constexpr int kItems = 2;  // the item worked on and the next one: more known ah
 //  - a row's running maximum is replaced only when it grows by more than 2^8 (decided per warp): O and the sum carry the
 //    same stale factor, which cancels.
 // TMEM: S/P of A and B (2 x 64 columns each), O of A and B (HD columns each).
-// Bound by the softmax warps and the MMAs together: 8,192 bf16 tokens of 32 / 8 heads in 366 us (1,500 TFLOP/s; the
+// Bound by the softmax warps and the MMAs together: 8,192 bf16 tokens of 32 / 8 heads in 368 us (1,490 TFLOP/s; the
 // library's GEMM reaches 1,892).
 // Keys that a row does not see: their scores are replaced; their V must not meet the zero probabilities if it is not
 // finite, so blocks on the causal edge or the sequence's end are looked through in shared memory: rows behind the

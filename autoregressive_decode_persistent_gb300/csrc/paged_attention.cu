@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
 #pragma unroll
         for (int g = 0; g < RG; ++g) {
           // bf16's 8 bits would leave the weights' rounding as large as the result's: their remainder is weighed too
-          // (error against 64 bits of one 131,011-position bf16 row: 2.6e-3 without, the plain form's 1.8e-3 with it)
+          // (error against 64 bits of one 131,011-position bf16 row: 2.6e-3 without, the plain form's 1.6e-3 with it)
           uint32_t pf[NT][2], pl[NT][2];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {

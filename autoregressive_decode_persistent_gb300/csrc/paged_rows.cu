@@ -123,7 +123,7 @@ __device__ __forceinline__ void store_row8(uint8_t* p, const float (&x)[8]) {
 
 // Rows into pages (WRITE) or pages into rows, one warp per packed row.  Its K heads and then its V heads are one
 // line of 8-element pieces, a piece per lane, so that small rows fill a warp too.  Copying: bound by memory (73,361 bf16
-// rows of 8 x 128 read back in 92 us, 6.5 TB/s; 8 pieces in flight per lane instead of 4: the same, and 51 us instead of 47
+// rows of 8 x 128 read back in 92 us, 6.5 TB/s; 8 pieces in flight per lane instead of 4: the same, and 50 us instead of 47
 // for 34,360 rows quantised, 4.5 TB/s).
 // Quantising takes a row's absolute maximum over the HD / 8 lanes that hold it (NaN carried along), divides by
 // the scale max / 448 and rounds to the nearest code.

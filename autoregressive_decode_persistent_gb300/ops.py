@@ -152,7 +152,8 @@ def paged_attention(q, k_pages, v_pages, table, lens, *, scale: float | None = N
     """Attention of one new token per sequence, q [seqs, heads, head_dim] f16 or bf16, over its cached positions.
 
     scale: default 1 / sqrt(head_dim).  workspace: optional uint8 tensor of adp.adp_paged_attention_workspace
-    bytes (not shared by calls that may run at the same time); by default one is allocated on the current stream."""
+    bytes (not shared by calls that may run at the same time); by default one is allocated on the current stream.
+    The work is split by the table's width: a table no wider than the longest context is fastest."""
     where = "paged_attention"
     device = k_pages.get_device()
     kv = _paged(where, k_pages, v_pages, table, lens, k_scale, v_scale, device)
@@ -188,7 +189,8 @@ def packed_attention(q, k, v, cu_q, cu_k, *, scale: float | None = None, out=Non
 
     cu_q, cu_k: int32 [seqs + 1] row offsets; query i of a sequence with lq queries and lk keys sees keys up to
     i + lk - lq.  scale: default 1 / sqrt(head_dim).  Rows of q from cu_q[-1] on are padding: their rows of `out`
-    are left as they were (unset where out is allocated here)."""
+    are left as they were (unset where out is allocated here).  A wait inside the kernel that ran out (on a GPU that stood
+    still for a second) leaves rows unset, too: `status` tells."""
     where = "packed_attention"
     device = q.get_device()
     if not q.is_cuda or len(q.shape) != 3 or len(k.shape) != 3:

@@ -406,6 +406,8 @@ int adp_paged_kv_read(const adp_paged_kv* kv, void* k, void* v, int32_t rows_dty
  *  scale       finite
  *  workspace   DEVICE scratch of at least adp_paged_attention_workspace bytes, 16-byte aligned (may be NULL
  *              where that is 0); its contents do not matter.  Calls that may run at the same time need one each.
+ * How the work is split goes by the table's width, not by the lengths, which the host does not see: a table no wider than
+ * the longest context is fastest (few short sequences then take one launch and no workspace).
  * Scores, softmax and sums are fp32; before they weigh V, probabilities are rounded to two bf16 terms, or to fp16 (f16
  * caches; e4m3 caches: probability x value scale), to 11 bits down to 2^-21 of the largest and to a step of 2^-31 of it
  * below.  A sequence of length 0 gives zeros.  A position whose page number is outside the
@@ -450,7 +452,11 @@ int adp_packed_attention(const void* q, const void* k, const void* v, int32_t dt
  *  host_lens     HOST [n_seqs]: its length with the new rows, at most max_ctx
  *  dev_logits    DEVICE float [n_seqs][vocab], 16-byte aligned: the logits of each sequence's last new row (zeros where
  *                it has none)
- * Writes the new rows' K and V into their pages.  Like adp_prefill_tc it agrees with the oracle within the
+ * Writes the new rows' K and V into their pages.  Where every sequence has exactly one new row, adp_paged_attention
+ * attends over the pages.  Otherwise, single rows or not, the contexts of all sequences that have a new row are read back
+ * to 16 bits in every layer (scratch of 2 x 2 bytes x n_kv_heads x head_dim x the sum of their lengths) and attended to by
+ * adp_packed_attention: slower for the single rows, and over e4m3 pages scale x code is rounded to 16 bits first, so that a
+ * sequence's logits depend on the others' row counts within the tolerances.  Like adp_prefill_tc it agrees with the oracle within the
  * tolerances, not bit for bit (e4m3 pages add the cache's rounding).  head_dim 64 or 128 and a 16-bit operand
  * type equal to kv_dtype, else ADP_ERR_UNSUPPORTED_CONFIG.  Runs on the model's stream and synchronises it; scratch grows with
  * the most rows and keys seen.  Errors: as adp_prefill_tc, and what the operators report (ADP_ERR_INVALID_ARG: a
