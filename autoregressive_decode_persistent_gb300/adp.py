@@ -90,6 +90,11 @@ class PagedKV(ctypes.Structure):
                                                "table_width")]
 
 
+class Rope(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("n_positions", ctypes.c_int32), ("rotated", ctypes.c_int32),
+                ("q_gain", ctypes.c_void_p), ("k_gain", ctypes.c_void_p), ("gain_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
 _lib = None
 
 # (name, restype, argtypes)
@@ -154,11 +159,27 @@ _SIGS = [
     ("adp_paged_kv_read", ctypes.c_int, [ctypes.POINTER(PagedKV), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
                                          ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32,
                                          ctypes.c_void_p, ctypes.c_void_p]),
+    ("adp_paged_kv_append", ctypes.c_int, [ctypes.POINTER(PagedKV), ctypes.POINTER(Rope), ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64,
+                                           ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
+                                           ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p]),
     ("adp_paged_attention", ctypes.c_int, [ctypes.POINTER(PagedKV), ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
                                            ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_int64,
                                            ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p]),
     ("adp_paged_attention_workspace", ctypes.c_int, [ctypes.POINTER(PagedKV), ctypes.c_int32,
                                                      ctypes.POINTER(ctypes.c_uint64)]),
+    ("adp_paged_window_attention", ctypes.c_int, [ctypes.POINTER(PagedKV), ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                                  ctypes.c_int64, ctypes.c_float, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                                  ctypes.c_int64, ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p,
+                                                  ctypes.c_void_p]),
+    ("adp_paged_window_attention_workspace", ctypes.c_int, [ctypes.POINTER(PagedKV), ctypes.c_int32, ctypes.c_int32,
+                                                            ctypes.c_int32, ctypes.POINTER(ctypes.c_uint64)]),
+    ("adp_paged_chunk_attention", ctypes.c_int, [ctypes.POINTER(PagedKV), ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                                 ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_int32,
+                                                 ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                                 ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p]),
+    ("adp_paged_chunk_attention_workspace", ctypes.c_int, [ctypes.POINTER(PagedKV), ctypes.c_int32, ctypes.c_int32,
+                                                           ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(ctypes.c_uint64)]),
     ("adp_paged_forward", ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(PagedKV), ctypes.c_void_p, ctypes.c_void_p,
                                          ctypes.c_void_p, ctypes.c_void_p]),
     ("adp_packed_attention", ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
@@ -467,6 +488,13 @@ def adp_paged_kv_read(kv: PagedKV, k, v, rows_dtype: int, k_stride: int, v_strid
                                             _ptr(dev_status), stream), "adp_paged_kv_read")
 
 
+def adp_paged_kv_append(kv: PagedKV, rope: Rope, q, k, v, rows_dtype: int, n_heads: int, q_stride: int, k_stride: int, v_stride: int,
+                        cu_rows, n_rows: int, out, out_dtype: int, out_stride: int, dev_status=None, stream: int = 0):
+    _check(load_library().adp_paged_kv_append(kv, rope, _ptr(q), _ptr(k), _ptr(v), rows_dtype, n_heads, q_stride, k_stride,
+                                              v_stride, _ptr(cu_rows), n_rows, _ptr(out), out_dtype, out_stride,
+                                              _ptr(dev_status), stream), "adp_paged_kv_append")
+
+
 def adp_paged_attention_workspace(kv: PagedKV, n_heads: int) -> int:
     n = ctypes.c_uint64()
     _check(load_library().adp_paged_attention_workspace(kv, n_heads, ctypes.byref(n)), "adp_paged_attention_workspace")
@@ -478,6 +506,35 @@ def adp_paged_attention(kv: PagedKV, q, q_dtype: int, n_heads: int, q_stride: in
     _check(load_library().adp_paged_attention(kv, _ptr(q), q_dtype, n_heads, q_stride, scale, _ptr(out), out_stride,
                                               _ptr(workspace), workspace_bytes, _ptr(dev_status), stream),
            "adp_paged_attention")
+
+
+def adp_paged_window_attention_workspace(kv: PagedKV, n_heads: int, window: int, sinks: int) -> int:
+    n = ctypes.c_uint64()
+    _check(load_library().adp_paged_window_attention_workspace(kv, n_heads, window, sinks, ctypes.byref(n)),
+           "adp_paged_window_attention_workspace")
+    return n.value
+
+
+def adp_paged_window_attention(kv: PagedKV, q, q_dtype: int, n_heads: int, q_stride: int, scale: float, window: int, sinks: int,
+                               out, out_stride: int, workspace, workspace_bytes: int, dev_status=None, stream: int = 0):
+    _check(load_library().adp_paged_window_attention(kv, _ptr(q), q_dtype, n_heads, q_stride, scale, window, sinks, _ptr(out),
+                                                     out_stride, _ptr(workspace), workspace_bytes, _ptr(dev_status), stream),
+           "adp_paged_window_attention")
+
+
+def adp_paged_chunk_attention_workspace(kv: PagedKV, n_heads: int, n_rows: int, window: int, sinks: int) -> int:
+    n = ctypes.c_uint64()
+    _check(load_library().adp_paged_chunk_attention_workspace(kv, n_heads, n_rows, window, sinks, ctypes.byref(n)),
+           "adp_paged_chunk_attention_workspace")
+    return n.value
+
+
+def adp_paged_chunk_attention(kv: PagedKV, q, q_dtype: int, n_heads: int, q_stride: int, cu_rows, n_rows: int, scale: float,
+                              window: int, sinks: int, out, out_stride: int, workspace, workspace_bytes: int, dev_status=None,
+                              stream: int = 0):
+    _check(load_library().adp_paged_chunk_attention(kv, _ptr(q), q_dtype, n_heads, q_stride, _ptr(cu_rows), n_rows, scale, window,
+                                                    sinks, _ptr(out), out_stride, _ptr(workspace), workspace_bytes,
+                                                    _ptr(dev_status), stream), "adp_paged_chunk_attention")
 
 
 def adp_paged_forward(model, layers, tokens, cu_rows, lens, dev_logits):

@@ -1,6 +1,6 @@
 """Build libadp.so (the engine's C ABI) in-tree with nvcc for sm_103a.
 
-Ten translation units compiled in parallel, then linked as a shared library with the
+Thirteen translation units compiled in parallel, then linked as a shared library with the
 static CUDA runtime. -fmad=false keeps every multiply-add that the arithmetic contract does
 not fuse explicitly as a separate multiply and add; no fast-math flags.
 
@@ -21,7 +21,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libadp.so")
 TEST_LIB = os.path.join(HERE, "libadp_test.so")
 SOURCES = ["decode.cu", "decode_batch.cu", "prefill.cu", "repack.cu", "engine.cu", "noalloc.cu", "probe.cu",
-           "paged_rows.cu", "paged_attention.cu", "packed_attention.cu"]
+           "paged_rows.cu", "paged_append.cu",
+           "paged_attention.cu", "paged_window.cu", "paged_chunk.cu", "packed_attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-fmad=false", "-Xcompiler", "-fPIC", "-Xcompiler", "-ffp-contract=off",
          "-Xcompiler", "-fvisibility=hidden"]

@@ -166,6 +166,8 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) 
 // between 8-row groups of K, lbo between the 64-wide blocks of M or N; 16 rows of K further is 2,048 bytes.
 // The instruction descriptor's bit for an MN-major B operand.
 constexpr uint32_t kTcIdescBMn = 1u << 16;
+// The one that negates A.
+constexpr uint32_t kTcIdescANeg = 1u << 13;
 
 // D[tmem] (+)= A[smem] * B[smem]^T with the descriptors' low words and their common high word.
 __device__ __forceinline__ void tc_mma_f16_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
@@ -192,6 +194,14 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, i
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
       ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// The same of a 4-D box.
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* map, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
 }
 

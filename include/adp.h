@@ -397,6 +397,34 @@ int adp_paged_kv_read(const adp_paged_kv* kv, void* k, void* v, int32_t rows_dty
                       int64_t v_stride, const int32_t* cu_rows, int32_t n_rows, int32_t* dev_status,
                       void* cuda_stream);
 
+/* Position rotation, and norms of query and key heads in front of it. */
+typedef struct {
+  const float *cos, *sin;     /* DEVICE [n_positions][rotated / 2]: cosines and sines of each position's angles, 16-byte aligned */
+  int32_t n_positions;
+  int32_t rotated;            /* elements of a head that are rotated: a multiple of 16 up to head_dim; pairs i, i + rotated / 2 */
+  const void *q_gain, *k_gain; /* DEVICE [head_dim] of gain_dtype, 16-byte aligned: heads x become x / sqrt(mean(x^2) + eps) x gain
+                                  first; NULL: no norm */
+  int32_t gain_dtype;         /* ADP_F16, ADP_BF16 or ADP_F32 */
+  float eps;                  /* finite, at least 0 */
+} adp_rope;
+
+/* Append packed rows of a fused projection to their sequences: queries and keys are normed per head (where there are gains) and
+ * rotated by their positions, the queries go to out, keys and values into their pages.  Geometry, pages and reports as
+ * adp_paged_kv_write (row i of sequence s is position p = lens[s] - (cu_rows[s + 1] - i)); elements i and i + r of a head
+ * (r = rotated / 2, i < r) become x_i cos[p][i] - x_(i+r) sin[p][i] and x_(i+r) cos[p][i] + x_i sin[p][i], the others stay.
+ *  q, k, v     DEVICE rows [n_rows][n_heads or n_kv_heads][head_dim] of rows_dtype (ADP_F16, ADP_BF16 or ADP_F32), consecutive
+ *              rows q_stride / k_stride / v_stride elements apart (multiples of 16 bytes), 16-byte aligned
+ *  n_heads     query heads, at most 4096; 0: keys and values only (q and out are ignored)
+ *  out         DEVICE rows [n_rows][n_heads][head_dim] of out_dtype (ADP_F16, ADP_BF16 or ADP_F32), 16-byte aligned; may be q where
+ *              types and strides are the same
+ * Everything is computed in fp32 (a mean of squares beyond its range gives zeros) and rounded once.  A row without a page is not
+ * written and reported as adp_paged_kv_write does, one at a position behind the cosines' is not written and reported as
+ * ADP_ERR_CONTEXT_OVERFLOW; both give zeros in out.  Padding rows of out are left as they were. */
+int adp_paged_kv_append(const adp_paged_kv* kv, const adp_rope* rope, const void* q, const void* k, const void* v,
+                        int32_t rows_dtype, int32_t n_heads, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                        const int32_t* cu_rows, int32_t n_rows, void* out, int32_t out_dtype, int64_t out_stride,
+                        int32_t* dev_status, void* cuda_stream);
+
 /* Attention of one new token per sequence: out[s][h] = sum_p softmax_p(scale q[s][h] . K[p][g]) V[p][g]
  * over positions p < lens[s] (the new token's own row is cached first), g = h / (n_heads / n_kv_heads).
  *  q, out      DEVICE [n_seqs][n_heads][head_dim] of q_dtype (ADP_F16 or ADP_BF16; the cache's own type
@@ -420,6 +448,44 @@ int adp_paged_attention(const adp_paged_kv* kv, const void* q, int32_t q_dtype, 
 /* Bytes of scratch adp_paged_attention needs for this cache's shape (0 for few short sequences, a few MB at most;
  * asks the current device for its SM count). */
 int adp_paged_attention_workspace(const adp_paged_kv* kv, int32_t n_heads, uint64_t* bytes);
+
+/* adp_paged_attention with a sliding window: the new token sees the last `window` positions (its own row is the last of them;
+ * at least 1) and the first `sinks` ones (0 or more) and no others, whose pages are neither read nor looked up: their table
+ * entries may name no page.  Arguments, rounding, reports and errors as adp_paged_attention; the workspace is that of the call
+ * below, and the work is split by the window where that is shorter than the table. */
+int adp_paged_window_attention(const adp_paged_kv* kv, const void* q, int32_t q_dtype, int32_t n_heads, int64_t q_stride,
+                               float scale, int32_t window, int32_t sinks, void* out, int64_t out_stride, void* workspace,
+                               uint64_t workspace_bytes, int32_t* dev_status, void* cuda_stream);
+int adp_paged_window_attention_workspace(const adp_paged_kv* kv, int32_t n_heads, int32_t window, int32_t sinks,
+                                         uint64_t* bytes);
+
+/* Attention of every sequence's last rows over the pages: a chunk of a prompt behind its cached part, tokens to be verified,
+ * single tokens, or all of them together.  Sequence s has rows cu_rows[s] .. cu_rows[s + 1] - 1 of q, and they are its last
+ * positions, as adp_paged_kv_write has them (their own K and V are cached first): the row at position p sees positions j <= p,
+ * with a window only those with j > p - window and the first `sinks` ones.  out = softmax(scale q . K) V as above.
+ *  q, out      DEVICE [n_rows][n_heads][head_dim] of q_dtype (ADP_F16 or ADP_BF16; the cache's own type where that is a 16-bit
+ *              one), rows q_stride / out_stride elements apart (multiples of 8), 16-byte aligned
+ *  cu_rows     DEVICE [n_seqs + 1], ascending from 0; rows from cu_rows[n_seqs] on are padding, and their rows of out are left
+ *              as they were
+ *  n_heads     a multiple of n_kv_heads, at most 128 times as many; n_seqs at most 8192
+ *  window      0: none; else at least 1, the row's own position is the last of them.  Pages of which no row sees anything are
+ *              neither read nor looked up: their table entries may name no page
+ *  sinks       at least 0 (without a window it says nothing)
+ *  workspace   DEVICE scratch of at least adp_paged_chunk_attention_workspace bytes, 16-byte aligned (may be NULL where that
+ *              is 0); its contents do not matter.  Calls that may run at the same time need one each.
+ * Scores, softmax and sums are fp32; before they weigh V, probabilities are rounded to the cache's 16-bit type (fp16 ones held
+ * 2^7 times larger), over e4m3 pages probability x value scale to fp16 as in adp_paged_attention.  A row that sees nothing
+ * gives zeros.  What a row does not see does not reach it, whatever it holds.  Bad pages and lengths are treated and reported as in
+ * adp_paged_attention; a sequence with more rows than positions (its first rows give zeros) and offsets that do not start at
+ * 0, descend or lie outside [0, n_rows] (cut to it) are reported as ADP_ERR_INVALID_ARG; a wait inside the kernel that ran out
+ * (1 s and more) is reported as ADP_ERR_PIPELINE_TIMEOUT, and leaves rows of out unset: only dev_status tells.  Equal inputs
+ * give equal bits on one GPU. */
+int adp_paged_chunk_attention(const adp_paged_kv* kv, const void* q, int32_t q_dtype, int32_t n_heads, int64_t q_stride,
+                              const int32_t* cu_rows, int32_t n_rows, float scale, int32_t window, int32_t sinks, void* out,
+                              int64_t out_stride, void* workspace, uint64_t workspace_bytes, int32_t* dev_status,
+                              void* cuda_stream);
+int adp_paged_chunk_attention_workspace(const adp_paged_kv* kv, int32_t n_heads, int32_t n_rows, int32_t window, int32_t sinks,
+                                        uint64_t* bytes);
 
 /* Causal attention of packed prompts: query i of sequence s (row cu_q[s] + i) sees keys j <= i + (lk - lq) of
  * sequence s, lq and lk its numbers of query and key rows, so that the last query sees every key: a prompt's
