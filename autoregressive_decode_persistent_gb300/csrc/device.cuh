@@ -45,6 +45,17 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* b, uint32_t parity) {
   return ok != 0;
 }
 
+// The same without waiting at all (a try may suspend the thread for a while).
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Wait for the phase of `parity` to complete.  Gives up (returns false) when *abort becomes
 // nonzero or after limit_ns; every wait in the kernel is bounded.
 __device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity, volatile int32_t* abort, uint64_t limit_ns) {

@@ -22,43 +22,51 @@ struct AppendArgs {
   const float *cos, *sin;
   const uint8_t *q_gain, *k_gain;
   int32_t* status;
-  int32_t n_rows, n_heads, n_pos, turned;  // turned: pieces of 8 elements that are first of a rotated pair (angles / 8)
+  int32_t n_rows, n_heads, n_pos, turned;  // turned: pieces of 8 elements that are the first of rotated pairs
   int32_t parts, part_heads;               // warps that share a row, and their heads (of its line of heads)
   int32_t out_dt, gain_dt;
   float eps;
 };
 
-// A row's heads are one line: queries, keys, values.  A warp takes one row, or a part of its line where there are few rows;
-// its lanes hold pieces of 8 elements, HD / 8 of them a head, kAhead pieces in flight per lane.  Per head: the mean square over
-// the head's lanes (a norm's x / sqrt(mean(x^2) + eps) x gain), then the rotation of elements i and i + r by the position's
-// angle i (r angles): the partner's piece comes from another lane, and a lane's 8 cosines and sines are the same for all of
-// the row's heads.  Everything in fp32, rounded once on the way out (keys to codes x scale in e4m3 pages).
+// A row's heads are one line: queries, keys, values.  A warp takes one row, or a part of its line where there are few rows.
+// HD / 16 lanes hold a head, two pieces of 8 elements each: a lane with rotated elements has both halves of its pairs (pieces
+// u and u + turned), so that the rotation needs no other lane, and the mean square and the largest magnitude take three
+// exchanges a head.  A lane's 8 cosines and sines are the same for all of the row's heads.  Per head: a norm's x / sqrt(mean(x^2) +
+// eps) x gain, then x_i cos - x_(i+r) sin and x_(i+r) cos + x_i sin; everything in fp32, in pairs where there are
+// instructions for them, and rounded once on the way out (keys to codes x scale in e4m3 pages).
 template <int ROWDT, int CDT, int HD>
 __global__ void __launch_bounds__(256) paged_append_kernel(const AppendArgs a) {
-  constexpr int LPR = HD / 8;  // lanes that hold a head
-  constexpr int HPS = 32 / LPR;  // heads of a step of the warp
-  constexpr int kAhead = 4;
+  constexpr int LPH = HD / 16;    // lanes that hold a head
+  constexpr int HPS = 32 / LPH;   // heads of a step of the warp
+  constexpr int kAhead = ROWDT == DT_F32 ? 1 : 2;  // steps in flight
   constexpr int RB = elem_bytes(ROWDT);
   const PagedView& c = a.c;
-  const int lane = threadIdx.x & 31, li = lane % LPR, piece = li * 8;
+  const int lane = threadIdx.x & 31, u = lane % LPH;
+  const int pa = u < a.turned ? u : 2 * u, pb = u < a.turned ? u + a.turned : 2 * u + 1;  // this lane's pieces of a head
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   // offsets that are wrong are reported, whichever rows they would move
   for (int64_t s = (int64_t)blockIdx.x * 256 + threadIdx.x; s < c.n_seqs; s += (int64_t)gridDim.x * 256)
     if (a.cu[s + 1] < a.cu[s] || (s == 0 && a.cu[0] != 0)) report(a.status, ADP_ERR_INVALID_ARG);
-  const int i = (int)(w / a.parts);
+  const int i = a.parts == 1 ? (int)w : (int)(w / a.parts);
   if (i >= a.n_rows) return;
   const int heads = a.n_heads + 2 * c.n_kv_heads;
-  const int first = (int)(w % a.parts) * a.part_heads, last = min(first + a.part_heads, heads);
-  const uint8_t *const rq = a.q + (int64_t)i * a.q_stride + piece * RB, *const rk = a.k + (int64_t)i * a.k_stride + piece * RB,
-                *const rv = a.v + (int64_t)i * a.v_stride + piece * RB;
-  Raw8<ROWDT> raw[kAhead];
+  const int first = a.parts == 1 ? 0 : (int)(w - (int64_t)i * a.parts) * a.part_heads, last = min(first + a.part_heads, heads);
+  const uint8_t *const rq = a.q + (int64_t)i * a.q_stride, *const rk = a.k + (int64_t)i * a.k_stride,
+                *const rv = a.v + (int64_t)i * a.v_stride;
+  Raw8<ROWDT> raw[kAhead][2];
   // the rows are asked for in front of the look-ups that say where they go
   auto load_rows = [&](int h0) {
 #pragma unroll
     for (int n = 0; n < kAhead; ++n) {
-      const int h = h0 + n * HPS + lane / LPR, hk = h - a.n_heads, hv = hk - c.n_kv_heads;
-      if (h < last) raw[n].load(hk < 0 ? rq + h * (HD * RB) : hv < 0 ? rk + hk * (HD * RB) : rv + hv * (HD * RB));
-      else raw[n].clear();
+      const int h = h0 + n * HPS + lane / LPH, hk = h - a.n_heads, hv = hk - c.n_kv_heads;
+      if (h < last) {
+        const uint8_t* p = hk < 0 ? rq + h * (HD * RB) : hv < 0 ? rk + hk * (HD * RB) : rv + hv * (HD * RB);
+        raw[n][0].load(p + pa * (8 * RB));
+        raw[n][1].load(p + pb * (8 * RB));
+      } else {
+        raw[n][0].clear();
+        raw[n][1].clear();
+      }
     }
   };
   load_rows(first);
@@ -78,92 +86,119 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const AppendArgs a) {
     if (lane == 0) report(a.status, ADP_ERR_CONTEXT_OVERFLOW);
     page = -1;
   }
-  const bool there = page >= 0;
-  // this lane's angles, and the lane with the other halves of its pairs
-  const bool low = li < a.turned, turned = li < 2 * a.turned;
-  const int partner = low ? lane + a.turned : turned ? lane - a.turned : lane;
-  float cs[8], sn[8];
-  if (turned && there) {
-    const int64_t at = pos * (a.turned * 8) + (low ? li : li - a.turned) * 8;
+  const bool there = page >= 0, turned = u < a.turned && there;
+  float2 cs[4], sn[4], ns[4];  // this lane's angles
+  if (turned) {
+    const int64_t at = pos * (a.turned * 8) + u * 8;
 #pragma unroll
-    for (int e = 0; e < 8; e += 4) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(a.cos + at + e)), y = __ldg(reinterpret_cast<const float4*>(a.sin + at + e));
-      cs[e] = x.x, cs[e + 1] = x.y, cs[e + 2] = x.z, cs[e + 3] = x.w;
-      sn[e] = y.x, sn[e + 1] = y.y, sn[e + 2] = y.z, sn[e + 3] = y.w;
+    for (int e = 0; e < 4; e += 2) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(a.cos + at + 2 * e)), y = __ldg(reinterpret_cast<const float4*>(a.sin + at + 2 * e));
+      cs[e] = make_float2(x.x, x.y), cs[e + 1] = make_float2(x.z, x.w);
+      sn[e] = make_float2(y.x, y.y), sn[e + 1] = make_float2(y.z, y.w);
+      ns[e] = make_float2(-y.x, -y.y), ns[e + 1] = make_float2(-y.z, -y.w);
     }
-    if (low)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sn[e] = -sn[e];
   }
   const int slot = (int)(pos & ((1 << c.log2_page) - 1));
   const int head_step = (HD * elem_bytes(CDT)) << c.log2_page;  // (32 bits hold it, as in the other rows' kernels)
-  const int64_t cell0 = (int64_t)page * c.page_bytes + ((int64_t)slot * HD + piece) * elem_bytes(CDT);
+  const int64_t cell0 = (int64_t)page * c.page_bytes + (int64_t)slot * (HD * elem_bytes(CDT));
   const int64_t scale0 = CDT == DT_E4M3 ? (int64_t)page * c.scale_stride + slot : 0;
-  uint8_t* const ro = a.out + (int64_t)i * a.out_stride + piece * elem_bytes(a.out_dt);
+  uint8_t* const ro = a.out + (int64_t)i * a.out_stride;
+  auto pairs = [](const float (&x)[8], float2 (&y)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = make_float2(x[2 * e], x[2 * e + 1]);
+  };
+  auto gains = [&](const uint8_t* g, int p, float2 (&y)[4]) {
+    float x[8];
+    if (a.gain_dt == DT_F32) {
+      const float4 s = __ldg(reinterpret_cast<const float4*>(g) + 2 * p), t = __ldg(reinterpret_cast<const float4*>(g) + 2 * p + 1);
+      x[0] = s.x, x[1] = s.y, x[2] = s.z, x[3] = s.w, x[4] = t.x, x[5] = t.y, x[6] = t.z, x[7] = t.w;
+    } else if (a.gain_dt == DT_BF16) {
+      load8<DT_BF16>(g + p * 16, x);
+    } else {
+      load8<DT_F16>(g + p * 16, x);
+    }
+    pairs(x, y);
+  };
 #pragma unroll 1
   for (int h0 = first; h0 < last; h0 += kAhead * HPS) {
     if (h0 > first) load_rows(h0);
 #pragma unroll
     for (int n = 0; n < kAhead; ++n) {
       if (h0 + n * HPS >= last) break;
-      const int h = h0 + n * HPS + lane / LPR, hk = h - a.n_heads, hv = hk - c.n_kv_heads;
+      const int h = h0 + n * HPS + lane / LPH, hk = h - a.n_heads, hv = hk - c.n_kv_heads;
       const bool on = h < last, is_q = hk < 0, is_v = hv >= 0;
-      float x[8];
-      raw[n].expand(x);
-      if (!__all_sync(0xFFFFFFFFu, is_v)) {
-        const uint8_t* gain = is_q ? a.q_gain : is_v ? nullptr : a.k_gain;
-        if (a.q_gain || a.k_gain) {
-          float sum = 0.0f;
+      float2 x[2][4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
+      for (int k = 0; k < 2; ++k) {
+        float y[8];
+        raw[n][k].expand(y);
+        pairs(y, x[k]);
+      }
+      if (!is_v) {
+        const uint8_t* gain = is_q ? a.q_gain : a.k_gain;
+        if (gain) {  // (all lanes of a head alike)
+          float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-          for (int d = LPR / 2; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-          if (gain) {
-            const float f = rsqrtf(sum * (1.0f / HD) + a.eps);
-            float g[8];
-            if (a.gain_dt == DT_F32) {
-              const float4 u = __ldg(reinterpret_cast<const float4*>(gain) + 2 * li), v = __ldg(reinterpret_cast<const float4*>(gain) + 2 * li + 1);
-              g[0] = u.x, g[1] = u.y, g[2] = u.z, g[3] = u.w, g[4] = v.x, g[5] = v.y, g[6] = v.z, g[7] = v.w;
-            } else if (a.gain_dt == DT_BF16) {
-              load8<DT_BF16>(gain + piece * 2, g);
-            } else {
-              load8<DT_F16>(gain + piece * 2, g);
-            }
+          for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = x[e] * f * g[e];
+            for (int e = 0; e < 4; ++e) sum = __ffma2_rn(x[k][e], x[k][e], sum);
+          float ss = sum.x + sum.y;
+          const uint32_t mates = (LPH == 32 ? ~0u : (1u << LPH) - 1) << (lane / LPH * LPH);
+#pragma unroll
+          for (int d = LPH / 2; d >= 1; d >>= 1) ss += __shfl_xor_sync(mates, ss, d);
+          const float f = rsqrtf(ss * (1.0f / HD) + a.eps);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float2 g[4];
+            gains(gain, k ? pb : pa, g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[k][e] = __fmul2_rn(__fmul2_rn(x[k][e], make_float2(f, f)), g[e]);
           }
         }
+        if (turned) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float y = __shfl_sync(0xFFFFFFFFu, x[e], partner);
-          if (turned && !is_v) x[e] = fmaf(x[e], cs[e], y * sn[e]);
+          for (int e = 0; e < 4; ++e) {
+            const float2 p = x[0][e], q = x[1][e];
+            x[0][e] = __ffma2_rn(p, cs[e], __fmul2_rn(q, ns[e]));
+            x[1][e] = __ffma2_rn(q, cs[e], __fmul2_rn(p, sn[e]));
+          }
         }
-      }
-      float top = 0.0f;
-      if constexpr (CDT == DT_E4M3) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(x[e]));
-#pragma unroll
-        for (int d = LPR / 2; d >= 1; d >>= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
       }
       if (!on) continue;
       if (is_q) {
-        if (!there) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-        }
         uint8_t* p = ro + h * HD * elem_bytes(a.out_dt);
-        if (a.out_dt == DT_BF16) store_row8<DT_BF16>(p, x);
-        else if (a.out_dt == DT_F16) store_row8<DT_F16>(p, x);
-        else store_row8<DT_F32>(p, x);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int at = k ? pb : pa;
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[2 * e] = there ? x[k][e].x : 0.0f, y[2 * e + 1] = there ? x[k][e].y : 0.0f;
+          if (a.out_dt == DT_BF16) store_row8<DT_BF16>(p + at * 16, y);
+          else if (a.out_dt == DT_F16) store_row8<DT_F16>(p + at * 16, y);
+          else store_row8<DT_F32>(p + at * 32, y);
+        }
       } else if (there) {
         const int hc = is_v ? hv : hk;
         uint8_t* cell = (is_v ? c.v : c.k) + cell0 + hc * head_step;
         if constexpr (CDT == DT_E4M3) {
-          const float s = quantise8(x, top);
-          if (li == 0) (is_v ? c.v_scale : c.k_scale)[scale0 + ((int64_t)hc << c.log2_page)] = s;
+          float top = 0.0f;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max_nan(max_nan(top, fabsf(x[k][e].x)), fabsf(x[k][e].y));
+          const uint32_t mates = (LPH == 32 ? ~0u : (1u << LPH) - 1) << (lane / LPH * LPH);
+#pragma unroll
+          for (int d = LPH / 2; d >= 1; d >>= 1) top = max_nan(top, __shfl_xor_sync(mates, top, d));
+          const float s = quantise16(x, top);
+          if (u == 0) (is_v ? c.v_scale : c.k_scale)[scale0 + ((int64_t)hc << c.log2_page)] = s;
         }
-        store_row8<CDT>(cell, x);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[2 * e] = x[k][e].x, y[2 * e + 1] = x[k][e].y;
+          store_row8<CDT>(cell + (k ? pb : pa) * 8 * elem_bytes(CDT), y);
+        }
       }
     }
   }
@@ -228,7 +263,7 @@ extern "C" int adp_paged_kv_append(const adp_paged_kv* kv, const adp_rope* rope,
   a.out_dt = n_heads > 0 ? out_dtype : ADP_F16;
   a.gain_dt = rope->gain_dtype;
   a.eps = rope->eps;
-  const int heads = n_heads + 2 * kv->n_kv_heads, step = 32 / (kv->head_dim / 8);
+  const int heads = n_heads + 2 * kv->n_kv_heads, step = 32 / (kv->head_dim / 16);
   const int most = (heads + step - 1) / step, want = sms * kWarpsPerSm / n_rows;
   a.parts = want < 1 ? 1 : want > most ? most : want;
   a.part_heads = (most + a.parts - 1) / a.parts * step;

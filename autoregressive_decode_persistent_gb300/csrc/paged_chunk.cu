@@ -18,7 +18,6 @@ namespace {
 constexpr int kRows = 128;              // rows of a query tile (M of the MMA)
 constexpr int kKeys = kChunkKeys;
 constexpr float kRescale = 8.0f;        // base-2 growth of a row's maximum that rescales its output
-constexpr float kFactorMax = 1.329227996e36f;  // 2^120, of a value scale relative to the largest product
 constexpr int kItems = 2;               // the piece of work and the next one
 
 // What a CTA has left for the join: its first piece's first part may go on from the CTA before, its last one may go on behind it.
@@ -35,11 +34,13 @@ struct ChunkArgs {
   uint8_t* out;
   int64_t out_stride;            // bytes
   int32_t n_rows, group, tok;    // query heads per KV head; tokens of a tile
+  int32_t few;                   // tokens of a quarter of a tile (0: a token does not fit)
   int32_t window, sinks;
   float scale_log2;              // of |scale|, and above 0
+  int32_t even_scales;           // e4m3: four positions' scales are 16 aligned bytes wherever their pages lie
   uint32_t neg;                  // scale < 0: the instruction descriptor's bit that negates A
   int32_t rows_cap;              // rows of a partial result (128 or 256)
-  float* part_o;                 // [ctas][2][rows_cap][head_dim]
+  float* part_o;                 // [ctas][2][rows_cap / 32][head_dim / 4][32 rows][4]
   float2* part_ml;               // [ctas][2][rows_cap]
   ChunkMeta* meta;               // [ctas]
   int32_t* status;
@@ -69,8 +70,10 @@ struct Item {
   int32_t stop;  // no work is left
   __device__ __forceinline__ int first() const { return len - lq + t0; }
   __device__ __forceinline__ int last(int span) const { return len - lq + min(t0 + span, lq) - 1; }
-  // its rows fit one tile: the tiles are two halves of the blocks, in turn
+  // its rows fit one tile: the tiles take turns at the blocks
   __device__ __forceinline__ bool half(int tok) const { return lq - t0 <= tok; }
+  // its rows fit a quarter of a tile: each warp of a tile has them all, and takes a quarter of a block's positions
+  __device__ __forceinline__ bool quarter(int few) const { return lq - t0 <= few; }
 };
 // Blocks that tile t of the item works on, and the way from one to the next.
 struct Own {
@@ -83,31 +86,49 @@ __device__ __forceinline__ Own own_blocks(const Item& w, const ChunkSpan& s, int
   const int last = w.first() + tok - 1;  // what tile A's last row sees is a beginning of the line
   return Own{last < 0 ? 0 : min(max(last / kKeys + 1 - s.gap - w.i0, 0), n), 1, 0};
 }
+// The bits below n of 64.
+__device__ __forceinline__ uint64_t below(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
+
 // Whether some row of the item does not see all positions of the block at position kb.
 __device__ __forceinline__ bool edge_block(int kb, int first, int last, int window, int sinks) {
   return kb + kKeys - 1 > first || (kb <= last - window && kb + kKeys - 1 >= sinks);
 }
 
-// The line of all work: sequences, in them pairs of tiles of tokens, in them KV heads, in them blocks.
+// The table's entry for a position (any position at or behind 0), and the page that it names: -2 where none of the n positions
+// from pos on, all in one page, is seen by a row, -1 where it names none.
+__device__ __forceinline__ int table_entry(const ChunkArgs& a, const int32_t* row, int pos) {
+  return __ldg(row + min(pos >> a.c.log2_page, a.c.table_width - 1));
+}
+__device__ __forceinline__ int page_of(const ChunkArgs& a, int entry, int pos, int n, int low, int last) {
+  if (pos > last || (pos + n <= low && pos >= a.sinks)) return -2;
+  return entry >= 0 && entry < a.c.n_pages ? entry : -1;
+}
+
+// The line of all work: KV heads, in them sequences, in them pairs of tiles of tokens, in them blocks.
 struct Place {
-  int32_t b, t, h, j;  // sequence, pair, KV head, block; b = n_seqs: the end
+  int32_t h, b, t, j;  // KV head, sequence, pair, block
+  __device__ __forceinline__ bool before(const Place& o) const {
+    return h != o.h ? h < o.h : b != o.b ? b < o.b : t != o.t ? t < o.t : j < o.j;
+  }
 };
 
 __device__ __forceinline__ int pair_blocks(const ChunkArgs& a, const Rows& r, int t) {
   const int span = 2 * a.tok, first = r.len - r.lq + t * span, last = r.len - r.lq + min((t + 1) * span, r.lq) - 1;
   return chunk_span(first, last, a.window, a.sinks).n;
 }
+__device__ __forceinline__ Rows shfl_rows(const Rows& r, int l) {
+  return Rows{__shfl_sync(0xFFFFFFFFu, r.q0, l), __shfl_sync(0xFFFFFFFFu, r.lq, l), __shfl_sync(0xFFFFFFFFu, r.len, l)};
+}
 // Units of a sequence for one KV head, one lane per sequence; long ones are added up by the whole warp.
 __device__ __forceinline__ int64_t sequence_units(const ChunkArgs& a, const Rows& r, int lane) {
-  constexpr int kAlone = 4;
+  constexpr int kAlone = 2;
   const int span = 2 * a.tok, pairs = (r.lq + span - 1) / span;
   int64_t sum = 0;
   if (pairs <= kAlone)
     for (int t = 0; t < pairs; ++t) sum += pair_blocks(a, r, t) + kChunkOver;
   for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, pairs > kAlone); todo; todo &= todo - 1) {
-    const int l = __ffs(todo) - 1;
-    const Rows o{__shfl_sync(0xFFFFFFFFu, r.q0, l), __shfl_sync(0xFFFFFFFFu, r.lq, l), __shfl_sync(0xFFFFFFFFu, r.len, l)};
-    const int n = __shfl_sync(0xFFFFFFFFu, pairs, l);
+    const int l = __ffs(todo) - 1, n = __shfl_sync(0xFFFFFFFFu, pairs, l);
+    const Rows o = shfl_rows(r, l);
     int64_t s = 0;
     for (int t = lane; t < n; t += 32) s += pair_blocks(a, o, t) + kChunkOver;
 #pragma unroll
@@ -124,39 +145,51 @@ __device__ __forceinline__ int64_t scan_inclusive(int64_t x, int lane) {
   }
   return x;
 }
-// Where a cut of the line at unit x goes.  chunks: units in front of every 32 sequences, for one KV head.  A whole warp asks.
-__device__ __noinline__ Place find_place(const ChunkArgs& a, const int64_t* chunks, int n_chunks, int64_t x, int lane) {
-  const int hkv = a.c.n_kv_heads;
-  if (x >= chunks[n_chunks] * hkv) return Place{a.c.n_seqs, 0, 0, 0};
-  int ch = 0;
-  for (int at = 0; at < n_chunks; at += 32) {
-    const int n = __popc(__ballot_sync(0xFFFFFFFFu, at + lane < n_chunks && chunks[at + lane] * hkv <= x));
-    if (n) ch = at + n - 1;
-    if (n < 32) break;
+// Units and pairs of 32 sequences, for one KV head.
+struct Units {
+  int64_t units;
+  int32_t pairs;
+};
+
+// The warp that finds the work: its lanes hold 32 sequences at a time.
+struct Finder {
+  const ChunkArgs& a;
+  const int lane, span;
+  int chunk;       // the sequences held: from 32 x chunk on
+  Rows mine;
+  int64_t units, upto;  // of this lane's sequence, and with those before it
+  __device__ __forceinline__ Finder(const ChunkArgs& args, int l) : a(args), lane(l), span(2 * args.tok), chunk(-1), mine{0, 0, 0}, units(0), upto(0) {}
+  __device__ __forceinline__ void hold(int ch, int32_t* status) {
+    if (ch == chunk) return;
+    chunk = ch;
+    mine = Rows{0, 0, 0};
+    if (ch * 32 + lane < a.c.n_seqs) mine = rows_of(a, ch * 32 + lane, status);
   }
-  x -= chunks[ch] * hkv;
-  Rows r{0, 0, 0};
-  if (ch * 32 + lane < a.c.n_seqs) r = rows_of(a, ch * 32 + lane, nullptr);
-  const int64_t units = sequence_units(a, r, lane), upto = scan_inclusive(units, lane);
-  const int l = min(__popc(__ballot_sync(0xFFFFFFFFu, upto * hkv <= x)), 31);
-  x -= __shfl_sync(0xFFFFFFFFu, upto - units, l) * hkv;
-  const Rows o{__shfl_sync(0xFFFFFFFFu, r.q0, l), __shfl_sync(0xFFFFFFFFu, r.lq, l), __shfl_sync(0xFFFFFFFFu, r.len, l)};
-  const int span = 2 * a.tok, pairs = (o.lq + span - 1) / span;
-  for (int t0 = 0; t0 < pairs; t0 += 32) {
-    const int blocks = t0 + lane < pairs ? pair_blocks(a, o, t0 + lane) : 0;
-    const int64_t mine = t0 + lane < pairs ? blocks + kChunkOver : 0, sum = scan_inclusive(mine, lane);
-    const int p = __popc(__ballot_sync(0xFFFFFFFFu, sum * hkv <= x));
-    if (p == 32) {
-      x -= __shfl_sync(0xFFFFFFFFu, sum, 31) * hkv;
-      continue;
+  __device__ __forceinline__ void add_up() {
+    units = sequence_units(a, mine, lane);
+    upto = scan_inclusive(units, lane);
+  }
+  __device__ __forceinline__ int pairs() const { return (mine.lq + span - 1) / span; }
+  // Where a cut at unit x of a head's line goes, within the sequences held (and added up).
+  __device__ __forceinline__ Place place(int h, int64_t x) const {
+    const int l = min(__popc(__ballot_sync(0xFFFFFFFFu, upto <= x)), 31);
+    x -= __shfl_sync(0xFFFFFFFFu, upto - units, l);
+    const Rows o = shfl_rows(mine, l);
+    const int n = (o.lq + span - 1) / span;
+    for (int t0 = 0; t0 < n; t0 += 32) {
+      const int blocks = t0 + lane < n ? pair_blocks(a, o, t0 + lane) : 0;
+      const int64_t own = t0 + lane < n ? blocks + kChunkOver : 0, sum = scan_inclusive(own, lane);
+      const int p = __popc(__ballot_sync(0xFFFFFFFFu, sum <= x));
+      if (p == 32) {
+        x -= __shfl_sync(0xFFFFFFFFu, sum, 31);
+        continue;
+      }
+      x -= __shfl_sync(0xFFFFFFFFu, sum - own, p);
+      return Place{h, chunk * 32 + l, t0 + p, chunk_cut(__shfl_sync(0xFFFFFFFFu, blocks, p), x)};
     }
-    x -= __shfl_sync(0xFFFFFFFFu, sum - mine, p) * hkv;
-    const int n = __shfl_sync(0xFFFFFFFFu, blocks, p);
-    const int h = (int)min(x / (n + kChunkOver), (int64_t)hkv - 1);
-    return Place{ch * 32 + l, t0 + p, h, chunk_cut(n, x - (int64_t)h * (n + kChunkOver))};
+    return Place{h, chunk * 32 + l, n, 0};  // (the offsets changed while this call ran)
   }
-  return Place{a.c.n_seqs, 0, 0, 0};  // (the offsets changed while this call ran)
-}
+};
 
 // Per ring slot of e4m3 blocks: the scales, log2 of the value scales and its largest over each half of the block.
 struct SlotScales {
@@ -166,46 +199,89 @@ struct SlotScales {
 template <int HD, int CDT>
 struct ChunkSmem {
   static constexpr bool kConv = CDT == DT_E4M3;
-  static constexpr int kSlots = kConv ? (HD == 128 ? 3 : 6) : (HD == 128 ? 5 : 8);  // of a block of K and one of V
-  static constexpr int kRaw = kConv ? (HD == 128 ? 3 : 6) : 0;                       // blocks of codes under way
+  static constexpr int kSlots = HD == 64 ? 8 : kConv ? 3 : 4;  // of a block of K and one of V
+  static constexpr int kRaw = kConv ? (HD == 128 ? 5 : 8) : 0;   // blocks of codes of K or of V under way
   static constexpr uint32_t kQBlock = 128 * 128;            // 128 rows x 64 elements, swizzled
   static constexpr uint32_t kQTile = (HD / 64) * kQBlock;
   static constexpr uint32_t kBlock = kKeys * 128;           // the same of K or V
   static constexpr uint32_t kTile = (HD / 64) * kBlock;
   static constexpr uint32_t kPair = 2 * kTile;
-  static constexpr uint32_t kRawBytes = 2 * kKeys * HD + 512;  // codes, and a scale per row of K and V
+  static constexpr int kOutBytes = kConv ? 64 : 128;        // of a row of results on their way out
+  static constexpr int kOutCols = kOutBytes / 8;            // columns of results that tiles and warps add up at a time, in two buffers
+  static constexpr uint32_t kRawBytes = kKeys * HD + kKeys * 4;  // codes, and a scale for each row
   static constexpr uint32_t kRawAt = 2 * kQTile + kSlots * kPair;
-  static constexpr uint32_t kScales = kRawAt + kRaw * kRawBytes;                           // [kSlots], e4m3
+  static constexpr uint32_t kOut = kRawAt + kRaw * kRawBytes;
+  static constexpr uint32_t kScales = kOut + 8 * 32 * kOutBytes;                           // [kSlots], e4m3
   static constexpr uint32_t kQf = kScales + (kConv ? kSlots * sizeof(SlotScales) : 0);     // [256] of the rows of Q, e4m3
-  static constexpr uint32_t kHalf = kQf + (kConv ? 2 * kRows * 4 : 0);                     // [2 or 3][128]
-  static constexpr uint32_t kCtl = kHalf + (kConv ? 3 : 2) * kRows * 4;
-  static constexpr size_t kBytes = 1024 + kCtl + 512;
+  static constexpr uint32_t kHalf = kQf + (kConv ? 2 * kRows * 4 : 0);                     // [2][256]
+  static constexpr uint32_t kCtl = kHalf + 4 * kRows * 4;
+  static constexpr uint32_t kCtlBytes = kConv ? 768 : 512;
+  static constexpr size_t kBytes = kCtl + kCtlBytes;
 };
 
+// LOAD: registers of a thread of the softmax warps, of those that find, copy and issue, and of those that load; the four groups of
+// 128 threads start with 128 each.
+constexpr int kSoftmaxRegs = 160, kIssueRegs = 72, kLoadRegs = 120;
+static_assert(2 * kSoftmaxRegs + kIssueRegs + kLoadRegs == 4 * 128, "what is taken has to be given");
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xFFFFu), __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// Four e4m3 codes as fp16 (exact): the low pair and the high pair.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
 }
+// Copy of consecutive bytes (a multiple of 16, from and to multiples of 16) into this CTA's shared memory, completing on an mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ uint4 zero_codes[kKeys * 128 / 16];  // what is read where a block's positions have no place
 __device__ __forceinline__ float log2_scale_of(float s) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fabsf(s)));
   return fmaxf(y, -126.0f);  // (2^-126: the least scale there is)
 }
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
+// What was taken out of the values (of blocks lo .. hi, by their positions) and is seen by a row: the sum for 4 columns from col on.
+template <int HD, int CDT>
+__device__ __forceinline__ float4 taken_out(const ChunkArgs& a, const Item& w, int pos, int col, int lo, int hi) {
+  const int first = w.first(), last = w.last(2 * a.tok), from = max(max(pos, 0) - a.window + 1, 0);
+  const ChunkSpan sp = chunk_span(first, last, a.window, a.sinks);
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = w.i0; i < w.i1; ++i) {
+    const int kb = chunk_block(sp, i) * kKeys;
+    if (kb < lo || kb > hi || !(w.quarter(a.few) || edge_block(kb, first, last, a.window, a.sinks))) continue;
+    for (int key = kb; key < kb + kKeys && key <= pos; ++key) {
+      if (key < from && key >= a.sinks) continue;
+      const int page = paged_page(a.c.table + (int64_t)w.b * a.c.table_width, a.c.table_width, a.c.n_pages, a.c.log2_page, key);
+      if (page < 0) continue;
+      const int at = (w.h << a.c.log2_page) + (key & ((1 << a.c.log2_page) - 1));
+      const uint8_t* pv = a.c.v + (int64_t)page * a.c.page_bytes + (int64_t)at * HD * elem_bytes(CDT);
+      const float f = CDT == DT_E4M3 ? a.c.v_scale[(int64_t)page * a.c.scale_stride + at] : 1.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float v = load_elem(pv, col + e, CDT);
+        if (CDT == DT_E4M3) v *= f;
+        sum[e] += isfinite(v) ? 0.0f : v;
+      }
+    }
+  }
+  return make_float4(sum[0], sum[1], sum[2], sum[3]);
 }
 
 // CDT: the pages' type; QDT: the queries' (that of 16-bit pages).  LOAD: four warps bring K and V into the ring (e4m3 pages,
@@ -213,7 +289,7 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 template <int HD, int CDT, int QDT, bool LOAD>
 __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                       const __grid_constant__ CUtensorMap mv, const ChunkArgs a) {
+                       const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mf, const ChunkArgs a) {
   using L = ChunkSmem<HD, CDT>;
   constexpr int NS = L::kSlots;
   constexpr bool Q8 = CDT == DT_E4M3;
@@ -221,8 +297,12 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
   constexpr bool QCONV = Q8 && QDT == DT_BF16;      // bf16 queries beside fp16 codes
   static_assert(LOAD || !Q8, "");
   constexpr int kWarps = LOAD ? 16 : 12;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  // (there is no room to align it by hand, and no need: no other shared memory lies in front)
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {
+    report(a.status, ADP_ERR_CUDA);
+    return;
+  }
   uint8_t* Qs = smem;
   uint8_t* ring = smem + 2 * L::kQTile;
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kCtl);
@@ -231,39 +311,41 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
   uint64_t* qfull = empty + NS;
   uint64_t* qready = qfull + 1;       // (QCONV)
   uint64_t* qempty = qready + 1;
-  uint64_t* hfull = qempty + 1;       // tile B's half is done, and read
-  uint64_t* hfree = hfull + 1;
-  uint64_t* done = hfree + 1;
+  uint64_t* joined = qempty + 1;      // the softmax warps meet
+  uint64_t* done = joined + 1;
   uint64_t* sfull = done + 1;         // [2][2]: tile, buffer
   uint64_t* pready = sfull + 4;       // [2][2]
   uint64_t* odone = pready + 4;       // [2][2]
   uint64_t* ifull = odone + 4;        // [kItems]
   uint64_t* iempty = ifull + kItems;  // [kItems]
-  uint64_t* hole = iempty + kItems;   // [NS]: positions of the block whose page has no place
+  uint64_t* vfull = iempty + kItems;       // [NS] e4m3: the block's V (and full: its K)
+  uint64_t* rawfull = vfull + (Q8 ? NS : 0);  // [kRaw]
+  uint64_t* rawempty = rawfull + L::kRaw;  // [kRaw]
+  uint64_t* rawhole = rawempty + L::kRaw;  // [kRaw], as hole
+  uint64_t* hole = rawhole + L::kRaw;      // [NS]: positions of the block whose page has no place
   int32_t* ctl = reinterpret_cast<int32_t*>(hole + NS);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctl);
   volatile int32_t* ab = ctl + 1;
-  volatile int32_t* bad = ctl + 2;    // a non-finite value was taken out of an edge block
-  volatile int32_t* holes = ctl + 3;  // some block had a position without a page
-  Item* items = reinterpret_cast<Item*>(ctl + 6);  // [kItems]; the waits' limit lies in front
-  float* s_half = reinterpret_cast<float*>(smem + L::kHalf);  // tile B's half of an item: maxima, sums, e4m3's factors of its output
+  volatile int32_t* holes = ctl + 2;  // some block had a position without a page
+  int32_t* taken = ctl + 6;           // positions of the first and of the last block that a non-finite value was taken out of
+  Item* items = reinterpret_cast<Item*>(ctl + 8);  // [kItems]
+  float* s_half = reinterpret_cast<float*>(smem + L::kHalf);  // where tiles and warps share rows: maxima and sums
   float* s_qf = reinterpret_cast<float*>(smem + L::kQf);
   SlotScales* s_scale = reinterpret_cast<SlotScales*>(smem + L::kScales);
-  __shared__ Place s_cut[2];
-  static_assert((2 * NS + 22) * 8 + NS * 8 + 24 + kItems * sizeof(Item) <= 512, "the control words' room");
+  static_assert(((Q8 ? 4 : 3) * NS + 21 + 3 * L::kRaw) * 8 + 32 + kItems * sizeof(Item) <= L::kCtlBytes, "the control words' room");
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&full[s], LOAD ? 4 : 1);
       mbar_init(&empty[s], 2);  // tiles
+      if constexpr (Q8) mbar_init(&vfull[s], 4);
       hole[s] = 0;
     }
     mbar_init(qfull, 1);
     mbar_init(qready, 8);
     mbar_init(qempty, 2);
-    mbar_init(hfull, 4);
-    mbar_init(hfree, 4);
+    mbar_init(joined, 8);
     mbar_init(done, 2);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sfull[i], 1);
@@ -272,31 +354,31 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&ifull[i], 1);
-      mbar_init(&iempty[i], 10 + (LOAD ? 4 : 1));  // the issuing and the softmax warps, those that load
+      mbar_init(&iempty[i], 10 + (LOAD ? 4 : 0) + (!LOAD || Q8 ? 1 : 0));  // the issuing and the softmax warps, those that load
+    }
+    for (int i = 0; i < L::kRaw; ++i) {
+      mbar_init(&rawfull[i], 1);
+      mbar_init(&rawempty[i], 4);
     }
     *ab = 0;
-    *bad = 0;
     *holes = 0;
+    taken[0] = 0x7FFFFFFF;
+    taken[1] = -1;
     *reinterpret_cast<uint64_t*>(ctl + 4) = a.wait_ns;
     mbar_fence_init();
   }
-  // ---- the line of all work: units of every 32 sequences, their running sums, and this CTA's cuts
+  // ---- units and pairs of every 32 sequences (one warp's worth: the finding warp adds them up alone)
   const int n_chunks = (a.c.n_seqs + 31) / 32, span = 2 * a.tok;
-  int64_t* chunks = reinterpret_cast<int64_t*>(smem);  // [n_chunks + 1], and a count (before anything is copied there)
-  unsigned long long* s_items = reinterpret_cast<unsigned long long*>(chunks + n_chunks + 1);
-  if (threadIdx.x == 0) *s_items = 0;
-  __syncthreads();
-  for (int ch = warp; ch < n_chunks; ch += kWarps) {
-    Rows r{0, 0, 0};
-    if (ch * 32 + lane < a.c.n_seqs) r = rows_of(a, ch * 32 + lane, a.status);
-    int64_t n = sequence_units(a, r, lane);
-    int pairs = (r.lq + span - 1) / span;
+  Units* chunks = reinterpret_cast<Units*>(smem);  // [n_chunks] (before anything is copied there)
+  if (n_chunks > 1) {
+    for (int ch = warp; ch < n_chunks; ch += kWarps) {
+      Rows r{0, 0, 0};
+      if (ch * 32 + lane < a.c.n_seqs) r = rows_of(a, ch * 32 + lane, a.status);
+      int64_t n = sequence_units(a, r, lane);
+      const int pairs = __reduce_add_sync(0xFFFFFFFFu, (r.lq + span - 1) / span);
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, d);
-    pairs = __reduce_add_sync(0xFFFFFFFFu, pairs);
-    if (lane == 0) {
-      chunks[ch] = n;
-      atomicAdd(s_items, (unsigned long long)pairs);
+      for (int d = 16; d >= 1; d >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, d);
+      if (lane == 0) chunks[ch] = Units{n, pairs};
     }
   }
   if (warp == 9) {
@@ -307,68 +389,95 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
-  if (warp == 0) {
-    int64_t run = 0;
-    for (int ch = 0; ch <= n_chunks; ch += 32) {
-      const int64_t n = ch + lane < n_chunks ? chunks[ch + lane] : 0, sum = scan_inclusive(n, lane);
-      if (ch + lane <= n_chunks) chunks[ch + lane] = run + sum - n;
-      run += __shfl_sync(0xFFFFFFFFu, sum, 31);
-    }
-  }
-  __syncthreads();
-  const int64_t total = chunks[n_chunks] * a.c.n_kv_heads;
-  const int parts = chunk_parts(total, (int64_t)*s_items * a.c.n_kv_heads, gridDim.x);
-  if (warp < 2) {
-    const int c = (int)blockIdx.x + warp;
-    const Place p = find_place(a, chunks, n_chunks, c >= parts ? total : split_begin(total, parts, c), lane);
-    if (lane == 0) s_cut[warp] = p;
-  }
-  fence_async_smem();  // (the sums have been read before copies take their place)
-  __syncthreads();
   int32_t never = 0;
+  auto wait = [&](uint64_t* b, uint32_t parity) {
+    if constexpr (LOAD) return mbar_wait_warp_inline(b, parity, ab);
+    else return mbar_wait_warp(b, parity, ab);
+  };
+  auto take_out = [&](int kb) {  // (rare)
+    atomicMin(&taken[0], kb);
+    atomicMax(&taken[1], kb);
+  };
 
   if (warp >= 8 && warp < 12) {
+    if constexpr (LOAD) give_registers<kIssueRegs>();
     if (warp == 10) {
       // ---- finds the pieces of work of this CTA's range and asks for their queries
-      Place p = s_cut[0];
-      const Place end = s_cut[1];
+      Finder f(a, lane);
+      const int hkv = a.c.n_kv_heads;
+      int64_t head_units = 0;  // of one KV head's line
+      int32_t pairs = 0;
+      if (n_chunks == 1) {
+        f.hold(0, a.status);
+        f.add_up();
+        head_units = __shfl_sync(0xFFFFFFFFu, f.upto, 31);
+        pairs = __reduce_add_sync(0xFFFFFFFFu, f.pairs());
+      } else {
+        for (int ch = lane; ch < n_chunks; ch += 32) head_units += chunks[ch].units, pairs += chunks[ch].pairs;
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) head_units += __shfl_xor_sync(0xFFFFFFFFu, head_units, d);
+        pairs = __reduce_add_sync(0xFFFFFFFFu, pairs);
+      }
+      const int parts = chunk_parts(head_units * hkv, (int64_t)pairs * hkv, gridDim.x);
+      // the cut in front of CTA c: hkv x head_units x c / parts units from the line's start
+      auto cut_at = [&](int c) {
+        if (c >= parts) return Place{hkv, 0, 0, 0};
+        const int h = hkv * c / parts;
+        int64_t x = (int64_t)((uint64_t)head_units * (uint32_t)(hkv * c - h * parts) / (uint32_t)parts);
+        int ch = 0;
+        if (n_chunks > 1) {
+          for (; ch + 1 < n_chunks; ch += 32) {  // 32 chunks at a time
+            const int64_t n = ch + lane < n_chunks ? chunks[ch + lane].units : 0, sum = scan_inclusive(n, lane);
+            const int k = __popc(__ballot_sync(0xFFFFFFFFu, sum <= x));
+            if (k < 32) {
+              x -= __shfl_sync(0xFFFFFFFFu, sum - n, k);
+              ch += k;
+              break;
+            }
+            x -= __shfl_sync(0xFFFFFFFFu, sum, 31);
+          }
+          ch = min(ch, n_chunks - 1);
+          f.hold(ch, nullptr);
+          f.add_up();
+        }
+        return f.place(h, x);
+      };
+      const Place end = cut_at((int)blockIdx.x + 1);
+      Place p = cut_at((int)blockIdx.x);
+      fence_async_smem();  // (the sums have been read before copies take their place)
       ChunkMeta left{};
       int published = 0, nq = 0;
       bool ok = true;
-      Rows r{0, 0, 0};
-      int pairs = 0;
-      auto enter = [&]() {  // the sequence p.b
-        if (p.b < a.c.n_seqs) r = rows_of(a, p.b, nullptr);
-        else r = Rows{0, 0, 0};
-        pairs = (r.lq + span - 1) / span;
-      };
-      auto before_end = [&]() {
-        return p.b != end.b ? p.b < end.b : p.t != end.t ? p.t < end.t : p.h != end.h ? p.h < end.h : p.j < end.j;
-      };
-      enter();
-      while (ok && p.b < a.c.n_seqs && before_end()) {
-        if (p.t >= pairs) {  // the next sequence with rows
-          p.t = p.h = p.j = 0;
+      Rows r = shfl_rows(f.mine, p.b & 31);
+      pairs = (r.lq + span - 1) / span;
+      while (ok && head_units > 0 && p.before(end)) {
+        if (p.t >= pairs) {  // the next sequence with rows, or the next head
+          p.t = p.j = 0;
           int b = p.b + 1;
-          while (b < a.c.n_seqs) {
-            const bool some = b + lane < a.c.n_seqs && rows_of(a, b + lane, nullptr).lq > 0;
-            const uint32_t m = __ballot_sync(0xFFFFFFFFu, some);
+          while (true) {
+            if (b >= a.c.n_seqs) {
+              b = 0;
+              if (++p.h >= hkv) break;
+            }
+            f.hold(b >> 5, nullptr);
+            const uint32_t m = __ballot_sync(0xFFFFFFFFu, f.mine.lq > 0) >> (b & 31);
             if (m) {
               b += __ffs(m) - 1;
               break;
             }
-            b += 32;
+            b = (b | 31) + 1;
           }
-          p.b = min(b, a.c.n_seqs);
-          enter();
+          p.b = b;
+          r = shfl_rows(f.mine, p.b & 31);
+          pairs = (r.lq + span - 1) / span;
           continue;
         }
         const int n = pair_blocks(a, r, p.t);
-        const bool here = p.b == end.b && p.t == end.t && p.h == end.h;
+        const bool here = p.h == end.h && p.b == end.b && p.t == end.t;
         const int i1 = here ? min(end.j, n) : n;
         if (p.j < i1 || n == 0) {
           const int s = published % kItems;
-          if (published >= kItems && !(ok = mbar_wait_warp(&iempty[s], (published / kItems - 1) & 1, ab))) break;
+          if (published >= kItems && !(ok = wait(&iempty[s], (published / kItems - 1) & 1))) break;
           const bool before = p.j > 0, behind = i1 < n;
           const Item w{r.q0, r.lq, r.len, p.b, p.t * span, p.h, p.j, i1, before ? 0 : behind ? 1 : -1, 0};
           if (before) left.first = behind ? 1 : 2;
@@ -385,24 +494,28 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
           }
           ++published;
           if (i1 > p.j) {
-            if (nq > 0 && !(ok = mbar_wait_warp(qempty, (nq - 1) & 1, ab))) break;
+            if (nq > 0 && !(ok = wait(qempty, (nq - 1) & 1))) break;
             if (lane == 0) {
-              const int tiles = w.half(a.tok) ? 1 : 2;
-              mbar_arrive_expect_tx(qfull, (uint32_t)(tiles * a.tok * a.group) * 128 * (HD / 64));
-              for (int t = 0; t < tiles; ++t)
+              // (a quarter of a tile four times, or the item's tiles)
+              const bool quarter = w.quarter(a.few);
+              const int boxes = quarter ? 4 : w.half(a.tok) ? 1 : 2, tok = quarter ? a.few : a.tok;
+              const uint32_t step = quarter ? 32 * 128 : L::kQTile;
+              mbar_arrive_expect_tx(qfull, (uint32_t)(boxes * tok * a.group) * 128 * (HD / 64));
+              for (int t = 0; t < boxes; ++t)
                 for (int c = 0; c < HD / 64; ++c)
-                  tma_load_3d(Qs + t * L::kQTile + c * L::kQBlock, &mq, c * 64, w.h * a.group, w.q0 + w.t0 + t * a.tok, qfull);
+                  tma_load_3d(Qs + t * step + c * L::kQBlock, quarter ? &mf : &mq, c * 64, w.h * a.group,
+                              w.q0 + w.t0 + (quarter ? 0 : t * a.tok), qfull);
             }
             ++nq;
             __syncwarp();
           }
         }
         p.j = 0;
-        if (++p.h == a.c.n_kv_heads) p.h = 0, ++p.t;
+        ++p.t;
       }
       if (ok) {
         const int s = published % kItems;
-        ok = published < kItems || mbar_wait_warp(&iempty[s], (published / kItems - 1) & 1, ab);
+        ok = published < kItems || wait(&iempty[s], (published / kItems - 1) & 1);
         if (ok && lane == 0) {
           items[s].stop = 1;
           mbar_arrive(&ifull[s]);
@@ -425,7 +538,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
         uint32_t dirty = 0;  // slots whose positions without a page have been said
         for (int it = 0; ok; ++it) {
           const int is = it % kItems;
-          if (!(ok = mbar_wait_warp(&ifull[is], (it / kItems) & 1, ab))) break;
+          if (!(ok = wait(&ifull[is], (it / kItems) & 1))) break;
           const Item w = items[is];
           __syncwarp();
           if (lane == 0) mbar_arrive(&iempty[is]);
@@ -433,16 +546,12 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
           const int last = w.last(span);
           const ChunkSpan sp = chunk_span(w.first(), last, a.window, a.sinks);
           const int32_t* trow = a.c.table + (int64_t)w.b * a.c.table_width;
-          auto page_of = [&](int i) {  // of this lane's box: -2 where nothing of it is seen, -1 where it has no place
-            const int pos = chunk_block(sp, i) * kKeys + bi * box;
-            if (pos > last || (pos + box <= sp.low && pos >= a.sinks)) return -2;
-            return paged_page(trow, a.c.table_width, a.c.n_pages, a.c.log2_page, pos);
-          };
-          int next = w.i0 < w.i1 ? page_of(w.i0) : -2;
+          int next = w.i0 < w.i1 ? table_entry(a, trow, chunk_block(sp, w.i0) * kKeys + bi * box) : 0;
           for (int i = w.i0; i < w.i1; ++i) {
-            const int page = next, s = g % NS;
-            if (i + 1 < w.i1) next = page_of(i + 1);
-            if (g >= NS && !(ok = mbar_wait_warp(&empty[s], (g / NS - 1) & 1, ab))) break;
+            const int pos = chunk_block(sp, i) * kKeys + bi * box, s = g % NS;
+            const int page = page_of(a, next, pos, box, sp.low, last);
+            if (i + 1 < w.i1) next = table_entry(a, trow, chunk_block(sp, i + 1) * kKeys + bi * box);
+            if (g >= NS && !(ok = wait(&empty[s], (g / NS - 1) & 1))) break;
             const uint32_t out = __ballot_sync(0xFFFFFFFFu, page == -1) & (boxes == 32 ? ~0u : (1u << boxes) - 1);
             if (out || ((dirty >> s) & 1)) {
               if (lane == 0) {
@@ -460,7 +569,6 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
             if (lane == 0) mbar_arrive_expect_tx(&full[s], L::kPair);
             __syncwarp();
             if (on) {
-              const int pos = chunk_block(sp, i) * kKeys + bi * box;
               // (a page number behind the pool: zeros)
               tma_load_4d(ring + s * L::kPair + to, is_v ? &mv : &mk, col * 64, pos & ((1 << a.c.log2_page) - 1), w.h,
                           page < 0 ? a.c.n_pages : page, &full[s]);
@@ -472,6 +580,91 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
         if (!ok) *ab = 1;
         if (lane == 0)
           for (int i = g > NS ? g - NS : 0; i < g; ++i) mbar_wait(&full[i % NS], (i / NS) & 1, &never, a.wait_ns);
+        __syncwarp();
+      } else if constexpr (Q8) {
+        // ---- copies blocks of codes of K, then of V, with their scales: the rows of a page and head are consecutive
+        constexpr int R = L::kRaw;
+        const int lg = min(a.c.log2_page, 6), box = 1 << lg, boxes = kKeys >> lg, in_page = (1 << a.c.log2_page) - 1;
+        const uint32_t raw = smem_u32(smem + L::kRawAt);
+        int g = 0;  // blocks of K or of V so far
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+          const int is = it % kItems;
+          if (!(ok = wait(&ifull[is], (it / kItems) & 1))) break;
+          const Item w = items[is];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&iempty[is]);
+          if (w.stop) break;
+          const int last = w.last(span);
+          const ChunkSpan sp = chunk_span(w.first(), last, a.window, a.sinks);
+          const int32_t* trow = a.c.table + (int64_t)w.b * a.c.table_width;
+          // 32 entries of the table row at a time, a lane's at entry base + lane
+          int base = -64, held = 0;
+          for (int i = w.i0; ok && i < w.i1; ++i) {
+            const int kb = chunk_block(sp, i) * kKeys;
+            int page[2] = {-2, -2}, at[2] = {0, 0};  // of this lane's boxes
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              if (k * 32 >= boxes) continue;
+              const int c = min(lane + 32 * k, boxes - 1), pos = kb + c * box, index = pos >> a.c.log2_page;
+              const int lo = (kb + k * 32 * box) >> a.c.log2_page, hi = (kb + (min(boxes, k * 32 + 32) - 1) * box) >> a.c.log2_page;
+              if (lo < base || hi >= base + 32) {
+                base = lo;
+                held = __ldg(trow + min(base + lane, a.c.table_width - 1));
+              }
+              const int entry = __shfl_sync(0xFFFFFFFFu, held, index - base);
+              at[k] = pos & in_page;
+              page[k] = lane + 32 * k < boxes ? page_of(a, entry, pos, box, sp.low, last) : -2;
+            }
+            uint64_t out = 0;  // positions without a place
+            if (__any_sync(0xFFFFFFFFu, page[0] == -1 || page[1] == -1)) {
+              const uint32_t o0 = __ballot_sync(0xFFFFFFFFu, page[0] == -1), o1 = __ballot_sync(0xFFFFFFFFu, page[1] == -1);
+              for (int c = 0; c < boxes; ++c)
+                if (((c < 32 ? o0 : o1) >> (c & 31)) & 1) out |= (box == 64 ? ~0ull : (1ull << box) - 1) << (c * box);
+              if (lane == 0) {
+                *holes = 1;
+                report(a.status, ADP_ERR_INVALID_ARG);
+              }
+            }
+#pragma unroll 1
+            for (int op = 0; op < 2; ++op, ++g) {
+              const int s = g % R;
+              if (g >= R && !(ok = wait(&rawempty[s], (g / R - 1) & 1))) break;
+              const uint8_t* const codes = op ? a.c.v : a.c.k;
+              const float* const scales = op ? a.c.v_scale : a.c.k_scale;
+              const uint32_t to = raw + s * L::kRawBytes;
+              if (lane == 0) rawhole[s] = out;
+              if (!a.even_scales) {
+#pragma unroll 1
+                for (int r = lane; r < kKeys; r += 32) {
+                  const int pos = kb + r, e = page_of(a, table_entry(a, trow, pos), pos, 1, sp.low, last);
+                  reinterpret_cast<float*>(smem + L::kRawAt + s * L::kRawBytes + kKeys * HD)[r] =
+                      e < 0 ? 0.0f : scales[(int64_t)e * a.c.scale_stride + (w.h << a.c.log2_page) + (pos & in_page)];
+                }
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive_expect_tx(&rawfull[s], kKeys * HD + (a.even_scales ? kKeys * 4 : 0));
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int c = lane + 32 * k;
+                if (c >= boxes) continue;
+                const int64_t cell = (w.h << a.c.log2_page) + at[k];
+                bulk_load(to + c * box * HD,
+                          page[k] < 0 ? reinterpret_cast<const uint8_t*>(zero_codes) : codes + (int64_t)page[k] * a.c.page_bytes + cell * HD,
+                          box * HD, &rawfull[s]);
+                if (a.even_scales)
+                  bulk_load(to + kKeys * HD + c * box * 4,
+                            page[k] < 0 ? reinterpret_cast<const float*>(zero_codes) : scales + (int64_t)page[k] * a.c.scale_stride + cell,
+                            box * 4, &rawfull[s]);
+              }
+              __syncwarp();
+            }
+          }
+        }
+        if (!ok) *ab = 1;
+        if (lane == 0)
+          for (int i = g > R ? g - R : 0; i < g; ++i) mbar_wait(&rawfull[i % R], (i / R) & 1, &never, a.wait_ns);
         __syncwarp();
       }
     } else {
@@ -485,13 +678,13 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
       const uint32_t k_lo = (smem_u32(ring) >> 4) | (1u << 16);
       const uint32_t v_lo = ((smem_u32(ring) + L::kTile) >> 4) | ((L::kBlock >> 4) << 16);
       const uint32_t tS = tmem + t * 128, tO = tmem + 256 + t * 128;
-      uint32_t ks = 0, kphase = 0, vs = 0;  // the ring's next block, and the slot of the next own block to weigh
+      uint32_t ks = 0, kphase = 0, vs = 0, vphase = 0;  // the ring's next block, and the next own block to weigh
       uint32_t s_buf = 0, s_phase = 0, p_buf = 0, p_phase = 0, q_phase = 0;
       bool ok = true;
 #pragma unroll 1
       for (int it = 0; ok; ++it) {
         const int is = it % kItems;
-        if (!(ok = mbar_wait_warp(&ifull[is], (it / kItems) & 1, ab))) break;
+        if (!(ok = wait(&ifull[is], (it / kItems) & 1))) break;
         const Item w = items[is];
         __syncwarp();
         if (elect_one()) mbar_arrive(&iempty[is]);
@@ -501,13 +694,15 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
         if (n == 0) continue;
         const Own own = own_blocks(w, chunk_span(w.first(), w.last(span), a.window, a.sinks), t, a.tok);
         const uint32_t q_lo = q_lo0 + (w.half(a.tok) ? 0 : t * (L::kQTile >> 4));
-        if (!(ok = mbar_wait_warp(QCONV ? qready : qfull, q_phase, ab))) break;
+        if (!(ok = wait(QCONV ? qready : qfull, q_phase))) break;
         q_phase ^= 1;
         int at = 0;  // blocks of the item that have been waited for
-        vs = (ks + own.off) % NS;
-        // the next block of the item, which is this tile's or not (then it is freed)
+        vs = ks + own.off;
+        vphase = kphase;
+        if (vs >= NS) vs -= NS, vphase ^= 1;
+        // the next block of the item is not this tile's: it is freed once it is there
         auto skip = [&]() {
-          if (!mbar_wait_warp(&full[ks], kphase, ab)) return false;
+          if (!wait(&full[ks], kphase)) return false;
           if (elect_one()) mbar_arrive(&empty[ks]);
           __syncwarp();
           ++at;
@@ -519,7 +714,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
           const int i = own.off + k * own.step;
           while (at < i)
             if (!skip()) return false;
-          if (!mbar_wait_warp(&full[ks], kphase, ab) || !mbar_wait_warp(&odone[2 * t + s_buf], s_phase ^ 1, ab)) return false;
+          if (!wait(&full[ks], kphase) || !wait(&odone[2 * t + s_buf], s_phase ^ 1)) return false;
           const uint32_t b = k_lo + ks * (L::kPair >> 4), d = tS + s_buf * 64;
           tc_fence_after();
           if (elect_one()) {
@@ -537,16 +732,28 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
           if (++ks == NS) ks = 0, kphase ^= 1;
           return true;
         };
-        if (own.n > 0) {
-          if (!(ok = score(0))) break;
-        } else {
+        if (own.n == 0) {
           if (elect_one()) mbar_arrive(qempty);
           __syncwarp();
         }
+        // The next block's scores go in front of this one's product where its K is there: else the product comes first, for
+        // the slot that the other block waits for may be this one's.
+        int scored = 0;
 #pragma unroll 1
         for (int k = 0; k < own.n; ++k) {
-          if (k + 1 < own.n && !(ok = score(k + 1))) break;
-          if (!(ok = mbar_wait_warp(&pready[2 * t + p_buf], p_phase, ab))) break;
+          if (scored == k && !(ok = score(scored++))) break;
+          if (scored < own.n) {
+            bool there = true;
+            while (there && at < own.off + scored * own.step) {
+              there = __all_sync(0xFFFFFFFFu, mbar_test_wait(&full[ks], kphase));
+              if (there) skip();
+            }
+            if (there && __all_sync(0xFFFFFFFFu, mbar_test_wait(&full[ks], kphase)) && !(ok = score(scored++))) break;
+          }
+          if (!(ok = wait(&pready[2 * t + p_buf], p_phase))) break;
+          if constexpr (Q8) {
+            if (!(ok = wait(&vfull[vs], vphase))) break;
+          }
           tc_fence_after();
           const uint32_t b = v_lo + vs * (L::kPair >> 4), p = tS + p_buf * 64;
           if (elect_one()) {
@@ -559,7 +766,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
           p_phase ^= p_buf;
           p_buf ^= 1;
           vs += own.step;
-          if (vs >= NS) vs -= NS;
+          if (vs >= NS) vs -= NS, vphase ^= 1;
         }
         while (ok && at < n) ok = skip();
       }
@@ -569,179 +776,219 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
     }
   } else if (warp >= 12) {
     if constexpr (LOAD) {
-      // ---- four warps that load: consecutive lanes take consecutive 16-byte pieces of a row
-      constexpr int EB = elem_bytes(CDT), PPR = HD * EB / 16, RSTEP = 128 / PPR, NR = kKeys / RSTEP;
-      constexpr int kAhead = Q8 ? L::kRaw - 1 : 2;
-      const int lt = threadIdx.x - 384, piece = lt % PPR, row0 = lt / PPR;
-      uint8_t* const raw = smem + L::kRawAt;
-      int g = 0, landed = 0;     // blocks asked for, and those handed over
-      uint32_t edges = 0, gaps = 0;  // of the blocks under way, the last one lowest: edge blocks; this thread's row has no place
+      give_registers<kLoadRegs>();
+      const int lt = threadIdx.x - 384;
       bool ok = true;
-      auto wait_slot = [&](int n) { return n < NS || mbar_wait_warp(&empty[n % NS], (n / NS - 1) & 1, ab); };
-      // The oldest block under way: its copies have ended for this thread.
-      auto hand_over = [&]() {
-        const int s = landed % NS, age = g - 1 - landed;
-        if constexpr (Q8) {
-          if (!wait_slot(landed)) return false;
-          const uint8_t* from = raw + (landed % L::kRaw) * L::kRawBytes;
-          const bool edge = (edges >> age) & 1;
-          bool taken = false;
+      auto wait_slot = [&](int n) { return n < NS || wait(&empty[n % NS], (n / NS - 1) & 1); };
+      // positions of a block without a place, said by the warps that hold its rows
+      auto say_holes = [&](int s, bool gap) {
+        if (warp >= 14) return;
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, gap);
+        if (lane == 0) {
+          reinterpret_cast<uint32_t*>(&hole[s])[warp - 12] = m;
+          if (m) {
+            *holes = 1;
+            report(a.status, ADP_ERR_INVALID_ARG);
+          }
+        }
+      };
+      if constexpr (Q8) {
+        // ---- four warps that bring codes to fp16 (exactly) in the ring, and the rows' scales beside them
+        constexpr int PPR = HD / 16, RSTEP = 128 / PPR, NR = kKeys / RSTEP, R = L::kRaw;  // 16-byte pieces of a row; rows of this thread
+        // (head_dim 128: half a row of an even and of an odd position to every 8 lanes, so that their stores meet in no bank)
+        const int piece = HD == 128 ? ((lane >> 3) & 1) * 4 + (lane & 3) : lane & 3;
+        const int row0 = HD == 128 ? (warp - 12) * 4 + (lane >> 4) * 2 + ((lane >> 2) & 1) : (warp - 12) * 8 + (lane >> 2);
+        const uint32_t raw = smem_u32(smem + L::kRawAt) + row0 * HD + piece * 16;
+        const uint32_t to = smem_u32(ring) + (2 * piece / 8) * L::kBlock + row0 * 128;
+        const uint32_t to0 = to + (((2 * piece & 7) ^ (row0 & 7)) << 4), to1 = to + (((2 * piece + 1 & 7) ^ (row0 & 7)) << 4);
+        int g = 0, slot = 0, rs = 0;  // blocks so far, their slot, and the next one of codes
+        uint32_t raw_phase = 0;
+        for (int it = 0; ok; ++it) {
+          const int is = it % kItems;
+          if (!(ok = wait(&ifull[is], (it / kItems) & 1))) break;
+          const Item w = items[is];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&iempty[is]);
+          if (w.stop) break;
+          const int first = w.first(), last = w.last(span);
+          const bool quarter = w.quarter(a.few);
+          const ChunkSpan sp = chunk_span(first, last, a.window, a.sinks);
+          for (int i = w.i0; ok && i < w.i1; ++i, ++g) {
+            const int kb = chunk_block(sp, i) * kKeys;
+            const bool edge = quarter || edge_block(kb, first, last, a.window, a.sinks);
+            SlotScales& z = s_scale[slot];
+#pragma unroll 1
+            for (int op = 0; op < 2; ++op) {  // K, V
+              if (!(ok = wait(&rawfull[rs], raw_phase))) break;
+              uint4 c[NR];
 #pragma unroll
-          for (int n = 0; n < 2 * NR; ++n) {
-            uint4 w = *reinterpret_cast<const uint4*>(from + (n * 128 + lt) * 16);
-            uint32_t* u = reinterpret_cast<uint32_t*>(&w);
-            if (edge && n >= NR) {
-              uint32_t nan = 0;
+              for (int n = 0; n < NR; ++n)
+                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(c[n].x), "=r"(c[n].y), "=r"(c[n].z), "=r"(c[n].w)
+                             : "r"(raw + rs * L::kRawBytes + n * RSTEP * HD));
+              float sc = 0.0f;
+              const bool mine = lt < kKeys;
+              if (mine) sc = reinterpret_cast<const volatile float*>(smem + L::kRawAt + rs * L::kRawBytes + kKeys * HD)[lt];
+              const uint64_t out = rawhole[rs];
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&rawempty[rs]);
+              if (++rs == R) rs = 0, raw_phase ^= 1;
+              if (op == 0 && !(ok = wait_slot(g))) break;
+              if (edge) {  // values that are not numbers must not meet weights of zero; behind the last row lies anything
+                if (kb + lt > last) sc = 0.0f;
+                bool some = false;
+                if (op == 1) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) nan |= (u[e] & 0x7F7F7F7Fu) + 0x01010101u;
-              if (nan & 0x80808080u) {
-                taken = true;
+                  for (int n = 0; n < NR; ++n) {
+                    uint32_t* u = reinterpret_cast<uint32_t*>(&c[n]);
+                    uint32_t nan = 0;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                    for (int e = 0; e < 4; ++e) nan |= (u[e] & 0x7F7F7F7Fu) + 0x01010101u;
+                    if (nan & 0x80808080u) {
+                      some |= kb + row0 + n * RSTEP <= last;
 #pragma unroll
-                  for (int k = 0; k < 32; k += 8)
-                    if (((u[e] >> k) & 0x7Fu) == 0x7Fu) u[e] &= ~(0xFFu << k);
+                      for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8)
+                          if (((u[e] >> k) & 0x7Fu) == 0x7Fu) u[e] &= ~(0xFFu << k);
+                    }
+                  }
+                  if (!isfinite(sc)) sc = 0.0f, some = true;
+                }
+                if (some) take_out(kb);
               }
+#pragma unroll
+              for (int n = 0; n < NR; ++n) {
+                const uint32_t at = slot * L::kPair + op * L::kTile + n * RSTEP * 128;
+                uint32_t f[8];
+                e4m3x4_to_f16(c[n].x, f[0], f[1]);
+                e4m3x4_to_f16(c[n].y, f[2], f[3]);
+                e4m3x4_to_f16(c[n].z, f[4], f[5]);
+                e4m3x4_to_f16(c[n].w, f[6], f[7]);
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to0 + at), "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3]) : "memory");
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to1 + at), "r"(f[4]), "r"(f[5]), "r"(f[6]), "r"(f[7]) : "memory");
+              }
+              if (mine) {
+                if (op == 0) {
+                  z.k[lt] = sc;
+                  if (lt == 0) hole[slot] = out;
+                } else {
+                  const float lv = log2_scale_of(sc);
+                  z.v[lt] = sc;
+                  z.lv[lt] = lv;
+                  float top = lv;
+#pragma unroll
+                  for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                  if (lane == 0) z.top[warp - 12] = top;
+                }
+              }
+              fence_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(op ? &vfull[slot] : &full[slot]);
             }
-            uint32_t f[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) f[2 * e] = e4m3x2_to_f16x2(u[e]), f[2 * e + 1] = e4m3x2_to_f16x2(u[e] >> 16);
-            const int row = row0 + (n % NR) * RSTEP;
-            uint8_t* to = ring + s * L::kPair + (n >= NR ? L::kTile : 0) + row * 128;
-            // (lanes of the second 64 elements store their odd piece first: no two of a row's lanes meet in a bank)
-            const int odd = HD == 128 ? piece >> 2 : 0;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int q = 2 * piece + (k ^ odd);
-              const uint4 v = (k ^ odd) ? make_uint4(f[4], f[5], f[6], f[7]) : make_uint4(f[0], f[1], f[2], f[3]);
-              *reinterpret_cast<uint4*>(to + (q >> 3) * L::kBlock + (((q & 7) ^ (row & 7)) << 4)) = v;
-            }
-          }
-          float sc = *reinterpret_cast<const float*>(from + 2 * kKeys * HD + lt * 4);
-          SlotScales& z = s_scale[s];
-          if (lt < kKeys) {
-            z.k[lt] = sc;
-          } else {
-            if (edge && !isfinite(sc)) sc = 0.0f, taken = true;
-            const float lv = log2_scale_of(sc);
-            z.v[lt - kKeys] = sc;
-            z.lv[lt - kKeys] = lv;
-            float top = lv;
-#pragma unroll
-            for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-            if (lane == 0) z.top[warp - 14] = top;
-          }
-          if (taken) *bad = 1;
-        }
-        if (warp < 14) {  // positions of the block without a place
-          const uint32_t m = __ballot_sync(0xFFFFFFFFu, (gaps >> age) & 1);
-          if (lane == 0) {
-            reinterpret_cast<uint32_t*>(&hole[s])[warp - 12] = m;
-            if (m) *holes = 1;
+            if (!ok) break;
+            if (++slot == NS) slot = 0;
           }
         }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[s]);
-        ++landed;
-        return true;
-      };
-      auto flush = [&]() {
-        cp_async_wait<0>();
-        while (landed < g)
-          if (!hand_over()) return false;
-        return true;
-      };
-      for (int it = 0; ok; ++it) {
-        const int is = it % kItems;
-        // (a piece of work that is not known yet may wait for the blocks under way)
-        if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(&ifull[is], (it / kItems) & 1)))
-          if (!(ok = flush() && mbar_wait_warp(&ifull[is], (it / kItems) & 1, ab))) break;
-        const Item w = items[is];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&iempty[is]);
-        if (w.stop) break;
-        const int first = w.first(), last = w.last(span);
-        const ChunkSpan sp = chunk_span(first, last, a.window, a.sinks);
-        const int32_t* trow = a.c.table + (int64_t)w.b * a.c.table_width;
-        const int in_page = (1 << a.c.log2_page) - 1;
-        auto page_of = [&](int pos) {  // -2 where it is not seen by any row, -1 where it has no place
-          if (pos > last || (pos < sp.low && pos >= a.sinks)) return -2;
-          return paged_page(trow, a.c.table_width, a.c.n_pages, a.c.log2_page, pos);
+      } else {
+        // ---- four warps that copy rows of 16-bit pages too small for tensor copies: consecutive lanes take consecutive
+        // 16-byte pieces of a row
+        constexpr int PPR = HD / 8, RSTEP = 128 / PPR, NR = kKeys / RSTEP, kAhead = NS >= 5 ? 2 : 1;
+        // block g waits for the slot of block g - NS, whose product is issued behind the scores of its tile's next block
+        // (g - NS + 2 where tiles take turns): those under way must all lie behind that one
+        static_assert(kAhead <= NS - 3, "");
+        const int piece = lt % PPR, row0 = lt / PPR;
+        int g = 0, landed = 0;  // blocks asked for, and those handed over
+        uint32_t gaps = 0;      // of the blocks under way, the last one lowest: this thread's row has no place
+        auto hand_over = [&]() {  // the oldest block under way: its copies have ended for this thread
+          const int s = landed % NS;
+          say_holes(s, (gaps >> (g - 1 - landed)) & 1);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[s]);
+          ++landed;
         };
-        int next[NR], next_sc = -2;
-        auto look_up = [&](int i) {
-          const int kb = chunk_block(sp, i) * kKeys;
-#pragma unroll
-          for (int n = 0; n < NR; ++n) next[n] = page_of(kb + row0 + n * RSTEP);
-          next_sc = page_of(kb + (lt & (kKeys - 1)));
+        auto flush = [&]() {
+          cp_async_wait<0>();
+          while (landed < g) hand_over();
         };
-        if (w.i0 < w.i1) look_up(w.i0);
-        for (int i = w.i0; i < w.i1; ++i) {
-          const int kb = chunk_block(sp, i) * kKeys;
-          int page[NR];
+        for (int it = 0; ok; ++it) {
+          const int is = it % kItems;
+          // (a piece of work that is not known yet may wait for the blocks under way)
+          if (!__all_sync(0xFFFFFFFFu, mbar_test_wait(&ifull[is], (it / kItems) & 1))) {
+            flush();
+            if (!(ok = wait(&ifull[is], (it / kItems) & 1))) break;
+          }
+          const Item w = items[is];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&iempty[is]);
+          if (w.stop) break;
+          const int last = w.last(span), in_page = (1 << a.c.log2_page) - 1;
+          const ChunkSpan sp = chunk_span(w.first(), last, a.window, a.sinks);
+          const int32_t* trow = a.c.table + (int64_t)w.b * a.c.table_width;
+          int next[NR], next_own = 0;
+          auto look_up = [&](int i) {
+            const int kb = chunk_block(sp, i) * kKeys;
 #pragma unroll
-          for (int n = 0; n < NR; ++n) page[n] = next[n];
-          const int page_sc = next_sc;
-          if (i + 1 < w.i1) look_up(i + 1);
-          if constexpr (!Q8) {
+            for (int n = 0; n < NR; ++n) next[n] = table_entry(a, trow, kb + row0 + n * RSTEP);
+            next_own = table_entry(a, trow, kb + (lt & (kKeys - 1)));
+          };
+          if (w.i0 < w.i1) look_up(w.i0);
+          for (int i = w.i0; i < w.i1; ++i) {
+            const int kb = chunk_block(sp, i) * kKeys;
+            int page[NR];
+#pragma unroll
+            for (int n = 0; n < NR; ++n) page[n] = page_of(a, next[n], kb + row0 + n * RSTEP, 1, sp.low, last);
+            gaps = (gaps << 1) | (page_of(a, next_own, kb + (lt & (kKeys - 1)), 1, sp.low, last) == -1 ? 1u : 0u);
+            if (i + 1 < w.i1) look_up(i + 1);
             if (!(ok = wait_slot(g))) break;
-          }
-          edges = (edges << 1) | (edge_block(kb, first, last, a.window, a.sinks) ? 1u : 0u);
-          gaps = (gaps << 1) | (page_sc == -1 ? 1u : 0u);
-          if (page_sc == -1) report(a.status, ADP_ERR_INVALID_ARG);
 #pragma unroll
-          for (int n = 0; n < 2 * NR; ++n) {
-            const int row = row0 + (n % NR) * RSTEP, pg = page[n % NR];
-            const int64_t cell = (int64_t)max(pg, 0) * a.c.page_bytes +
-                                 (int64_t)((w.h << a.c.log2_page) + ((kb + row) & in_page)) * (HD * EB) + piece * 16;
-            uint32_t to;
-            if constexpr (Q8) {
-              to = smem_u32(raw + (g % (Q8 ? L::kRaw : 1)) * L::kRawBytes) + (n * 128 + lt) * 16;
-            } else {
-              to = smem_u32(ring + (g % NS) * L::kPair) + (n >= NR ? L::kTile : 0) + (piece >> 3) * L::kBlock + row * 128 +
-                   (((piece & 7) ^ (row & 7)) << 4);
+            for (int n = 0; n < 2 * NR; ++n) {
+              const int row = row0 + (n % NR) * RSTEP, pg = page[n % NR];
+              const int64_t cell = (int64_t)max(pg, 0) * a.c.page_bytes +
+                                   (int64_t)((w.h << a.c.log2_page) + ((kb + row) & in_page)) * (HD * 2) + piece * 16;
+              cp_async16(smem_u32(ring + (g % NS) * L::kPair) + (n >= NR ? L::kTile : 0) + (piece >> 3) * L::kBlock + row * 128 +
+                             (((piece & 7) ^ (row & 7)) << 4),
+                         (n >= NR ? a.c.v : a.c.k) + cell, pg >= 0);
             }
-            cp_async16(to, (n >= NR ? a.c.v : a.c.k) + cell, pg >= 0);
-          }
-          if constexpr (Q8) {
-            const float* from = lt < kKeys ? a.c.k_scale : a.c.v_scale;
-            const int64_t cell = (int64_t)max(page_sc, 0) * a.c.scale_stride + (w.h << a.c.log2_page) + ((kb + (lt & (kKeys - 1))) & in_page);
-            cp_async4(smem_u32(raw + (g % (Q8 ? L::kRaw : 1)) * L::kRawBytes) + 2 * kKeys * HD + lt * 4, from + cell, page_sc >= 0);
-          }
-          cp_async_commit();
-          ++g;
-          if (g - landed > kAhead) {
-            cp_async_wait<kAhead>();
-            if (!(ok = hand_over())) break;
+            cp_async_commit();
+            ++g;
+            if (g - landed > kAhead) {
+              cp_async_wait<kAhead>();
+              hand_over();
+            }
           }
         }
+        flush();
       }
-      if (ok) ok = flush();
       if (!ok) *ab = 1;
-      cp_async_wait<0>();
     }
   } else {
     // ---- softmax: warps 0-3 tile A, 4-7 tile B; thread = row = TMEM lane
-    const int t = warp >> 2, r = threadIdx.x & 127;
-    const int row_tok = r / a.group, row_head = r % a.group;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    if constexpr (LOAD) take_registers<kSoftmaxRegs>();
+    const int t = warp >> 2, r = threadIdx.x & 127, sub = warp & 3;
+    const uint32_t lanes = (uint32_t)(sub * 32) << 16;
     const uint32_t tS = tmem + lanes + t * 128, tO = tmem + lanes + 256 + t * 128;
     bool ok = true;
-    uint32_t ns = 0, nh = 0, nq = 0;  // own blocks, items in halves, items with queries so far
+    uint32_t ns = 0, nj = 0, nq = 0;  // own blocks, meetings of the softmax warps, items with queries so far
     uint32_t g = 0;                   // ring blocks of the items before
-    auto wait_all = [&](uint64_t* b, uint32_t parity) { return mbar_wait_warp(b, parity, ab); };
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(joined);
+      return wait(joined, nj++ & 1);
+    };
     for (int it = 0; ok; ++it) {
       const int is = it % kItems;
-      if (!(ok = wait_all(&ifull[is], (it / kItems) & 1))) break;
+      if (!(ok = wait(&ifull[is], (it / kItems) & 1))) break;
       const Item w = items[is];
       if (w.stop) break;
       const int first = w.first(), last = w.last(span), n = w.i1 - w.i0;
       const ChunkSpan sp = chunk_span(first, last, a.window, a.sinks);
       const Own own = own_blocks(w, sp, t, a.tok);
-      const bool half = w.half(a.tok);
+      const bool half = w.half(a.tok), quarter = w.quarter(a.few);
+      const int row = quarter ? lane : r, row_tok = row / a.group, row_head = row - row_tok * a.group;
       const int tok = w.t0 + (half ? 0 : t * a.tok) + row_tok;
-      const bool live = r < a.tok * a.group && tok < w.lq;
+      const bool live = row_tok < (quarter ? a.few : a.tok) && tok < w.lq;
       const bool warp_live = __any_sync(0xFFFFFFFFu, live);
       const int pos = w.len - w.lq + tok;  // this row's position: it sees keys up to it
       const int from = max(max(pos, 0) - a.window + 1, 0);  // from its window's first on, and the first ones
@@ -752,7 +999,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
         // bf16 queries meet fp16 codes: the row is brought to a largest magnitude in [1, 2) by a power of two, so that its
         // 8-bit significands fit fp16 (an element below 2^-17 loses bits: at most 2^-25, half fp16's least step)
         if (n > 0) {
-          if (!(ok = wait_all(qfull, nq & 1))) break;
+          if (!(ok = wait(qfull, nq & 1))) break;
           if (t == 0 || !half) {
             uint8_t* q = Qs + t * L::kQTile + r * 128;
             auto at = [&](int c) { return reinterpret_cast<uint4*>(q + (c / 8) * L::kQBlock + (((c & 7) ^ (r & 7)) << 4)); };
@@ -767,7 +1014,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
             }
             const uint32_t e2 = min(max(__float_as_uint(top) >> 23, 1u), 253u);
             const float inv = __uint_as_float((254u - e2) << 23);
-            if (r < a.tok * a.group) {
+            if (row_tok < (quarter ? a.few : a.tok)) {
 #pragma unroll 4
               for (int c = 0; c < HD / 8; ++c) {
                 const uint4 v = *at(c);
@@ -784,7 +1031,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
           fence_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(qready);
-          if (!(ok = wait_all(qready, nq & 1))) break;
+          if (!(ok = wait(qready, nq & 1))) break;
           // (kept finite, as the scale itself)
           scale = fminf(fmaxf(scale * s_qf[half ? r : t * kRows + r], kScaleMin), 3.40282347e38f);
           ++nq;
@@ -794,17 +1041,134 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
       // replaced (never by what stands in rows that are not the sequence's: it must not decide how the others are rounded)
       float m = -INFINITY, ms = 0.0f, l = 0.0f, limit = live ? -INFINITY : INFINITY;
       // e4m3: what weighs V's codes are the products weight x value scale, which have a running maximum of their own, mo
-      // (base-2 exponents: score + log2 of the scale); O is relative to it, and vc = 2^(m - mo) brings them there
+      // (base-2 exponents: score + log2 of the scale); O is relative to it, and vc = 2^((m - mo) / 2), twice, brings them there
       float mo = -INFINITY, vc = 1.0f;
+      // The softmax of N columns from col on of own block k, whose scores lie in buffer buf: P takes their place, 16 bits each.
+      auto block = [&](auto columns, int col, int k, uint32_t buf, int slot, int kb) {
+        constexpr int N = decltype(columns)::value;
+        float x[N];
+        if constexpr (N == kKeys) {
+          tmem_ld64(tS + buf * 64, x);
+        } else {
+          uint32_t u[N];
+          tmem_ld16(tS + buf * 64 + col, u);
+#pragma unroll
+          for (int c = 0; c < N; ++c) x[c] = __uint_as_float(u[c]);
+        }
+        [[maybe_unused]] const SlotScales& z = s_scale[Q8 ? slot : 0];
+        if constexpr (Q8) {
+#pragma unroll
+          for (int c = 0; c < N; c += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&z.k[col + c]);
+            const float2 u = __fmul2_rn(make_float2(x[c], x[c + 1]), make_float2(f.x, f.y));
+            const float2 v = __fmul2_rn(make_float2(x[c + 2], x[c + 3]), make_float2(f.z, f.w));
+            x[c] = u.x, x[c + 1] = u.y, x[c + 2] = v.x, x[c + 3] = v.y;
+          }
+        }
+        const int kc = kb + col;
+        const bool hidden = kc + N - 1 > warp_first || (kc <= warp_last - a.window && kc + N - 1 >= a.sinks);
+        if (hidden || *holes) {
+          // columns up to this row's position, from its window's first on or of the first ones, but those without a place
+          uint64_t see = below(pos - kc + 1) & (~below(from - kc) | below(a.sinks - kc));
+          if (*holes) see &= ~(*reinterpret_cast<volatile uint64_t*>(&hole[slot]) >> col);
+          const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
+#pragma unroll
+          for (int c = 0; c < N; ++c) x[c] = ((c < 32 ? lo : hi) >> (c & 31)) & 1 ? x[c] : -INFINITY;
+        }
+        float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int c = 4; c < N - 4; c += 8) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top[e] = max3(top[e], x[c + e], x[c + 4 + e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], x[N - 4 + e]);
+        const float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
+        bool grow = mx > limit;
+        if constexpr (Q8) grow |= live && mx > -INFINITY && fmaf(mx, scale, fmaxf(z.top[0], z.top[1])) > mo + kRescale;
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+          const float mn = live && mx > -INFINITY ? fmaxf(m, mx * scale) : m;
+          float f = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
+          m = mn;
+          ms = m == -INFINITY ? 0.0f : m - kWeightUp<BF>;
+          l *= f;
+          if (live && m > -INFINITY) limit = (m + kRescale) / scale;
+          if constexpr (Q8) {  // (both maxima at once: mo is m - 126 at least, and vc finite)
+            float mw = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < N; c += 4) {
+              const float4 lv = *reinterpret_cast<const float4*>(&z.lv[col + c]);
+              mw = fmaxf(fmaxf(mw, fmaf(x[c], scale, lv.x)), fmaf(x[c + 1], scale, lv.y));
+              mw = fmaxf(fmaxf(mw, fmaf(x[c + 2], scale, lv.z)), fmaf(x[c + 3], scale, lv.w));
+            }
+            mw = live ? fmaxf(mo, mw) : mo;
+            f = mw == -INFINITY ? 1.0f : exp2_fast(mo - mw);
+            mo = mw;
+            vc = mw == -INFINITY ? 1.0f : exp2_fast(0.5f * (m - mw));
+          }
+          if (k > 0) {
+            // own block k - 1's product must be in O
+            if (!wait(&odone[2 * t + (buf ^ 1)], ((ns - 1) >> 1) & 1)) return false;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < HD; c0 += 32) {
+              float o[32];
+              tmem_ld32(tO + c0, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= f;
+              tmem_st32(tO + c0, o);
+            }
+          }
+        }
+        const float2 sc = make_float2(scale, scale), nm = make_float2(-ms, -ms);
+        [[maybe_unused]] const float2 vc2 = make_float2(vc, vc);
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        constexpr int NS2 = N < 32 ? N : 32;
+#pragma unroll
+        for (int c0 = 0; c0 < N; c0 += NS2) {
+          uint32_t u[NS2 / 2];
+#pragma unroll
+          for (int e = 0; e < NS2; e += 4) {
+            [[maybe_unused]] float4 f;
+            if constexpr (Q8) f = *reinterpret_cast<const float4*>(&z.v[col + c0 + e]);
+#pragma unroll
+            for (int d = 0; d < 4; d += 2) {
+              const float2 y = __ffma2_rn(make_float2(x[c0 + e + d], x[c0 + e + d + 1]), sc, nm);
+              float2 p = make_float2(exp2_fast(y.x), exp2_fast(y.y));  // (0 where x is -infinity: not seen)
+              sum[d >> 1] = __fadd2_rn(sum[d >> 1], p);
+              if constexpr (Q8)  // (in this order nothing that counts leaves fp32's range)
+                p = __fmul2_rn(__fmul2_rn(__fmul2_rn(p, vc2), d ? make_float2(f.z, f.w) : make_float2(f.x, f.y)), vc2);
+              u[(e + d) >> 1] = pack2(p.x, p.y, BF ? DT_BF16 : DT_F16);
+            }
+          }
+          if constexpr (N == kKeys) {
+            tmem_st16(tS + buf * 64 + c0 / 2, u);
+          } else {  // the other warps have the other positions: weights of zero here
+            const uint32_t none[8] = {};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (q != sub) tmem_st8(tS + buf * 64 + q * 8, none);
+            tmem_st8(tS + buf * 64 + sub * 8, u);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        return true;
+      };
       for (int k = 0; k < own.n; ++k, ++ns) {
         const uint32_t buf = ns & 1;
         const int i = own.off + k * own.step;
-        if (!(ok = wait_all(&sfull[2 * t + buf], (ns >> 1) & 1))) break;
+        if (!(ok = wait(&sfull[2 * t + buf], (ns >> 1) & 1))) break;
         tc_fence_after();
         __syncwarp();
         const int slot = (g + i) % NS, kb = chunk_block(sp, w.i0 + i) * kKeys;
-        // ---- an edge block's values in 16 bits, looked through by the tiles that weigh them (they take out the same)
-        if (!Q8 && edge_block(kb, first, last, a.window, a.sinks)) {
+        if constexpr (Q8) {  // (the scales of V come with V)
+          if (!(ok = wait(&vfull[slot], ((g + i) / NS) & 1))) break;
+        }
+        // ---- an edge block's values in 16 bits, looked through by the tiles that weigh them (they take out the same; and
+        // every block's where some warps' weights are zero)
+        if (!Q8 && (quarter || edge_block(kb, first, last, a.window, a.sinks))) {
           uint8_t* vt = ring + slot * L::kPair + L::kTile;
           const int key = r >> 1;  // two threads to a key
           auto piece = [&](int c) {
@@ -823,7 +1187,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
               over |= ((v.x & kExp2) + kOne2) | ((v.y & kExp2) + kOne2) | ((v.z & kExp2) + kOne2) | ((v.w & kExp2) + kOne2);
             }
             if (over & 0x80008000u) {
-              *bad = 1;
+              take_out(kb);
 #pragma unroll 1
               for (int c = r & 1; c < HD / 8; c += 2) {
                 uint4 v = *piece(c);
@@ -839,201 +1203,154 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
           __syncwarp();
         }
         if (warp_live) {
-          float x[kKeys];
-          tmem_ld64(tS + buf * 64, x);
-          const SlotScales& z = s_scale[Q8 ? slot : 0];
-          if constexpr (Q8) {
-#pragma unroll
-            for (int c = 0; c < kKeys; c += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(&z.k[c]);
-              x[c] *= f.x, x[c + 1] *= f.y, x[c + 2] *= f.z, x[c + 3] *= f.w;
-            }
-          }
-          if (kb + kKeys - 1 > warp_first || (kb <= warp_last - a.window && kb + kKeys - 1 >= a.sinks)) {
-            const int left = pos - kb, right = from - kb, few = a.sinks - kb;  // columns c <= left, and c >= right or c < few
-#pragma unroll
-            for (int c = 0; c < kKeys; ++c) x[c] = c <= left && (c >= right || c < few) ? x[c] : -INFINITY;
-          }
-          if (*holes) {
-            const uint64_t out = *reinterpret_cast<volatile uint64_t*>(&hole[slot]);
-#pragma unroll
-            for (int c = 0; c < kKeys; ++c) x[c] = (out >> c) & 1 ? -INFINITY : x[c];
-          }
-          float top[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-          for (int c = 4; c < kKeys - 4; c += 8) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top[e] = max3(top[e], x[c + e], x[c + 4 + e]);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], x[kKeys - 4 + e]);
-          const float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
-          bool grow = mx > limit;
-          if constexpr (Q8) grow |= live && mx > -INFINITY && fmaf(mx, scale, fmaxf(z.top[0], z.top[1])) > mo + kRescale;
-          if (__any_sync(0xFFFFFFFFu, grow)) {
-            const float mn = live && mx > -INFINITY ? fmaxf(m, mx * scale) : m;
-            float f = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
-            m = mn;
-            ms = m == -INFINITY ? 0.0f : m - kWeightUp<BF>;
-            l *= f;
-            if (live && m > -INFINITY) limit = (m + kRescale) / scale;
-            if constexpr (Q8) {  // (both maxima at once: mo is m - 126 at least, and vc finite)
-              float mw = -INFINITY;
-#pragma unroll
-              for (int c = 0; c < kKeys; c += 4) {
-                const float4 lv = *reinterpret_cast<const float4*>(&z.lv[c]);
-                mw = fmaxf(fmaxf(mw, fmaf(x[c], scale, lv.x)), fmaf(x[c + 1], scale, lv.y));
-                mw = fmaxf(fmaxf(mw, fmaf(x[c + 2], scale, lv.z)), fmaf(x[c + 3], scale, lv.w));
-              }
-              mw = live ? fmaxf(mo, mw) : mo;
-              f = mw == -INFINITY ? 1.0f : exp2_fast(mo - mw);
-              mo = mw;
-              vc = mw == -INFINITY ? 1.0f : exp2_fast(m - mw);
-            }
-            if (k > 0) {
-              // own block k - 1's product must be in O
-              if (!(ok = wait_all(&odone[2 * t + (buf ^ 1)], ((ns - 1) >> 1) & 1))) break;
-              tc_fence_after();
-#pragma unroll 1
-              for (int c0 = 0; c0 < HD; c0 += 32) {
-                float o[32];
-                tmem_ld32(tO + c0, o);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= f;
-                tmem_st32(tO + c0, o);
-              }
-            }
-          }
-          const float2 sc = make_float2(scale, scale), nm = make_float2(-ms, -ms);
-          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-          for (int c0 = 0; c0 < kKeys; c0 += 32) {
-            uint32_t u[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 y = __ffma2_rn(make_float2(x[c0 + e], x[c0 + e + 1]), sc, nm);
-              float2 p = make_float2(exp2_fast(y.x), exp2_fast(y.y));  // (0 where x is -infinity: not seen)
-              sum[(e >> 1) & 1] = __fadd2_rn(sum[(e >> 1) & 1], p);
-              if constexpr (Q8) {  // (cut where the weight is 0 next to it, or as good as: 0 times infinity is none)
-                const float2 f = *reinterpret_cast<const float2*>(&z.v[c0 + e]);
-                p.x *= min_nan(f.x * vc, kFactorMax);
-                p.y *= min_nan(f.y * vc, kFactorMax);
-              }
-              u[e >> 1] = pack2(p.x, p.y, BF ? DT_BF16 : DT_F16);
-            }
-            tmem_st16(tS + buf * 64 + c0 / 2, u);
-          }
-          tmem_st_wait();
-          tc_fence_before();
-          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          ok = quarter ? block(std::integral_constant<int, kKeys / 4>(), sub * (kKeys / 4), k, buf, slot, kb)
+                       : block(std::integral_constant<int, kKeys>(), 0, k, buf, slot, kb);
+          if (!ok) break;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&pready[2 * t + buf]);
       }
       // ---- behind the last two products (the others' ends were waited for when S took their P's place)
-      if (ok && own.n > 1) ok = wait_all(&odone[2 * t + (ns & 1)], ((ns - 2) >> 1) & 1);
-      if (ok && own.n > 0) ok = wait_all(&odone[2 * t + (~ns & 1)], ((ns - 1) >> 1) & 1);
+      if (ok && own.n > 1) ok = wait(&odone[2 * t + (ns & 1)], ((ns - 2) >> 1) & 1);
+      if (ok && own.n > 0) ok = wait(&odone[2 * t + (~ns & 1)], ((ns - 1) >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
       g += n;
-      const float out_of = Q8 && mo > -INFINITY ? 0.5f * (mo - m) : 0.0f;  // O is relative to mo (brought to m in two steps)
-      float own_f = exp2_fast(out_of), other_f = 0.0f;
-      bool other = false;
-      if (half && n > 1) {
-        if (t == 1) {
-          s_half[r] = m;
-          s_half[kRows + r] = l;
-          if constexpr (Q8) s_half[2 * kRows + r] = own_f;
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(hfull);
-          if (!(ok = wait_all(hfree, nh & 1))) break;
-          tc_fence_after();
-        } else {
-          if (!(ok = wait_all(hfull, nh & 1))) break;
-          tc_fence_after();
-          other = true;
+      // (e4m3: O is relative to mo, and brought to m in two steps)
+      const float own_f = Q8 && mo > -INFINITY ? exp2_fast(0.5f * (mo - m)) : 1.0f;
+      auto load_o = [&](int c0, float f, float (&o)[16]) {  // 16 columns of O times f, 0 where nothing was seen
+        uint32_t u[16];
+        tmem_ld16(tO + c0, u);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float y = __uint_as_float(u[e]);
+          if (Q8) y = y * own_f * own_f;
+          o[e] = l == 0.0f ? 0.0f : y * f;
         }
-        ++nh;
-      }
-      if (t == 0 || !half) {
-        float fb = 0.0f, fa = 1.0f;
-        if (other) {
-          const float mb = s_half[r], top = fmaxf(m, mb), base = top == -INFINITY ? 0.0f : top;
-          other_f = Q8 ? s_half[2 * kRows + r] : 1.0f;
-          fa = exp2_fast(m - base);
-          fb = exp2_fast(mb - base);
-          l = fmaf(l, fa, s_half[kRows + r] * fb);
-          m = top;
-        }
-        const float inv = w.part >= 0 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
-        uint8_t* po = a.out + (int64_t)(w.q0 + tok) * a.out_stride + (int64_t)(w.h * a.group + row_head) * HD * 2;
-        const int64_t prow = w.part >= 0 ? ((int64_t)blockIdx.x * 2 + w.part) * a.rows_cap + t * kRows + r : 0;
-        if (w.part >= 0 && live) a.part_ml[prow] = make_float2(m, l);
-        if (warp_live) {
+      };
+      uint8_t* const out = a.out + (int64_t)(w.q0 + tok) * a.out_stride + (int64_t)(w.h * a.group + row_head) * HD * 2;
+      const int64_t prow = ((int64_t)blockIdx.x * 2 + max(w.part, 0)) * a.rows_cap;  // the first row of a partial result
+      int lo = 0, hi = -1;  // the blocks that values were taken out of
+      auto look = [&]() {
+        lo = *reinterpret_cast<volatile int32_t*>(&taken[0]);
+        hi = *reinterpret_cast<volatile int32_t*>(&taken[1]);
+      };
+      uint8_t* const stage = smem + L::kOut;
+      if (half) {
+        // ---- both tiles (and all their warps) have these rows: maxima and sums, then the results, some columns at a time
+        s_half[t * kRows + r] = m;
+        s_half[(2 + t) * kRows + r] = l;
+        if (!(ok = meet())) break;
+        look();
+        float top = -INFINITY, total = 0.0f;
+        const int step = quarter ? 32 : kRows;
+        for (int q = row; q < 2 * kRows; q += step) top = fmaxf(top, s_half[q]);
+        const float base = top == -INFINITY ? 0.0f : top;
+        for (int q = row; q < 2 * kRows; q += step) total = fmaf(exp2_fast(s_half[q] - base), s_half[2 * kRows + q], total);
+        const float f = exp2_fast(m - base) * (w.part >= 0 || total == 0.0f ? 1.0f : 1.0f / total);
+        if (w.part >= 0 && live && t == 0 && (!quarter || sub == 0)) a.part_ml[prow + row] = make_float2(top, total);
+        constexpr int C = L::kOutCols, P = C / 4;  // (two buffers of 256 rows of C floats each)
+        auto cell = [&](int b, int q, int p) {
+          return reinterpret_cast<float4*>(stage + (b * 2 * kRows + q) * C * 4 + ((p ^ (P == 4 ? (q >> 1) & 3 : (q >> 2) & 1)) << 4));
+        };
+        // this thread adds up piece p of row rr of some columns (and of the rows 256 / P behind, where all rows of a tile differ)
+        const int id = t * kRows + r, p = id % P, rr = id / P, fit = min(quarter ? 32 : kRows, (w.lq - w.t0) * a.group);
+        auto add_up = [&](int b, int q0, int col) {
+          float4 x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            x[k] = quarter || k == 0 || k == 4 ? *cell(b, q0 + 32 * k, p) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v.x += x[k].x, v.y += x[k].y, v.z += x[k].z, v.w += x[k].w;
+          const int rt = q0 / a.group;
+          if (hi >= 0) {
+            const float4 y = taken_out<HD, CDT>(a, w, w.len - w.lq + w.t0 + rt, col, lo, hi);
+            v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+          }
+          if (w.part >= 0)
+            reinterpret_cast<float4*>(a.part_o)[(prow + (q0 & ~31)) * (HD / 4) + (col / 4) * 32 + (q0 & 31)] = v;
+          else
+            *reinterpret_cast<uint2*>(a.out + (int64_t)(w.q0 + w.t0 + rt) * a.out_stride +
+                                      ((int64_t)(w.h * a.group + q0 - rt * a.group) * HD + col) * 2) =
+                make_uint2(pack2(v.x, v.y, QDT), pack2(v.z, v.w, QDT));
+        };
 #pragma unroll 1
-          for (int c0 = 0; c0 < HD; c0 += 32) {
-            float o[32];
-            if (own.n > 0) {
-              tmem_ld32(tO + c0, o);
-            } else {
+        for (int c0 = 0; c0 < HD; c0 += C) {
+          const int b = (c0 / C) & 1;
+          if (warp_live) {
+            float o[16];  // (8 of them where C is 8)
+            load_o(c0 & ~15, f, o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+            for (int e = 0; e < P; ++e) {
+              float4 v = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              if (C == 8 && (c0 & 8)) v = make_float4(o[4 * e + 8], o[4 * e + 9], o[4 * e + 10], o[4 * e + 11]);
+              *cell(b, id, e) = v;
             }
-            if (Q8 || other) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = o[e] * own_f * own_f * fa;
-            }
-            if (other) {
-              float q[32];
-              tmem_ld32(tO + 128 + c0, q);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = fmaf(q[e] * other_f * other_f, fb, o[e]);
-            }
+          }
+          if (!(ok = meet())) break;
+          for (int q0 = rr; q0 < fit; q0 += 2 * kRows / P) add_up(b, q0, c0 + 4 * p);
+        }
+        if (ok) ok = meet();  // (what comes next takes these maxima, sums and results' place)
+        if (!ok) break;
+      } else if (w.part >= 0) {
+        // ---- a part: consecutive lanes' rows are consecutive there
+        look();
+        if (live) a.part_ml[prow + t * kRows + r] = make_float2(m, l);
+        if (warp_live) {
+          float4* const to = reinterpret_cast<float4*>(a.part_o) + (prow + t * kRows + sub * 32) * (HD / 4) + lane;
+#pragma unroll 1
+          for (int c0 = 0; c0 < HD; c0 += 16) {
+            float o[16];
+            load_o(c0, 1.0f, o);
             if (live) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = l == 0.0f ? 0.0f : o[e] * inv;
-              if (*bad) {  // what was taken out of edge blocks comes to the rows that see it
-                for (int i = w.i0; i < w.i1; ++i) {
-                  const int kb = chunk_block(sp, i) * kKeys;
-                  if (!edge_block(kb, first, last, a.window, a.sinks)) continue;
-                  for (int key = kb; key < kb + kKeys && key <= pos; ++key) {
-                    if (key < from && key >= a.sinks) continue;
-                    const int page = paged_page(a.c.table + (int64_t)w.b * a.c.table_width, a.c.table_width, a.c.n_pages, a.c.log2_page, key);
-                    if (page < 0) continue;
-                    const int cell = (w.h << a.c.log2_page) + (key & ((1 << a.c.log2_page) - 1));
-                    const uint8_t* pv = a.c.v + (int64_t)page * a.c.page_bytes + ((int64_t)cell * HD + c0) * elem_bytes(CDT);
-                    const float f = Q8 ? a.c.v_scale[(int64_t)page * a.c.scale_stride + cell] : 1.0f;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                      float v = load_elem(pv, e, CDT);
-                      if (Q8) v *= f;
-                      o[e] += isfinite(v) ? 0.0f : v;
-                    }
-                  }
+              for (int p = 0; p < 4; ++p) {
+                float4 v = make_float4(o[4 * p], o[4 * p + 1], o[4 * p + 2], o[4 * p + 3]);
+                if (hi >= 0) {
+                  const float4 x = taken_out<HD, CDT>(a, w, pos, c0 + 4 * p, lo, hi);
+                  v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
                 }
-              }
-              if (w.part >= 0) {
-                float4* to = reinterpret_cast<float4*>(a.part_o + prow * HD + c0);
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) to[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-              } else {
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                  uint32_t u[4];
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) u[k] = pack2(o[e + 2 * k], o[e + 2 * k + 1], QDT);
-                  *reinterpret_cast<uint4*>(po + (c0 + e) * 2) = make_uint4(u[0], u[1], u[2], u[3]);
-                }
+                to[(c0 / 4 + p) * 32] = v;
               }
             }
             __syncwarp();
           }
         }
-        if (other) {
-          tc_fence_before();
+      } else if (warp_live) {
+        // ---- whole: this warp's rows go through shared memory, 16-byte pieces swizzled, so that consecutive lanes store
+        // consecutive pieces of a row
+        constexpr int OB = L::kOutBytes, PP = OB / 16;  // bytes and pieces of a row at a time
+        uint8_t* const mine = stage + warp * 32 * OB;
+        auto cell = [&](int q, int p) { return reinterpret_cast<uint4*>(mine + q * OB + ((p ^ (PP == 8 ? q & 7 : (q >> 1) & 3)) << 4)); };
+        look();
+        const uint32_t alive = __ballot_sync(0xFFFFFFFFu, live);
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+        for (int c0 = 0; c0 < HD; c0 += 16) {
+          float o[16];
+          load_o(c0, inv, o);
+          if (hi >= 0 && live) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              const float4 x = taken_out<HD, CDT>(a, w, pos, c0 + 4 * p, lo, hi);
+              o[4 * p] += x.x, o[4 * p + 1] += x.y, o[4 * p + 2] += x.z, o[4 * p + 3] += x.w;
+            }
+          }
+          const int at = c0 / 8;  // pieces in front
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+            *cell(lane, (at + p) % PP) = make_uint4(pack2(o[8 * p], o[8 * p + 1], QDT), pack2(o[8 * p + 2], o[8 * p + 3], QDT),
+                                                    pack2(o[8 * p + 4], o[8 * p + 5], QDT), pack2(o[8 * p + 6], o[8 * p + 7], QDT));
+          if ((at + 2) % PP) continue;
           __syncwarp();
-          if (lane == 0) mbar_arrive(hfree);
+#pragma unroll
+          for (int k = 0; k < PP; ++k) {
+            const int q = (k * 32 + lane) / PP;
+            uint8_t* to = reinterpret_cast<uint8_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(out), q));
+            if ((alive >> q) & 1) *reinterpret_cast<uint4*>(to + (at + 2 - PP + lane % PP) * 16) = *cell(q, lane % PP);
+          }
+          __syncwarp();
         }
       }
       tc_fence_before();
@@ -1054,43 +1371,52 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-// Joins the pieces that several CTAs share: block (c, y) takes the piece that starts in CTA c and goes on behind it, and 8 of
-// its rows, a warp each.
+// Joins the pieces that several CTAs share: block (c, y) takes the piece that starts in CTA c and goes on behind it, and 32 of its
+// rows.  A lane is a row, a warp 16 of its columns (consecutive lanes' rows are consecutive in a partial result).
 template <int HD, int QDT>
-__global__ void __launch_bounds__(256) paged_chunk_join_kernel(const ChunkArgs a) {
-  constexpr int W = HD / 32;
+__global__ void __launch_bounds__(HD * 2) paged_chunk_join_kernel(const ChunkArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const ChunkMeta meta = a.meta[blockIdx.x];
-  const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, c0 = (threadIdx.x >> 5) * 16, r = blockIdx.y * 32 + lane;
   const int tile = r / kRows, rr = r % kRows, tok = tile * a.tok + rr / a.group;
-  if (!meta.starts || rr >= a.tok * a.group || tok >= meta.tokens) return;
+  const bool live = meta.starts && rr < a.tok * a.group && tok < meta.tokens;
+  if (!__any_sync(0xFFFFFFFFu, live)) return;
   const int ctas = (int)gridDim.x + 1;
-  float m = -INFINITY, l = 0.0f, o[W];
+  float m = -INFINITY, l = 0.0f;
+  float4 o[4] = {};
+  auto add = [&](int64_t slot) {
+    const float2 ml = live ? a.part_ml[slot * a.rows_cap + r] : make_float2(-INFINITY, 0.0f);
+    const float4* from = reinterpret_cast<const float4*>(a.part_o) + (slot * a.rows_cap + blockIdx.y * 32) * (HD / 4) + c0 * 8 + lane;
+    float4 x[4];
 #pragma unroll
-  for (int e = 0; e < W; ++e) o[e] = 0.0f;
-  auto add = [&](int64_t row) {
-    const float2 ml = a.part_ml[row];
+    for (int p = 0; p < 4; ++p) x[p] = live ? from[p * 32] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.0f : mn;
     const float f = exp2_fast(m - base), g = exp2_fast(ml.x - base);
     m = mn;
     l = fmaf(l, f, g * ml.y);
 #pragma unroll
-    for (int e = 0; e < W; ++e) o[e] = fmaf(o[e], f, g * a.part_o[row * HD + e * 32 + lane]);
+    for (int p = 0; p < 4; ++p) {
+      o[p].x = fmaf(o[p].x, f, g * x[p].x), o[p].y = fmaf(o[p].y, f, g * x[p].y);
+      o[p].z = fmaf(o[p].z, f, g * x[p].z), o[p].w = fmaf(o[p].w, f, g * x[p].w);
+    }
   };
-  add(((int64_t)blockIdx.x * 2 + 1) * a.rows_cap + r);
-  for (int c0 = (int)blockIdx.x + 1; c0 < ctas; c0 += 32) {
-    const int first = c0 + lane < ctas ? a.meta[c0 + lane].first : 0;
+  add((int64_t)blockIdx.x * 2 + 1);
+  for (int c = (int)blockIdx.x + 1; c < ctas; c += 32) {
+    const int first = c + lane < ctas ? a.meta[c + lane].first : 0;
     const uint32_t ends = __ballot_sync(0xFFFFFFFFu, first == 2);
     uint32_t has = __ballot_sync(0xFFFFFFFFu, first != 0);
     if (ends) has &= (ends ^ (ends - 1));  // up to the first end
-    for (; has; has &= has - 1) add((int64_t)(c0 + __ffs(has) - 1) * 2 * a.rows_cap + r);
+    for (; has; has &= has - 1) add((int64_t)(c + __ffs(has) - 1) * 2);
     if (ends) break;
   }
+  if (!live) return;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint8_t* po = a.out + (int64_t)(meta.row0 + tok) * a.out_stride + (int64_t)(meta.head * a.group + rr % a.group) * HD * 2;
+  uint4* po = reinterpret_cast<uint4*>(a.out + (int64_t)(meta.row0 + tok) * a.out_stride +
+                                       ((int64_t)(meta.head * a.group + rr % a.group) * HD + c0) * 2);
 #pragma unroll
-  for (int e = 0; e < W; ++e)
-    reinterpret_cast<uint16_t*>(po)[e * 32 + lane] = round_kv(l == 0.0f ? 0.0f : o[e] * inv, QDT);
+  for (int p = 0; p < 4; p += 2)
+    po[p / 2] = make_uint4(pack2(o[p].x * inv, o[p].y * inv, QDT), pack2(o[p].z * inv, o[p].w * inv, QDT),
+                           pack2(o[p + 1].x * inv, o[p + 1].y * inv, QDT), pack2(o[p + 1].z * inv, o[p + 1].w * inv, QDT));
 }
 
 // ---------------------------------------------------------------- host side
@@ -1134,19 +1460,19 @@ template <int HD, int CDT, int QDT, bool LOAD>
 struct ChunkKey {};
 
 template <int HD, int CDT, int QDT, bool LOAD>
-cudaError_t chunk_launch(const CUtensorMap (&m)[3], const ChunkArgs& a, const ChunkPlan& p, cudaStream_t st) {
+cudaError_t chunk_launch(const CUtensorMap (&m)[4], const ChunkArgs& a, const ChunkPlan& p, cudaStream_t st) {
   auto* kernel = paged_chunk_kernel<HD, CDT, QDT, LOAD>;
   constexpr size_t smem = ChunkSmem<HD, CDT>::kBytes;
   cudaError_t e = allow_smem<ChunkKey<HD, CDT, QDT, LOAD>>((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<p.ctas, LOAD ? 512 : 384, smem, st>>>(m[0], m[1], m[2], a);
+  kernel<<<p.ctas, LOAD ? 512 : 384, smem, st>>>(m[0], m[1], m[2], m[3], a);
   if ((e = cudaGetLastError()) != cudaSuccess || !p.rows_cap) return e;
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.ctas - 1, p.rows_cap / 8);  // no piece goes on behind the last CTA
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(p.ctas - 1, p.rows_cap / 32);  // no piece goes on behind the last CTA
+  cfg.blockDim = dim3(HD * 2);
   cfg.stream = st;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
@@ -1205,9 +1531,11 @@ extern "C" int adp_paged_chunk_attention(const adp_paged_kv* kv, const void* q, 
   a.n_rows = n_rows;
   a.group = group;
   a.tok = kRows / group;
+  a.few = 32 / group;
   // (a scale of 0 becomes the least normal number: the scores' differences vanish all the same, and what is not seen stays at
   // -infinity)
   a.scale_log2 = fmaxf(log2_scale(fabsf(scale)), kScaleMin);
+  a.even_scales = kv->page_size >= 4 && kv->scale_stride % 4 == 0 && aligned16(kv->k_scale) && aligned16(kv->v_scale);
   a.neg = scale < 0.0f ? kTcIdescANeg : 0;
   a.rows_cap = plan.rows_cap;
   if (plan.bytes) {
@@ -1219,8 +1547,9 @@ extern "C" int adp_paged_chunk_attention(const adp_paged_kv* kv, const void* q, 
   a.status = dev_status;
   const int64_t keys = (int64_t)kv->table_width * kv->page_size;
   a.wait_ns = packed_wait_ns((int32_t)keys, kv->n_seqs);
-  CUtensorMap m[3] = {};
+  CUtensorMap m[4] = {};
   if (!encode(&m[0], q, bf16, kv->head_dim, n_heads, n_rows, q_stride, group, a.tok)) return ADP_ERR_INVALID_ARG;
+  if (a.few && !encode(&m[3], q, bf16, kv->head_dim, n_heads, n_rows, q_stride, group, a.few)) return ADP_ERR_INVALID_ARG;
   if (!load && (!encode_pages(&m[1], kv->k, bf16, kv) || !encode_pages(&m[2], kv->v, bf16, kv))) return ADP_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   cudaError_t e = cudaErrorInvalidValue;

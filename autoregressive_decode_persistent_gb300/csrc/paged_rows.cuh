@@ -136,5 +136,29 @@ __device__ __forceinline__ float quantise8(float (&x)[8], float top) {
   return s;
 }
 
+// The same for two pieces of a row, as pairs of elements; the scale and its reciprocal are computed once.
+__device__ __forceinline__ float quantise16(float2 (&x)[2][4], float top) {
+  float s;
+  if (top > kTopFast) {
+    s = divide(top, kE4m3Max, 1.0f / kE4m3Max);
+    const float inv = __frcp_rn(s);
+    const float2 inv2 = make_float2(inv, inv), ns2 = make_float2(-s, -s);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {  // (divide(), two at a time)
+        const float2 y = __fmul2_rn(x[k][e], inv2);
+        x[k][e] = __ffma2_rn(__ffma2_rn(y, ns2, x[k][e]), inv2, y);
+      }
+  } else {
+    s = max_nan(__fdiv_rn(top, kE4m3Max), kScaleMin);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[k][e] = make_float2(__fdiv_rn(x[k][e].x, s), __fdiv_rn(x[k][e].y, s));
+  }
+  return s;
+}
+
 }  // namespace
 }  // namespace adp

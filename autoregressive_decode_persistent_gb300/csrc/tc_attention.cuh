@@ -39,15 +39,26 @@ __device__ __forceinline__ uint64_t wait_limit(volatile int32_t* abort) { return
 // A whole warp's wait with one answer for all of it.  What is not over at the first look is waited for in a function of
 // its own: between the warps of different roles the instruction caches hold little, and a long wait loop in line cost
 // 200 cycles even when there was nothing to wait for.
-__device__ __noinline__ bool mbar_wait_warp_slow(uint64_t* b, uint32_t parity, volatile int32_t* abort) {
-  const uint64_t t0 = globaltimer();
+__device__ __forceinline__ bool mbar_wait_warp_loop(uint64_t* b, uint32_t parity, volatile int32_t* abort) {
+  uint64_t t0 = 0;  // (the clock is asked late: reading it takes longer than most waits)
   for (uint32_t it = 1;; ++it) {
     if (__all_sync(0xFFFFFFFFu, mbar_try_wait(b, parity))) return true;
-    if ((it & 63) == 0 && __any_sync(0xFFFFFFFFu, *abort != 0 || globaltimer() - t0 > wait_limit(abort))) return false;
+    if ((it & 63) == 0) {
+      const uint64_t now = globaltimer();
+      if (t0 == 0) t0 = now;
+      if (__any_sync(0xFFFFFFFFu, *abort != 0 || now - t0 > wait_limit(abort))) return false;
+    }
   }
+}
+__device__ __noinline__ bool mbar_wait_warp_slow(uint64_t* b, uint32_t parity, volatile int32_t* abort) {
+  return mbar_wait_warp_loop(b, parity, abort);
 }
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* b, uint32_t parity, volatile int32_t* abort) {
   return __all_sync(0xFFFFFFFFu, mbar_try_wait(b, parity)) ? true : mbar_wait_warp_slow(b, parity, abort);
+}
+// The same without a call, for kernels that share out their registers (whose calls would need the largest share).
+__device__ __forceinline__ bool mbar_wait_warp_inline(uint64_t* b, uint32_t parity, volatile int32_t* abort) {
+  return __all_sync(0xFFFFFFFFu, mbar_try_wait(b, parity)) ? true : mbar_wait_warp_loop(b, parity, abort);
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
