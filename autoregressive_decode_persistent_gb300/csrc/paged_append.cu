@@ -13,6 +13,8 @@
 namespace adp {
 namespace {
 
+constexpr int kAppendThreads = 32;  // a warp: the last CTAs of a call leave few SMs idle (64: 140 us instead of 137, 256: 148)
+
 struct AppendArgs {
   PagedView c;
   const uint8_t *q, *k, *v;
@@ -35,17 +37,17 @@ struct AppendArgs {
 // eps) x gain, then x_i cos - x_(i+r) sin and x_(i+r) cos + x_i sin; everything in fp32, in pairs where there are
 // instructions for them, and rounded once on the way out (keys to codes x scale in e4m3 pages).
 template <int ROWDT, int CDT, int HD>
-__global__ void __launch_bounds__(256) paged_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendArgs a) {
   constexpr int LPH = HD / 16;    // lanes that hold a head
   constexpr int HPS = 32 / LPH;   // heads of a step of the warp
-  constexpr int kAhead = ROWDT == DT_F32 ? 1 : 2;  // steps in flight
+  constexpr int kAhead = ROWDT == DT_F32 ? 2 : 4;  // steps in flight
   constexpr int RB = elem_bytes(ROWDT);
   const PagedView& c = a.c;
   const int lane = threadIdx.x & 31, u = lane % LPH;
   const int pa = u < a.turned ? u : 2 * u, pb = u < a.turned ? u + a.turned : 2 * u + 1;  // this lane's pieces of a head
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int64_t w = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
   // offsets that are wrong are reported, whichever rows they would move
-  for (int64_t s = (int64_t)blockIdx.x * 256 + threadIdx.x; s < c.n_seqs; s += (int64_t)gridDim.x * 256)
+  for (int64_t s = (int64_t)blockIdx.x * kAppendThreads + threadIdx.x; s < c.n_seqs; s += (int64_t)gridDim.x * kAppendThreads)
     if (a.cu[s + 1] < a.cu[s] || (s == 0 && a.cu[0] != 0)) report(a.status, ADP_ERR_INVALID_ARG);
   const int i = a.parts == 1 ? (int)w : (int)(w / a.parts);
   if (i >= a.n_rows) return;
@@ -86,7 +88,14 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const AppendArgs a) {
     if (lane == 0) report(a.status, ADP_ERR_CONTEXT_OVERFLOW);
     page = -1;
   }
-  const bool there = page >= 0, turned = u < a.turned && there;
+  uint8_t* const ro = a.out + (int64_t)i * a.out_stride;
+  if (page < 0) {  // its queries become zeros
+    const int row_bytes = HD * elem_bytes(a.out_dt);
+    for (int at = first * row_bytes + lane * 16; at < min(last, a.n_heads) * row_bytes; at += 512)
+      *reinterpret_cast<uint4*>(ro + at) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const bool turned = u < a.turned;
   float2 cs[4], sn[4], ns[4];  // this lane's angles
   if (turned) {
     const int64_t at = pos * (a.turned * 8) + u * 8;
@@ -102,7 +111,6 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const AppendArgs a) {
   const int head_step = (HD * elem_bytes(CDT)) << c.log2_page;  // (32 bits hold it, as in the other rows' kernels)
   const int64_t cell0 = (int64_t)page * c.page_bytes + (int64_t)slot * (HD * elem_bytes(CDT));
   const int64_t scale0 = CDT == DT_E4M3 ? (int64_t)page * c.scale_stride + slot : 0;
-  uint8_t* const ro = a.out + (int64_t)i * a.out_stride;
   auto pairs = [](const float (&x)[8], float2 (&y)[4]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] = make_float2(x[2 * e], x[2 * e + 1]);
@@ -119,6 +127,8 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const AppendArgs a) {
     }
     pairs(x, y);
   };
+  const uint8_t* held = nullptr;  // whose gains this lane has
+  float2 g[2][4];
 #pragma unroll 1
   for (int h0 = first; h0 < last; h0 += kAhead * HPS) {
     if (h0 > first) load_rows(h0);
@@ -137,6 +147,11 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const AppendArgs a) {
       if (!is_v) {
         const uint8_t* gain = is_q ? a.q_gain : a.k_gain;
         if (gain) {  // (all lanes of a head alike)
+          if (gain != held) {
+            gains(gain, pa, g[0]);
+            gains(gain, pb, g[1]);
+            held = gain;
+          }
           float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
           for (int k = 0; k < 2; ++k)
@@ -149,10 +164,8 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const AppendArgs a) {
           const float f = rsqrtf(ss * (1.0f / HD) + a.eps);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float2 g[4];
-            gains(gain, k ? pb : pa, g);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[k][e] = __fmul2_rn(__fmul2_rn(x[k][e], make_float2(f, f)), g[e]);
+            for (int e = 0; e < 4; ++e) x[k][e] = __fmul2_rn(__fmul2_rn(x[k][e], make_float2(f, f)), g[k][e]);
           }
         }
         if (turned) {
@@ -172,12 +185,12 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const AppendArgs a) {
           const int at = k ? pb : pa;
           float y[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[2 * e] = there ? x[k][e].x : 0.0f, y[2 * e + 1] = there ? x[k][e].y : 0.0f;
+          for (int e = 0; e < 4; ++e) y[2 * e] = x[k][e].x, y[2 * e + 1] = x[k][e].y;
           if (a.out_dt == DT_BF16) store_row8<DT_BF16>(p + at * 16, y);
           else if (a.out_dt == DT_F16) store_row8<DT_F16>(p + at * 16, y);
           else store_row8<DT_F32>(p + at * 32, y);
         }
-      } else if (there) {
+      } else {
         const int hc = is_v ? hv : hk;
         uint8_t* cell = (is_v ? c.v : c.k) + cell0 + hc * head_step;
         if constexpr (CDT == DT_E4M3) {
@@ -268,14 +281,14 @@ extern "C" int adp_paged_kv_append(const adp_paged_kv* kv, const adp_rope* rope,
   a.parts = want < 1 ? 1 : want > most ? most : want;
   a.part_heads = (most + a.parts - 1) / a.parts * step;
   a.parts = (heads + a.part_heads - 1) / a.part_heads;
-  const int64_t grid = ((int64_t)n_rows * a.parts + 7) / 8;
+  const int64_t grid = ((int64_t)n_rows * a.parts + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
   if (grid > 0x7FFFFFFF) return ADP_ERR_UNSUPPORTED_CONFIG;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   auto by_rows = [&](auto cdt, auto hd) {
     constexpr int C = decltype(cdt)::value, H = decltype(hd)::value;
-    if (rows_dtype == ADP_F16) paged_append_kernel<DT_F16, C, H><<<(unsigned)grid, 256, 0, st>>>(a);
-    else if (rows_dtype == ADP_BF16) paged_append_kernel<DT_BF16, C, H><<<(unsigned)grid, 256, 0, st>>>(a);
-    else paged_append_kernel<DT_F32, C, H><<<(unsigned)grid, 256, 0, st>>>(a);
+    if (rows_dtype == ADP_F16) paged_append_kernel<DT_F16, C, H><<<(unsigned)grid, kAppendThreads, 0, st>>>(a);
+    else if (rows_dtype == ADP_BF16) paged_append_kernel<DT_BF16, C, H><<<(unsigned)grid, kAppendThreads, 0, st>>>(a);
+    else paged_append_kernel<DT_F32, C, H><<<(unsigned)grid, kAppendThreads, 0, st>>>(a);
   };
   auto by_cache = [&](auto hd) {
     if (kv->dtype == ADP_F16) by_rows(std::integral_constant<int, DT_F16>(), hd);

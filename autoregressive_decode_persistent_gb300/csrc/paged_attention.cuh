@@ -814,9 +814,9 @@ __global__ void __launch_bounds__(kPagedWarps * 32, kResident<NT>) paged_attenti
 }
 
 // Joins the segments that several CTAs share: block (c, h) takes the segment that starts in CTA c and goes on behind
-// it, and its head h.  Four warps read the parts in turn; the first threads join the warps' results.
-template <int HD, int QDT, int NT>
-__global__ void __launch_bounds__(128) paged_attention_join_kernel(AttnArgs a) {
+// it, and its head h.  JW warps read the parts in turn; the first threads join the warps' results.
+template <int HD, int QDT, int NT, int JW>
+__global__ void __launch_bounds__(JW * 32) paged_attention_join_kernel(AttnArgs a) {
   using Part = Partial<HD, NT>;
   constexpr int W = HD / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -833,8 +833,8 @@ __global__ void __launch_bounds__(128) paged_attention_join_kernel(AttnArgs a) {
   float m = -INFINITY, l = 0.0f, o[W];
 #pragma unroll
   for (int e = 0; e < W; ++e) o[e] = 0.0f;
-#pragma unroll 4
-  for (int k = warp; k < n; k += 4) {
+#pragma unroll JW
+  for (int k = warp; k < n; k += JW) {
     const Part& p = parts[(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)];
     const float pm = p.m[h], pl = p.l[h];
     float x[W];
@@ -847,15 +847,17 @@ __global__ void __launch_bounds__(128) paged_attention_join_kernel(AttnArgs a) {
 #pragma unroll
     for (int e = 0; e < W; ++e) o[e] = fmaf(o[e], f, g * x[e]);
   }
-  __shared__ float s_m[4], s_l[4], s_o[4][HD];
+  __shared__ float s_m[JW], s_l[JW], s_o[JW][HD];
   if (lane == 0) s_m[warp] = m, s_l[warp] = l;
 #pragma unroll
   for (int e = 0; e < W; ++e) s_o[warp][e * 32 + lane] = o[e];
   __syncthreads();
-  const float top = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  float sum = 0.0f, f[4];
+  float top = s_m[0];
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 1; w < JW; ++w) top = fmaxf(top, s_m[w]);
+  float sum = 0.0f, f[JW];
+#pragma unroll
+  for (int w = 0; w < JW; ++w) {
     f[w] = exp2_fast(s_m[w] - safe_max(top));
     sum = fmaf(f[w], s_l[w], sum);
   }
@@ -866,7 +868,7 @@ __global__ void __launch_bounds__(128) paged_attention_join_kernel(AttnArgs a) {
     for (int e = 0; e < 2; ++e) {
       x[e] = 0.0f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) x[e] = fmaf(f[w], s_o[w][threadIdx.x * 2 + e], x[e]);
+      for (int w = 0; w < JW; ++w) x[e] = fmaf(f[w], s_o[w][threadIdx.x * 2 + e], x[e]);
     }
     uint8_t* po = a.out + (int64_t)b * a.out_stride + (int64_t)(kvh * a.group + head0 + h) * HD * 2;
     reinterpret_cast<uint32_t*>(po)[threadIdx.x] = pack2(x[0] * inv, x[1] * inv, QDT);
@@ -951,11 +953,14 @@ cudaError_t attention_launch(const AttnArgs& a, int ctas, cudaStream_t st) {
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas - 1, a.group < NT * 8 ? a.group : NT * 8);  // no segment goes on behind the last CTA
-  cfg.blockDim = dim3(128);
+  // (one long context is cut into many parts, and a window leaves little else to wait for: 131,011 positions behind a window of
+  // 32,768)
+  constexpr int kJoinWarps = WIN ? 8 : 4;
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = st;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_attention_join_kernel<HD, QDT, NT>, a);
+  return cudaLaunchKernelEx(&cfg, paged_attention_join_kernel<HD, QDT, NT, kJoinWarps>, a);
 }
 
 inline int attention_check(const adp_paged_kv* kv, int32_t n_heads, PagedView* c) {

@@ -398,6 +398,86 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
     atomicMin(&taken[0], kb);
     atomicMax(&taken[1], kb);
   };
+  // Four warps (lt: the thread among them) bring the codes of K (op 0) or V (op 1) of block g, at positions from kb on, to fp16
+  // (exactly) in the block's slot, and the rows' scales beside them.  The slot is free, and so the codes' own
+  // place has been used for an earlier block of codes before: a barrier's phases tell only two apart.
+  [[maybe_unused]] auto bring_codes = [&](int lt, int op, int g, int slot, int kb, int last, bool edge) {
+    if constexpr (Q8) {
+      constexpr int PPR = HD / 16, RSTEP = 128 / PPR, NR = kKeys / RSTEP, R = L::kRaw;  // 16-byte pieces of a row; rows of this thread
+      const int q = lt >> 5, n_raw = 2 * g + op, rs = n_raw % R;
+      // (head_dim 128: half a row of an even and of an odd position to every 8 lanes, so that their stores meet in no bank)
+      const int piece = HD == 128 ? ((lane >> 3) & 1) * 4 + (lane & 3) : lane & 3;
+      const int row0 = HD == 128 ? q * 4 + (lane >> 4) * 2 + ((lane >> 2) & 1) : q * 8 + (lane >> 2);
+      if (!wait(&rawfull[rs], (n_raw / R) & 1)) return false;
+      uint4 c[NR];
+      const uint32_t raw = smem_u32(smem + L::kRawAt) + rs * L::kRawBytes + row0 * HD + piece * 16;
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(c[n].x), "=r"(c[n].y), "=r"(c[n].z), "=r"(c[n].w)
+                     : "r"(raw + n * RSTEP * HD));
+      const bool mine = q < 2;  // holds a row's scale
+      float sc = 0.0f;
+      if (mine) sc = reinterpret_cast<const volatile float*>(smem + L::kRawAt + rs * L::kRawBytes + kKeys * HD)[lt];
+      const uint64_t out = *reinterpret_cast<volatile uint64_t*>(&rawhole[rs]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&rawempty[rs]);
+      if (edge) {  // values that are not numbers must not meet weights of zero; behind the last row lies anything
+        if (kb + lt > last) sc = 0.0f;
+        bool some = false;
+        if (op == 1) {
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            uint32_t* u = reinterpret_cast<uint32_t*>(&c[n]);
+            uint32_t nan = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) nan |= (u[e] & 0x7F7F7F7Fu) + 0x01010101u;
+            if (nan & 0x80808080u) {
+              some |= kb + row0 + n * RSTEP <= last;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int k = 0; k < 32; k += 8)
+                  if (((u[e] >> k) & 0x7Fu) == 0x7Fu) u[e] &= ~(0xFFu << k);
+            }
+          }
+          if (!isfinite(sc)) sc = 0.0f, some = true;
+        }
+        if (some) take_out(kb);
+      }
+      const uint32_t to = smem_u32(ring) + slot * L::kPair + op * L::kTile + (2 * piece / 8) * L::kBlock + row0 * 128;
+      const uint32_t to0 = to + (((2 * piece & 7) ^ (row0 & 7)) << 4), to1 = to + (((2 * piece + 1 & 7) ^ (row0 & 7)) << 4);
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        uint32_t f[8];
+        e4m3x4_to_f16(c[n].x, f[0], f[1]);
+        e4m3x4_to_f16(c[n].y, f[2], f[3]);
+        e4m3x4_to_f16(c[n].z, f[4], f[5]);
+        e4m3x4_to_f16(c[n].w, f[6], f[7]);
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to0 + n * RSTEP * 128), "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3]) : "memory");
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to1 + n * RSTEP * 128), "r"(f[4]), "r"(f[5]), "r"(f[6]), "r"(f[7]) : "memory");
+      }
+      SlotScales& z = s_scale[slot];
+      if (mine) {
+        if (op == 0) {
+          z.k[lt] = sc;
+          if (lt == 0) hole[slot] = out;
+        } else {
+          const float lv = log2_scale_of(sc);
+          z.v[lt] = sc;
+          z.lv[lt] = lv;
+          float top = lv;
+#pragma unroll
+          for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+          if (lane == 0) z.top[q] = top;
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(op ? &vfull[slot] : &full[slot]);
+    }
+    return true;
+  };
 
   if (warp >= 8 && warp < 12) {
     if constexpr (LOAD) give_registers<kIssueRegs>();
@@ -780,29 +860,10 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
       const int lt = threadIdx.x - 384;
       bool ok = true;
       auto wait_slot = [&](int n) { return n < NS || wait(&empty[n % NS], (n / NS - 1) & 1); };
-      // positions of a block without a place, said by the warps that hold its rows
-      auto say_holes = [&](int s, bool gap) {
-        if (warp >= 14) return;
-        const uint32_t m = __ballot_sync(0xFFFFFFFFu, gap);
-        if (lane == 0) {
-          reinterpret_cast<uint32_t*>(&hole[s])[warp - 12] = m;
-          if (m) {
-            *holes = 1;
-            report(a.status, ADP_ERR_INVALID_ARG);
-          }
-        }
-      };
       if constexpr (Q8) {
-        // ---- four warps that bring codes to fp16 (exactly) in the ring, and the rows' scales beside them
-        constexpr int PPR = HD / 16, RSTEP = 128 / PPR, NR = kKeys / RSTEP, R = L::kRaw;  // 16-byte pieces of a row; rows of this thread
-        // (head_dim 128: half a row of an even and of an odd position to every 8 lanes, so that their stores meet in no bank)
-        const int piece = HD == 128 ? ((lane >> 3) & 1) * 4 + (lane & 3) : lane & 3;
-        const int row0 = HD == 128 ? (warp - 12) * 4 + (lane >> 4) * 2 + ((lane >> 2) & 1) : (warp - 12) * 8 + (lane >> 2);
-        const uint32_t raw = smem_u32(smem + L::kRawAt) + row0 * HD + piece * 16;
-        const uint32_t to = smem_u32(ring) + (2 * piece / 8) * L::kBlock + row0 * 128;
-        const uint32_t to0 = to + (((2 * piece & 7) ^ (row0 & 7)) << 4), to1 = to + (((2 * piece + 1 & 7) ^ (row0 & 7)) << 4);
-        int g = 0, slot = 0, rs = 0;  // blocks so far, their slot, and the next one of codes
-        uint32_t raw_phase = 0;
+        // ---- four warps that bring codes of K to fp16 in the ring, and those of V where the item has two tiles (else the
+        // tile's own softmax warps bring them there, which have little else to do)
+        int g = 0, slot = 0;  // blocks so far, and the next one's slot
         for (int it = 0; ok; ++it) {
           const int is = it % kItems;
           if (!(ok = wait(&ifull[is], (it / kItems) & 1))) break;
@@ -810,83 +871,15 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&iempty[is]);
           if (w.stop) break;
-          const int first = w.first(), last = w.last(span);
+          const int first = w.first(), last = w.last(span), ops = w.half(a.tok) ? 1 : 2;
           const bool quarter = w.quarter(a.few);
           const ChunkSpan sp = chunk_span(first, last, a.window, a.sinks);
           for (int i = w.i0; ok && i < w.i1; ++i, ++g) {
             const int kb = chunk_block(sp, i) * kKeys;
             const bool edge = quarter || edge_block(kb, first, last, a.window, a.sinks);
-            SlotScales& z = s_scale[slot];
 #pragma unroll 1
-            for (int op = 0; op < 2; ++op) {  // K, V
-              if (!(ok = wait(&rawfull[rs], raw_phase))) break;
-              uint4 c[NR];
-#pragma unroll
-              for (int n = 0; n < NR; ++n)
-                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(c[n].x), "=r"(c[n].y), "=r"(c[n].z), "=r"(c[n].w)
-                             : "r"(raw + rs * L::kRawBytes + n * RSTEP * HD));
-              float sc = 0.0f;
-              const bool mine = lt < kKeys;
-              if (mine) sc = reinterpret_cast<const volatile float*>(smem + L::kRawAt + rs * L::kRawBytes + kKeys * HD)[lt];
-              const uint64_t out = rawhole[rs];
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&rawempty[rs]);
-              if (++rs == R) rs = 0, raw_phase ^= 1;
-              if (op == 0 && !(ok = wait_slot(g))) break;
-              if (edge) {  // values that are not numbers must not meet weights of zero; behind the last row lies anything
-                if (kb + lt > last) sc = 0.0f;
-                bool some = false;
-                if (op == 1) {
-#pragma unroll
-                  for (int n = 0; n < NR; ++n) {
-                    uint32_t* u = reinterpret_cast<uint32_t*>(&c[n]);
-                    uint32_t nan = 0;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) nan |= (u[e] & 0x7F7F7F7Fu) + 0x01010101u;
-                    if (nan & 0x80808080u) {
-                      some |= kb + row0 + n * RSTEP <= last;
-#pragma unroll
-                      for (int e = 0; e < 4; ++e)
-#pragma unroll
-                        for (int k = 0; k < 32; k += 8)
-                          if (((u[e] >> k) & 0x7Fu) == 0x7Fu) u[e] &= ~(0xFFu << k);
-                    }
-                  }
-                  if (!isfinite(sc)) sc = 0.0f, some = true;
-                }
-                if (some) take_out(kb);
-              }
-#pragma unroll
-              for (int n = 0; n < NR; ++n) {
-                const uint32_t at = slot * L::kPair + op * L::kTile + n * RSTEP * 128;
-                uint32_t f[8];
-                e4m3x4_to_f16(c[n].x, f[0], f[1]);
-                e4m3x4_to_f16(c[n].y, f[2], f[3]);
-                e4m3x4_to_f16(c[n].z, f[4], f[5]);
-                e4m3x4_to_f16(c[n].w, f[6], f[7]);
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to0 + at), "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3]) : "memory");
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to1 + at), "r"(f[4]), "r"(f[5]), "r"(f[6]), "r"(f[7]) : "memory");
-              }
-              if (mine) {
-                if (op == 0) {
-                  z.k[lt] = sc;
-                  if (lt == 0) hole[slot] = out;
-                } else {
-                  const float lv = log2_scale_of(sc);
-                  z.v[lt] = sc;
-                  z.lv[lt] = lv;
-                  float top = lv;
-#pragma unroll
-                  for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                  if (lane == 0) z.top[warp - 12] = top;
-                }
-              }
-              fence_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(op ? &vfull[slot] : &full[slot]);
-            }
-            if (!ok) break;
+            for (int op = 0; ok && op < ops; ++op)
+              ok = (op == 1 || wait_slot(g)) && bring_codes(lt, op, g, slot, kb, last, edge);
             if (++slot == NS) slot = 0;
           }
         }
@@ -900,6 +893,18 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
         const int piece = lt % PPR, row0 = lt / PPR;
         int g = 0, landed = 0;  // blocks asked for, and those handed over
         uint32_t gaps = 0;      // of the blocks under way, the last one lowest: this thread's row has no place
+        // positions of a block without a place, said by the warps that hold its rows
+        auto say_holes = [&](int s, bool gap) {
+          if (warp >= 14) return;
+          const uint32_t m = __ballot_sync(0xFFFFFFFFu, gap);
+          if (lane == 0) {
+            reinterpret_cast<uint32_t*>(&hole[s])[warp - 12] = m;
+            if (m) {
+              *holes = 1;
+              report(a.status, ADP_ERR_INVALID_ARG);
+            }
+          }
+        };
         auto hand_over = [&]() {  // the oldest block under way: its copies have ended for this thread
           const int s = landed % NS;
           say_holes(s, (gaps >> (g - 1 - landed)) & 1);
@@ -1158,11 +1163,13 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
       };
       for (int k = 0; k < own.n; ++k, ++ns) {
         const uint32_t buf = ns & 1;
-        const int i = own.off + k * own.step;
+        const int i = own.off + k * own.step, slot = (g + i) % NS, kb = chunk_block(sp, w.i0 + i) * kKeys;
         if (!(ok = wait(&sfull[2 * t + buf], (ns >> 1) & 1))) break;
+        if constexpr (Q8) {  // (the block's scores are here, so its slot is its own and V may be written)
+          if (half && !(ok = bring_codes(r, 1, g + i, slot, kb, last, quarter || edge_block(kb, first, last, a.window, a.sinks)))) break;
+        }
         tc_fence_after();
         __syncwarp();
-        const int slot = (g + i) % NS, kb = chunk_block(sp, w.i0 + i) * kKeys;
         if constexpr (Q8) {  // (the scales of V come with V)
           if (!(ok = wait(&vfull[slot], ((g + i) / NS) & 1))) break;
         }

@@ -1,11 +1,13 @@
 """The paged KV cache operators and packed prompt attention on PyTorch tensors (include/adp.h has their semantics).
 
-Argument checks and marshalling only: every computation runs in libadp.so's kernels, on the current
-stream of the tensors' device, without synchronising.  Nothing is differentiable.  Wrong arguments raise
-adp.AdpError before anything is launched; wrong lengths or page numbers, which only the GPU sees, set the
-optional `status` tensor (int32, one element).
+Argument checks and marshalling only (those of the calls that serve single tokens and chunks in csrc/binding.cpp): every
+computation runs in libadp.so's kernels, on the current stream of the tensors' device, without synchronising.  Nothing is
+differentiable.  Wrong arguments raise adp.AdpError before anything is launched; wrong lengths or page numbers, which only
+the GPU sees, set the optional `status` tensor (int32, one element).
 """
 from __future__ import annotations
+
+import ctypes
 
 import torch
 
@@ -58,6 +60,22 @@ def _call(device: int, name: str, *args):
     else:
         with torch.cuda.device(device):
             adp._check(getattr(adp.load_library(), name)(*args, torch._C._cuda_getCurrentRawStream(device)), name)
+
+
+_binding = None
+
+
+def _native():
+    """The extension module with the checks of the calls below, given the addresses of the library's functions."""
+    global _binding
+    if _binding is None:
+        lib = adp.load_library()
+        from . import _binding as module  # (no fallback: build it with build.build())
+        names = ("adp_paged_kv_append", "adp_paged_attention", "adp_paged_attention_workspace", "adp_paged_window_attention",
+                 "adp_paged_window_attention_workspace", "adp_paged_chunk_attention", "adp_paged_chunk_attention_workspace")
+        module.setup(adp.AdpError, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
+        _binding = module
+    return _binding
 
 
 def _paged(where: str, k_pages, v_pages, table, lens, k_scale, v_scale, device: int) -> adp.PagedKV:
@@ -155,83 +173,8 @@ def paged_kv_append(k_pages, v_pages, table, lens, cu_rows, q, k, v, cos, sin, *
     cos, sin: fp32 [positions, rotated / 2], the cosines and sines of every position's angles; the first `rotated` elements of a
     head are turned in pairs i, i + rotated / 2.  q_gain, k_gain: [head_dim] of one type (f16, bf16 or f32).  Returns the queries, of
     q's type or in `out` (f16, bf16 or f32; may be q itself); q may be None: keys and values only."""
-    where = "paged_kv_append"
-    device = k_pages.get_device()
-    kv = _paged(where, k_pages, v_pages, table, lens, k_scale, v_scale, device)
-    cu = _indices(where, "cu_rows", cu_rows, kv.n_seqs + 1, device)
-    dtype, shape = k.dtype, k.shape
-    dt = _ROWS.get(dtype)
-    if dt is None or len(shape) != 3:
-        _refuse(where, "k and v rows must be [rows, kv_heads, head_dim] of f16, bf16 or f32")
-    n, hd = shape[0], kv.head_dim
-    shape = (n, kv.n_kv_heads, hd)
-    ks, vs = _rows(where, "k", k, shape, dtype, device), _rows(where, "v", v, shape, dtype, device)
-    qp = op = None
-    heads = qs = os = odt = 0
-    if q is not None:
-        if len(q.shape) != 3 or q.shape[1] < 1:
-            _refuse(where, "q must be [rows, heads, head_dim]")
-        heads = q.shape[1]
-        shape = (n, heads, hd)
-        qs, qp = _rows(where, "q", q, shape, dtype, device), q.data_ptr()
-        if out is None:
-            out = torch.empty_like(q, memory_format=torch.contiguous_format)
-            os, odt = heads * hd, dt
-        else:
-            odt = _ROWS.get(out.dtype)
-            if odt is None:
-                _refuse(where, "out must be of f16, bf16 or f32")
-            os = _rows(where, "out", out, shape, out.dtype, device)
-        op = out.data_ptr()
-    elif out is not None:
-        _refuse(where, "out goes with q")
-    angles = cos.shape
-    if cos.dtype is not torch.float32 or sin.dtype is not torch.float32 or len(angles) != 2 or sin.shape != angles \
-            or not cos.is_contiguous() or not sin.is_contiguous() or cos.get_device() != device or sin.get_device() != device:
-        _refuse(where, f"cos and sin must be alike: contiguous fp32 [positions, rotated / 2] on device {device}")
-    gains, gdt = [None, None], 0
-    for at, g in enumerate((q_gain, k_gain)):
-        if g is None:
-            continue
-        gdt = _ROWS.get(g.dtype)
-        if gdt is None or g.shape != (hd,) or not g.is_contiguous() or g.get_device() != device:
-            _refuse(where, f"q_gain and k_gain must be contiguous [{hd}] of f16, bf16 or f32 on device {device}")
-        gains[at] = g.data_ptr()
-    if q_gain is not None and k_gain is not None and q_gain.dtype is not k_gain.dtype:
-        _refuse(where, "q_gain and k_gain must be of one type")
-    rope = adp.Rope(cos.data_ptr(), sin.data_ptr(), angles[0], 2 * angles[1], *gains, gdt, eps)
-    _call(device, "adp_paged_kv_append", kv, rope, qp, k.data_ptr(), v.data_ptr(), dt, heads, qs, ks, vs, cu, n, op, odt, os,
-          _status(where, status, device))
-    return out
-
-
-def _window(where: str, window, sinks) -> tuple[int, int]:
-    """(0, 0) without a window."""
-    if window is None:
-        if sinks != 0:
-            _refuse(where, "sinks go with a window")
-        return 0, 0
-    if not 1 <= window or sinks < 0:
-        _refuse(where, "window must be at least 1, sinks at least 0")
-    top = 2 ** 31 - 1  # (longer than any sequence)
-    return min(window, top), min(sinks, top)
-
-
-def _workspace(where: str, workspace, device: int, like, bytes_of, *args):
-    """(address, bytes) of the given workspace or of a new one, of bytes_of(*args) bytes, on the current stream, and its owner."""
-    if workspace is not None:
-        if workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != device:
-            _refuse(where, "workspace must be a contiguous uint8 tensor on the tensors' device")
-        return workspace.data_ptr(), workspace.numel(), workspace
-    if device == torch._C._cuda_getDevice():
-        need = bytes_of(*args)
-    else:
-        with torch.cuda.device(device):
-            need = bytes_of(*args)
-    if need == 0:
-        return None, 0, None
-    workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
-    return workspace.data_ptr(), need, workspace
+    return _native().paged_kv_append(k_pages, v_pages, table, lens, cu_rows, q, k, v, cos, sin, q_gain, k_gain, eps, k_scale, v_scale,
+                                     out, status)
 
 
 def paged_attention(q, k_pages, v_pages, table, lens, *, window: int | None = None, sinks: int = 0, scale: float | None = None,
@@ -243,30 +186,7 @@ def paged_attention(q, k_pages, v_pages, table, lens, *, window: int | None = No
     adp.adp_paged_attention_workspace bytes, with a window adp.adp_paged_window_attention_workspace bytes (not shared by calls
     that may run at the same time); by default one is allocated on the current stream.
     The work is split by the table's width, or the window's: a table no wider than the longest context is fastest."""
-    where = "paged_attention"
-    device = k_pages.get_device()
-    window, sinks = _window(where, window, sinks)
-    kv = _paged(where, k_pages, v_pages, table, lens, k_scale, v_scale, device)
-    dtype, shape = q.dtype, q.shape
-    dt = _HALF.get(dtype)
-    if dt is None or len(shape) != 3 or shape[0] != kv.n_seqs or shape[2] != kv.head_dim or shape[2] < 1:
-        _refuse(where, "q must be [seqs, heads, head_dim] of f16 or bf16")
-    qs = _rows(where, "q", q, shape, dtype, device)
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        os = shape[1] * shape[2]
-    else:
-        os = _rows(where, "out", out, shape, dtype, device)
-    scale = shape[2] ** -0.5 if scale is None else scale
-    if window:
-        at, need, held = _workspace(where, workspace, device, q, adp.adp_paged_window_attention_workspace, kv, shape[1], window, sinks)
-        _call(device, "adp_paged_window_attention", kv, q.data_ptr(), dt, shape[1], qs, scale, window, sinks, out.data_ptr(), os, at,
-              need, _status(where, status, device))
-    else:
-        at, need, held = _workspace(where, workspace, device, q, adp.adp_paged_attention_workspace, kv, shape[1])
-        _call(device, "adp_paged_attention", kv, q.data_ptr(), dt, shape[1], qs, scale, out.data_ptr(), os, at, need,
-              _status(where, status, device))
-    return out
+    return _native().paged_attention(k_pages, v_pages, table, lens, q, window, sinks, scale, k_scale, v_scale, out, workspace, status)
 
 
 def paged_chunk_attention(q, k_pages, v_pages, table, lens, cu_rows, *, window: int | None = None, sinks: int = 0,
@@ -280,26 +200,8 @@ def paged_chunk_attention(q, k_pages, v_pages, table, lens, cu_rows, *, window: 
     workspace: optional uint8 tensor of adp.adp_paged_chunk_attention_workspace bytes (not shared by calls that may run at the
     same time); by default one is allocated on the current stream.  A wait inside the kernel that ran out leaves rows unset:
     `status` tells."""
-    where = "paged_chunk_attention"
-    device = k_pages.get_device()
-    window, sinks = _window(where, window, sinks)
-    kv = _paged(where, k_pages, v_pages, table, lens, k_scale, v_scale, device)
-    dtype, shape = q.dtype, q.shape
-    dt = _HALF.get(dtype)
-    if dt is None or len(shape) != 3 or shape[2] != kv.head_dim or shape[2] < 1:
-        _refuse(where, "q must be [rows, heads, head_dim] of f16 or bf16")
-    n, heads, hd = shape
-    qs = _rows(where, "q", q, shape, dtype, device)
-    cu = _indices(where, "cu_rows", cu_rows, kv.n_seqs + 1, device)
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        os = heads * hd
-    else:
-        os = _rows(where, "out", out, shape, dtype, device)
-    at, need, held = _workspace(where, workspace, device, q, adp.adp_paged_chunk_attention_workspace, kv, heads, n, window, sinks)
-    _call(device, "adp_paged_chunk_attention", kv, q.data_ptr(), dt, heads, qs, cu, n, hd ** -0.5 if scale is None else scale, window,
-          sinks, out.data_ptr(), os, at, need, _status(where, status, device))
-    return out
+    return _native().paged_chunk_attention(k_pages, v_pages, table, lens, q, cu_rows, window, sinks, scale, k_scale, v_scale, out,
+                                           workspace, status)
 
 
 def packed_attention(q, k, v, cu_q, cu_k, *, scale: float | None = None, out=None, status=None):
