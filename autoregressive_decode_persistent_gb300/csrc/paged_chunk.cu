@@ -20,13 +20,9 @@ constexpr int kKeys = kChunkKeys;
 constexpr float kRescale = 8.0f;        // base-2 growth of a row's maximum that rescales its output
 constexpr int kItems = 2;               // the piece of work and the next one
 
-// What a CTA has left for the join: its first piece's first part may go on from the CTA before, its last one may go on behind it.
-struct ChunkMeta {
-  int32_t first;              // slot 0: 0 unused, 1 a part that goes on behind this CTA, 2 the last part of its piece
-  int32_t starts;             // slot 1 holds the first part of a piece
-  int32_t row0, tokens, head;  // that piece: its first packed row, tokens, KV head
-  int32_t pad[3];
-};
+// What a range of work says of its first part of a piece (a word in global memory): nothing yet, the part is written and goes on in
+// the next range, it is written and ends there, or the range has none.
+enum PartState : int32_t { kPartOpen = 0, kPartGoesOn = 1, kPartEnds = 2, kPartNone = 3 };
 
 struct ChunkArgs {
   PagedView c;
@@ -40,9 +36,9 @@ struct ChunkArgs {
   int32_t even_scales;           // e4m3: four positions' scales are 16 aligned bytes wherever their pages lie
   uint32_t neg;                  // scale < 0: the instruction descriptor's bit that negates A
   int32_t rows_cap;              // rows of a partial result (128 or 256)
-  float* part_o;                 // [ctas][2][rows_cap / 32][head_dim / 4][32 rows][4]
-  float2* part_ml;               // [ctas][2][rows_cap]
-  ChunkMeta* meta;               // [ctas]
+  float* part_o;                 // [ctas][rows_cap / 32][head_dim / 4][32 rows][4]
+  float2* part_ml;               // [ctas][rows_cap]
+  int32_t* part_state;           // [ctas], PartState
   int32_t* status;
   uint64_t wait_ns;
 };
@@ -66,7 +62,7 @@ __device__ __forceinline__ Rows rows_of(const ChunkArgs& a, int b, int32_t* stat
 struct Item {
   int32_t q0, lq, len, b, t0, h;
   int32_t i0, i1;
-  int32_t part;  // -1: all of its blocks; else the slot of the partial result
+  int32_t part;  // -1: all of its blocks; 0: a part that goes on from the range before; 1: the first part of several
   int32_t stop;  // no work is left
   __device__ __forceinline__ int first() const { return len - lq + t0; }
   __device__ __forceinline__ int last(int span) const { return len - lq + min(t0 + span, lq) - 1; }
@@ -195,6 +191,15 @@ struct Finder {
 struct SlotScales {
   float k[kKeys], v[kKeys], lv[kKeys], top[4];
 };
+
+__device__ __forceinline__ void say_part(const ChunkArgs& a, int range, int32_t state) {
+  asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(a.part_state + range), "r"(state) : "memory");
+}
+__device__ __forceinline__ int32_t part_said(const ChunkArgs& a, int range) {
+  int32_t v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(a.part_state + range) : "memory");
+  return v;
+}
 
 template <int HD, int CDT>
 struct ChunkSmem {
@@ -367,6 +372,9 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
     *reinterpret_cast<uint64_t*>(ctl + 4) = a.wait_ns;
     mbar_fence_init();
   }
+  // A range's last piece is joined by the CTA that starts it, which waits for the next range's beginning: that range belongs to a CTA
+  // with a lower number, which is launched no later.
+  const int range = (int)(gridDim.x - 1 - blockIdx.x);
   // ---- units and pairs of every 32 sequences (one warp's worth: the finding warp adds them up alone)
   const int n_chunks = (a.c.n_seqs + 31) / 32, span = 2 * a.tok;
   Units* chunks = reinterpret_cast<Units*>(smem);  // [n_chunks] (before anything is copied there)
@@ -522,10 +530,10 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
         }
         return f.place(h, x);
       };
-      const Place end = cut_at((int)blockIdx.x + 1);
-      Place p = cut_at((int)blockIdx.x);
+      const Place end = cut_at(range + 1);
+      Place p = cut_at(range);
       fence_async_smem();  // (the sums have been read before copies take their place)
-      ChunkMeta left{};
+      if (a.part_state && lane == 0 && !(p.before(end) && p.j > 0 && head_units > 0)) say_part(a, range, kPartNone);
       int published = 0, nq = 0;
       bool ok = true;
       Rows r = shfl_rows(f.mine, p.b & 31);
@@ -560,13 +568,6 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
           if (published >= kItems && !(ok = wait(&iempty[s], (published / kItems - 1) & 1))) break;
           const bool before = p.j > 0, behind = i1 < n;
           const Item w{r.q0, r.lq, r.len, p.b, p.t * span, p.h, p.j, i1, before ? 0 : behind ? 1 : -1, 0};
-          if (before) left.first = behind ? 1 : 2;
-          if (!before && behind) {
-            left.starts = 1;
-            left.row0 = r.q0 + w.t0;
-            left.tokens = min(span, r.lq - w.t0);
-            left.head = p.h;
-          }
           __syncwarp();
           if (lane == 0) {
             items[s] = w;
@@ -602,7 +603,6 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
         }
       }
       if (!ok) *ab = 1;
-      if (lane == 0 && a.meta) a.meta[blockIdx.x] = left;
       // no copy may still be writing this CTA's shared memory when it exits
       if (nq > 0) mbar_wait(qfull, (nq - 1) & 1, &never, a.wait_ns);
       __syncwarp();
@@ -1224,7 +1224,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
       tc_fence_after();
       g += n;
       // (e4m3: O is relative to mo, and brought to m in two steps)
-      const float own_f = Q8 && mo > -INFINITY ? exp2_fast(0.5f * (mo - m)) : 1.0f;
+      float own_f = Q8 && mo > -INFINITY ? exp2_fast(0.5f * (mo - m)) : 1.0f;
       auto load_o = [&](int c0, float f, float (&o)[16]) {  // 16 columns of O times f, 0 where nothing was seen
         uint32_t u[16];
         tmem_ld16(tO + c0, u);
@@ -1236,7 +1236,53 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
         }
       };
       uint8_t* const out = a.out + (int64_t)(w.q0 + tok) * a.out_stride + (int64_t)(w.h * a.group + row_head) * HD * 2;
-      const int64_t prow = ((int64_t)blockIdx.x * 2 + max(w.part, 0)) * a.rows_cap;  // the first row of a partial result
+      const int64_t prow = (int64_t)range * a.rows_cap;  // the first row of this range's partial result
+      const bool says = !half || (t == 0 && (!quarter || sub == 0));  // of the warps with these rows, the one that speaks for them
+      if (w.part == 1 && says && warp_live) {
+        // ---- the first part of several: the others' results, of the next ranges in turn, come to its accumulators
+        for (int c = range + 1; ok && c < (int)gridDim.x; ++c) {
+          int32_t state = part_said(a, c);
+          if (state == kPartOpen) {
+            const uint64_t t0 = globaltimer();
+            while (ok && (state = part_said(a, c)) == kPartOpen) ok = *ab == 0 && globaltimer() - t0 <= a.wait_ns;
+          }
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          state = __shfl_sync(0xFFFFFFFFu, state, 0);
+          if (!ok) break;
+          if (state == kPartNone) continue;
+          const int64_t base = (int64_t)c * a.rows_cap + (half ? row & ~31 : t * kRows + sub * 32);
+          const float2 ml = live ? a.part_ml[base + lane] : make_float2(-INFINITY, 0.0f);
+          const float4* from = reinterpret_cast<const float4*>(a.part_o) + base * (HD / 4) + lane;
+          const float mn = fmaxf(m, ml.x), to = mn == -INFINITY ? 0.0f : mn;
+          const float f = exp2_fast(m - to), g = exp2_fast(ml.x - to);
+#pragma unroll 1
+          for (int c0 = 0; c0 < HD; c0 += 64) {
+            float4 x[16];
+#pragma unroll
+            for (int p = 0; p < 16; ++p) x[p] = live ? from[(c0 / 4 + p) * 32] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              float o[16];
+              load_o(c0 + 16 * h, f, o);
+              uint32_t u[16];
+#pragma unroll
+              for (int p = 0; p < 4; ++p) {
+                const float4 y = x[4 * h + p];
+                u[4 * p] = __float_as_uint(fmaf(y.x, g, o[4 * p])), u[4 * p + 1] = __float_as_uint(fmaf(y.y, g, o[4 * p + 1]));
+                u[4 * p + 2] = __float_as_uint(fmaf(y.z, g, o[4 * p + 2])), u[4 * p + 3] = __float_as_uint(fmaf(y.w, g, o[4 * p + 3]));
+              }
+              tmem_st16(tO + c0 + 16 * h, u);
+            }
+          }
+          tmem_st_wait();
+          m = mn;
+          l = fmaf(l, f, g * ml.y);
+          own_f = 1.0f;  // (O is relative to m now)
+          if (state == kPartEnds) break;
+        }
+        if (!ok) break;
+      }
+      const bool goes_on = w.i1 < sp.n;
       int lo = 0, hi = -1;  // the blocks that values were taken out of
       auto look = [&]() {
         lo = *reinterpret_cast<volatile int32_t*>(&taken[0]);
@@ -1254,8 +1300,8 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
         for (int q = row; q < 2 * kRows; q += step) top = fmaxf(top, s_half[q]);
         const float base = top == -INFINITY ? 0.0f : top;
         for (int q = row; q < 2 * kRows; q += step) total = fmaf(exp2_fast(s_half[q] - base), s_half[2 * kRows + q], total);
-        const float f = exp2_fast(m - base) * (w.part >= 0 || total == 0.0f ? 1.0f : 1.0f / total);
-        if (w.part >= 0 && live && t == 0 && (!quarter || sub == 0)) a.part_ml[prow + row] = make_float2(top, total);
+        const float f = exp2_fast(m - base) * (w.part == 0 ? 1.0f : total == 0.0f ? 0.0f : 1.0f / total);
+        if (w.part == 0 && live && says) a.part_ml[prow + row] = make_float2(top, total);
         constexpr int C = L::kOutCols, P = C / 4;  // (two buffers of 256 rows of C floats each)
         auto cell = [&](int b, int q, int p) {
           return reinterpret_cast<float4*>(stage + (b * 2 * kRows + q) * C * 4 + ((p ^ (P == 4 ? (q >> 1) & 3 : (q >> 2) & 1)) << 4));
@@ -1275,7 +1321,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
             const float4 y = taken_out<HD, CDT>(a, w, w.len - w.lq + w.t0 + rt, col, lo, hi);
             v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
           }
-          if (w.part >= 0)
+          if (w.part == 0)
             reinterpret_cast<float4*>(a.part_o)[(prow + (q0 & ~31)) * (HD / 4) + (col / 4) * 32 + (q0 & 31)] = v;
           else
             *reinterpret_cast<uint2*>(a.out + (int64_t)(w.q0 + w.t0 + rt) * a.out_stride +
@@ -1298,9 +1344,11 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
           if (!(ok = meet())) break;
           for (int q0 = rr; q0 < fit; q0 += 2 * kRows / P) add_up(b, q0, c0 + 4 * p);
         }
+        if (w.part == 0) __threadfence();
         if (ok) ok = meet();  // (what comes next takes these maxima, sums and results' place)
         if (!ok) break;
-      } else if (w.part >= 0) {
+        if (w.part == 0 && threadIdx.x == 0) say_part(a, range, goes_on ? kPartGoesOn : kPartEnds);
+      } else if (w.part == 0) {
         // ---- a part: consecutive lanes' rows are consecutive there
         look();
         if (live) a.part_ml[prow + t * kRows + r] = make_float2(m, l);
@@ -1324,6 +1372,9 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
             __syncwarp();
           }
         }
+        __threadfence();
+        if (!(ok = meet())) break;
+        if (threadIdx.x == 0) say_part(a, range, goes_on ? kPartGoesOn : kPartEnds);
       } else if (warp_live) {
         // ---- whole: this warp's rows go through shared memory, 16-byte pieces swizzled, so that consecutive lanes store
         // consecutive pieces of a row
@@ -1369,61 +1420,12 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
       if (r == 0) report(a.status, ADP_ERR_PIPELINE_TIMEOUT);
     }
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // no MMA may be in flight (nor TMEM in use) when the accumulators are freed
   if (warp == 9) mbar_wait(done, 0, &never, a.wait_ns);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 9) tmem_dealloc(tmem, 512);
-}
-
-// Joins the pieces that several CTAs share: block (c, y) takes the piece that starts in CTA c and goes on behind it, and 32 of its
-// rows.  A lane is a row, a warp 16 of its columns (consecutive lanes' rows are consecutive in a partial result).
-template <int HD, int QDT>
-__global__ void __launch_bounds__(HD * 2) paged_chunk_join_kernel(const ChunkArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const ChunkMeta meta = a.meta[blockIdx.x];
-  const int lane = threadIdx.x & 31, c0 = (threadIdx.x >> 5) * 16, r = blockIdx.y * 32 + lane;
-  const int tile = r / kRows, rr = r % kRows, tok = tile * a.tok + rr / a.group;
-  const bool live = meta.starts && rr < a.tok * a.group && tok < meta.tokens;
-  if (!__any_sync(0xFFFFFFFFu, live)) return;
-  const int ctas = (int)gridDim.x + 1;
-  float m = -INFINITY, l = 0.0f;
-  float4 o[4] = {};
-  auto add = [&](int64_t slot) {
-    const float2 ml = live ? a.part_ml[slot * a.rows_cap + r] : make_float2(-INFINITY, 0.0f);
-    const float4* from = reinterpret_cast<const float4*>(a.part_o) + (slot * a.rows_cap + blockIdx.y * 32) * (HD / 4) + c0 * 8 + lane;
-    float4 x[4];
-#pragma unroll
-    for (int p = 0; p < 4; ++p) x[p] = live ? from[p * 32] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.0f : mn;
-    const float f = exp2_fast(m - base), g = exp2_fast(ml.x - base);
-    m = mn;
-    l = fmaf(l, f, g * ml.y);
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      o[p].x = fmaf(o[p].x, f, g * x[p].x), o[p].y = fmaf(o[p].y, f, g * x[p].y);
-      o[p].z = fmaf(o[p].z, f, g * x[p].z), o[p].w = fmaf(o[p].w, f, g * x[p].w);
-    }
-  };
-  add((int64_t)blockIdx.x * 2 + 1);
-  for (int c = (int)blockIdx.x + 1; c < ctas; c += 32) {
-    const int first = c + lane < ctas ? a.meta[c + lane].first : 0;
-    const uint32_t ends = __ballot_sync(0xFFFFFFFFu, first == 2);
-    uint32_t has = __ballot_sync(0xFFFFFFFFu, first != 0);
-    if (ends) has &= (ends ^ (ends - 1));  // up to the first end
-    for (; has; has &= has - 1) add((int64_t)(c + __ffs(has) - 1) * 2);
-    if (ends) break;
-  }
-  if (!live) return;
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint4* po = reinterpret_cast<uint4*>(a.out + (int64_t)(meta.row0 + tok) * a.out_stride +
-                                       ((int64_t)(meta.head * a.group + rr % a.group) * HD + c0) * 2);
-#pragma unroll
-  for (int p = 0; p < 4; p += 2)
-    po[p / 2] = make_uint4(pack2(o[p].x * inv, o[p].y * inv, QDT), pack2(o[p].z * inv, o[p].w * inv, QDT),
-                           pack2(o[p + 1].x * inv, o[p + 1].y * inv, QDT), pack2(o[p + 1].z * inv, o[p + 1].w * inv, QDT));
 }
 
 // ---------------------------------------------------------------- host side
@@ -1458,7 +1460,7 @@ ChunkPlan chunk_plan(const adp_paged_kv* kv, int group, int n_rows, int sms, int
   p.ctas = chunk_parts(items * (blocks + kChunkOver), items, sms);
   if (blocks >= 2 * kChunkMinPart && p.ctas > 1) {
     p.rows_cap = n_rows <= tok ? kRows : 2 * kRows;
-    p.bytes = (size_t)p.ctas * (2 * p.rows_cap * ((size_t)kv->head_dim * sizeof(float) + sizeof(float2)) + sizeof(ChunkMeta));
+    p.bytes = (size_t)p.ctas * (p.rows_cap * ((size_t)kv->head_dim * sizeof(float) + sizeof(float2)) + sizeof(int32_t));
   }
   return p;
 }
@@ -1472,18 +1474,9 @@ cudaError_t chunk_launch(const CUtensorMap (&m)[4], const ChunkArgs& a, const Ch
   constexpr size_t smem = ChunkSmem<HD, CDT>::kBytes;
   cudaError_t e = allow_smem<ChunkKey<HD, CDT, QDT, LOAD>>((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
+  if (a.part_state && (e = cudaMemsetAsync(a.part_state, 0, (size_t)p.ctas * sizeof(int32_t), st)) != cudaSuccess) return e;
   kernel<<<p.ctas, LOAD ? 512 : 384, smem, st>>>(m[0], m[1], m[2], m[3], a);
-  if ((e = cudaGetLastError()) != cudaSuccess || !p.rows_cap) return e;
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.ctas - 1, p.rows_cap / 32);  // no piece goes on behind the last CTA
-  cfg.blockDim = dim3(HD * 2);
-  cfg.stream = st;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_chunk_join_kernel<HD, QDT>, a);
+  return cudaGetLastError();
 }
 
 int chunk_check(const adp_paged_kv* kv, int32_t n_heads, int32_t n_rows, int32_t window, int32_t sinks, PagedView* c) {
@@ -1546,10 +1539,10 @@ extern "C" int adp_paged_chunk_attention(const adp_paged_kv* kv, const void* q, 
   a.neg = scale < 0.0f ? kTcIdescANeg : 0;
   a.rows_cap = plan.rows_cap;
   if (plan.bytes) {
-    const size_t rows = (size_t)plan.ctas * 2 * plan.rows_cap;
+    const size_t rows = (size_t)plan.ctas * plan.rows_cap;
     a.part_o = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + rows * kv->head_dim);
-    a.meta = reinterpret_cast<ChunkMeta*>(a.part_ml + rows);
+    a.part_state = reinterpret_cast<int32_t*>(a.part_ml + rows);
   }
   a.status = dev_status;
   const int64_t keys = (int64_t)kv->table_width * kv->page_size;

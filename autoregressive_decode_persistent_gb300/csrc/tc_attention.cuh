@@ -56,9 +56,15 @@ __device__ __noinline__ bool mbar_wait_warp_slow(uint64_t* b, uint32_t parity, v
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* b, uint32_t parity, volatile int32_t* abort) {
   return __all_sync(0xFFFFFFFFu, mbar_try_wait(b, parity)) ? true : mbar_wait_warp_slow(b, parity, abort);
 }
-// The same without a call, for kernels that share out their registers (whose calls would need the largest share).
+// The same without a call, for kernels that share out their registers (whose calls would need the largest share), and as short
+// as can be: the kernel's loops have to stay in the instruction cache.  Gives up after about 2 s (3.5e9 cycles).
 __device__ __forceinline__ bool mbar_wait_warp_inline(uint64_t* b, uint32_t parity, volatile int32_t* abort) {
-  return __all_sync(0xFFFFFFFFu, mbar_try_wait(b, parity)) ? true : mbar_wait_warp_loop(b, parity, abort);
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(b, parity))) return true;
+  const uint32_t t0 = (uint32_t)clock();
+  do {
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(b, parity))) return true;
+  } while (__all_sync(0xFFFFFFFFu, *abort == 0 && (uint32_t)clock() - t0 < 3500000000u));
+  return false;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
