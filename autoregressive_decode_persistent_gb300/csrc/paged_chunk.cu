@@ -112,6 +112,9 @@ __device__ __forceinline__ int pair_blocks(const ChunkArgs& a, const Rows& r, in
   const int span = 2 * a.tok, first = r.len - r.lq + t * span, last = r.len - r.lq + min((t + 1) * span, r.lq) - 1;
   return chunk_span(first, last, a.window, a.sinks).n;
 }
+__device__ __forceinline__ int pair_units(const ChunkArgs& a, const Rows& r, int t) {
+  return pair_blocks(a, r, t) + chunk_over(r.lq - t * 2 * a.tok, a.tok);
+}
 __device__ __forceinline__ Rows shfl_rows(const Rows& r, int l) {
   return Rows{__shfl_sync(0xFFFFFFFFu, r.q0, l), __shfl_sync(0xFFFFFFFFu, r.lq, l), __shfl_sync(0xFFFFFFFFu, r.len, l)};
 }
@@ -121,12 +124,12 @@ __device__ __forceinline__ int64_t sequence_units(const ChunkArgs& a, const Rows
   const int span = 2 * a.tok, pairs = (r.lq + span - 1) / span;
   int64_t sum = 0;
   if (pairs <= kAlone)
-    for (int t = 0; t < pairs; ++t) sum += pair_blocks(a, r, t) + kChunkOver;
+    for (int t = 0; t < pairs; ++t) sum += pair_units(a, r, t);
   for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, pairs > kAlone); todo; todo &= todo - 1) {
     const int l = __ffs(todo) - 1, n = __shfl_sync(0xFFFFFFFFu, pairs, l);
     const Rows o = shfl_rows(r, l);
     int64_t s = 0;
-    for (int t = lane; t < n; t += 32) s += pair_blocks(a, o, t) + kChunkOver;
+    for (int t = lane; t < n; t += 32) s += pair_units(a, o, t);
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
     if (lane == l) sum = s;
@@ -174,14 +177,14 @@ struct Finder {
     const int n = (o.lq + span - 1) / span;
     for (int t0 = 0; t0 < n; t0 += 32) {
       const int blocks = t0 + lane < n ? pair_blocks(a, o, t0 + lane) : 0;
-      const int64_t own = t0 + lane < n ? blocks + kChunkOver : 0, sum = scan_inclusive(own, lane);
+      const int64_t own = t0 + lane < n ? pair_units(a, o, t0 + lane) : 0, sum = scan_inclusive(own, lane);
       const int p = __popc(__ballot_sync(0xFFFFFFFFu, sum <= x));
       if (p == 32) {
         x -= __shfl_sync(0xFFFFFFFFu, sum, 31);
         continue;
       }
       x -= __shfl_sync(0xFFFFFFFFu, sum - own, p);
-      return Place{h, chunk * 32 + l, t0 + p, chunk_cut(__shfl_sync(0xFFFFFFFFu, blocks, p), x)};
+      return Place{h, chunk * 32 + l, t0 + p, chunk_cut(__shfl_sync(0xFFFFFFFFu, blocks, p), x - chunk_over(o.lq - (t0 + p) * span, a.tok))};
     }
     return Place{h, chunk * 32 + l, n, 0};  // (the offsets changed while this call ran)
   }
@@ -270,7 +273,7 @@ __device__ __forceinline__ float4 taken_out(const ChunkArgs& a, const Item& w, i
   float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int i = w.i0; i < w.i1; ++i) {
     const int kb = chunk_block(sp, i) * kKeys;
-    if (kb < lo || kb > hi || !(w.quarter(a.few) || edge_block(kb, first, last, a.window, a.sinks))) continue;
+    if (kb < lo || kb > hi || !((CDT != DT_E4M3 && w.quarter(a.few)) || edge_block(kb, first, last, a.window, a.sinks))) continue;
     for (int key = kb; key < kb + kKeys && key <= pos; ++key) {
       if (key < from && key >= a.sinks) continue;
       const int page = paged_page(a.c.table + (int64_t)w.b * a.c.table_width, a.c.table_width, a.c.n_pages, a.c.log2_page, key);
@@ -407,8 +410,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
     atomicMax(&taken[1], kb);
   };
   // Four warps (lt: the thread among them) bring the codes of K (op 0) or V (op 1) of block g, at positions from kb on, to fp16
-  // (exactly) in the block's slot, and the rows' scales beside them.  The slot is free, and so the codes' own
-  // place has been used for an earlier block of codes before: a barrier's phases tell only two apart.
+  // (exactly) in the block's slot, which is free, and the rows' scales beside them.
   [[maybe_unused]] auto bring_codes = [&](int lt, int op, int g, int slot, int kb, int last, bool edge) {
     if constexpr (Q8) {
       constexpr int PPR = HD / 16, RSTEP = 128 / PPR, NR = kKeys / RSTEP, R = L::kRaw;  // 16-byte pieces of a row; rows of this thread
@@ -861,8 +863,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
       bool ok = true;
       auto wait_slot = [&](int n) { return n < NS || wait(&empty[n % NS], (n / NS - 1) & 1); };
       if constexpr (Q8) {
-        // ---- four warps that bring codes of K to fp16 in the ring, and those of V where the item has two tiles (else the
-        // tile's own softmax warps bring them there, which have little else to do)
+        // ---- four warps that bring codes to fp16 in the ring
         int g = 0, slot = 0;  // blocks so far, and the next one's slot
         for (int it = 0; ok; ++it) {
           const int is = it % kItems;
@@ -871,14 +872,13 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&iempty[is]);
           if (w.stop) break;
-          const int first = w.first(), last = w.last(span), ops = w.half(a.tok) ? 1 : 2;
-          const bool quarter = w.quarter(a.few);
+          const int first = w.first(), last = w.last(span);
           const ChunkSpan sp = chunk_span(first, last, a.window, a.sinks);
           for (int i = w.i0; ok && i < w.i1; ++i, ++g) {
             const int kb = chunk_block(sp, i) * kKeys;
-            const bool edge = quarter || edge_block(kb, first, last, a.window, a.sinks);
+            const bool edge = edge_block(kb, first, last, a.window, a.sinks);
 #pragma unroll 1
-            for (int op = 0; ok && op < ops; ++op)
+            for (int op = 0; ok && op < 2; ++op)
               ok = (op == 1 || wait_slot(g)) && bring_codes(lt, op, g, slot, kb, last, edge);
             if (++slot == NS) slot = 0;
           }
@@ -1165,9 +1165,6 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
         const uint32_t buf = ns & 1;
         const int i = own.off + k * own.step, slot = (g + i) % NS, kb = chunk_block(sp, w.i0 + i) * kKeys;
         if (!(ok = wait(&sfull[2 * t + buf], (ns >> 1) & 1))) break;
-        if constexpr (Q8) {  // (the block's scores are here, so its slot is its own and V may be written)
-          if (half && !(ok = bring_codes(r, 1, g + i, slot, kb, last, quarter || edge_block(kb, first, last, a.window, a.sinks)))) break;
-        }
         tc_fence_after();
         __syncwarp();
         if constexpr (Q8) {  // (the scales of V come with V)
@@ -1306,27 +1303,33 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
         auto cell = [&](int b, int q, int p) {
           return reinterpret_cast<float4*>(stage + (b * 2 * kRows + q) * C * 4 + ((p ^ (P == 4 ? (q >> 1) & 3 : (q >> 2) & 1)) << 4));
         };
-        // this thread adds up piece p of row rr of some columns (and of the rows 256 / P behind, where all rows of a tile differ)
-        const int id = t * kRows + r, p = id % P, rr = id / P, fit = min(quarter ? 32 : kRows, (w.lq - w.t0) * a.group);
-        auto add_up = [&](int b, int q0, int col) {
+        // this thread adds up piece p of row rr of some columns (and, with four pieces, of row rr + 64 where all 128 rows differ)
+        const int id = t * kRows + r, p = id % P, rr = id / P, fit = min(w.lq - w.t0, quarter ? a.few : a.tok) * a.group;
+        constexpr int kMine = P / 2;
+        uint8_t* to[kMine];
+        int tok_of[kMine];
+#pragma unroll
+        for (int k = 0; k < kMine; ++k) {
+          const int q0 = rr + 64 * k;
+          tok_of[k] = q0 / a.group;
+          to[k] = w.part == 0 ? reinterpret_cast<uint8_t*>(a.part_o) + ((prow + (q0 & ~31)) * (HD / 4) + (q0 & 31)) * 16
+                              : a.out + (int64_t)(w.q0 + w.t0 + tok_of[k]) * a.out_stride +
+                                    (int64_t)(w.h * a.group + q0 - tok_of[k] * a.group) * HD * 2;
+        }
+        auto add_up = [&](int b, int k, int col) {
           float4 x[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            x[k] = quarter || k == 0 || k == 4 ? *cell(b, q0 + 32 * k, p) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int e = 0; e < 8; ++e)
+            x[e] = quarter || e == 0 || e == 4 ? *cell(b, rr + 64 * k + 32 * e, p) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v.x += x[k].x, v.y += x[k].y, v.z += x[k].z, v.w += x[k].w;
-          const int rt = q0 / a.group;
+          for (int e = 0; e < 8; ++e) v.x += x[e].x, v.y += x[e].y, v.z += x[e].z, v.w += x[e].w;
           if (hi >= 0) {
-            const float4 y = taken_out<HD, CDT>(a, w, w.len - w.lq + w.t0 + rt, col, lo, hi);
+            const float4 y = taken_out<HD, CDT>(a, w, w.len - w.lq + w.t0 + tok_of[k], col, lo, hi);
             v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
           }
-          if (w.part == 0)
-            reinterpret_cast<float4*>(a.part_o)[(prow + (q0 & ~31)) * (HD / 4) + (col / 4) * 32 + (q0 & 31)] = v;
-          else
-            *reinterpret_cast<uint2*>(a.out + (int64_t)(w.q0 + w.t0 + rt) * a.out_stride +
-                                      ((int64_t)(w.h * a.group + q0 - rt * a.group) * HD + col) * 2) =
-                make_uint2(pack2(v.x, v.y, QDT), pack2(v.z, v.w, QDT));
+          if (w.part == 0) *reinterpret_cast<float4*>(to[k] + col * 128) = v;  // (a piece's 32 rows are consecutive there)
+          else *reinterpret_cast<uint2*>(to[k] + col * 2) = make_uint2(pack2(v.x, v.y, QDT), pack2(v.z, v.w, QDT));
         };
 #pragma unroll 1
         for (int c0 = 0; c0 < HD; c0 += C) {
@@ -1342,7 +1345,9 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
             }
           }
           if (!(ok = meet())) break;
-          for (int q0 = rr; q0 < fit; q0 += 2 * kRows / P) add_up(b, q0, c0 + 4 * p);
+#pragma unroll
+          for (int k = 0; k < kMine; ++k)
+            if (rr + 64 * k < fit) add_up(b, k, c0 + 4 * p);
         }
         if (w.part == 0) __threadfence();
         if (ok) ok = meet();  // (what comes next takes these maxima, sums and results' place)
@@ -1457,7 +1462,7 @@ ChunkPlan chunk_plan(const adp_paged_kv* kv, int group, int n_rows, int sms, int
   const int64_t seen = ((int64_t)window + span + kKeys - 2) / kKeys + 1 + ((int64_t)sinks + kKeys - 1) / kKeys;
   const int64_t blocks = seen < all ? seen : all;
   ChunkPlan p{};
-  p.ctas = chunk_parts(items * (blocks + kChunkOver), items, sms);
+  p.ctas = chunk_parts(items * (blocks + chunk_over(0, tok)), items, sms);
   if (blocks >= 2 * kChunkMinPart && p.ctas > 1) {
     p.rows_cap = n_rows <= tok ? kRows : 2 * kRows;
     p.bytes = (size_t)p.ctas * (p.rows_cap * ((size_t)kv->head_dim * sizeof(float) + sizeof(float2)) + sizeof(int32_t));
