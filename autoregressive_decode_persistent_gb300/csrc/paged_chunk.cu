@@ -30,7 +30,7 @@ struct ChunkArgs {
   uint8_t* out;
   int64_t out_stride;            // bytes
   int32_t n_rows, group, tok;    // query heads per KV head; tokens of a tile
-  int32_t few;                   // tokens of a quarter of a tile (0: a token does not fit)
+  int32_t few;                   // tokens of a quarter of a tile (0: a token does not fit, or there are no quarters)
   int32_t window, sinks;
   float scale_log2;              // of |scale|, and above 0
   int32_t even_scales;           // e4m3: four positions' scales are 16 aligned bytes wherever their pages lie
@@ -273,7 +273,7 @@ __device__ __forceinline__ float4 taken_out(const ChunkArgs& a, const Item& w, i
   float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int i = w.i0; i < w.i1; ++i) {
     const int kb = chunk_block(sp, i) * kKeys;
-    if (kb < lo || kb > hi || !((CDT != DT_E4M3 && w.quarter(a.few)) || edge_block(kb, first, last, a.window, a.sinks))) continue;
+    if (kb < lo || kb > hi || !(w.quarter(a.few) || edge_block(kb, first, last, a.window, a.sinks))) continue;
     for (int key = kb; key < kb + kKeys && key <= pos; ++key) {
       if (key < from && key >= a.sinks) continue;
       const int page = paged_page(a.c.table + (int64_t)w.b * a.c.table_width, a.c.table_width, a.c.n_pages, a.c.log2_page, key);
@@ -372,6 +372,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
     *holes = 0;
     taken[0] = 0x7FFFFFFF;
     taken[1] = -1;
+    ctl[3] = (int32_t)(a.wait_ns >> 19 < 0x7FFFFFFF ? a.wait_ns >> 19 : 0x7FFFFFFF);  // (2^20 cycles are 2^19 ns and more)
     *reinterpret_cast<uint64_t*>(ctl + 4) = a.wait_ns;
     mbar_fence_init();
   }
@@ -580,7 +581,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
             if (nq > 0 && !(ok = wait(qempty, (nq - 1) & 1))) break;
             if (lane == 0) {
               // (a quarter of a tile four times, or the item's tiles)
-              const bool quarter = w.quarter(a.few);
+              const bool quarter = !Q8 && w.quarter(a.few);
               const int boxes = quarter ? 4 : w.half(a.tok) ? 1 : 2, tok = quarter ? a.few : a.tok;
               const uint32_t step = quarter ? 32 * 128 : L::kQTile;
               mbar_arrive_expect_tx(qfull, (uint32_t)(boxes * tok * a.group) * 128 * (HD / 64));
@@ -818,19 +819,20 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
           if (elect_one()) mbar_arrive(qempty);
           __syncwarp();
         }
-        // The next block's scores go in front of this one's product where its K is there: else the product comes first, for
-        // the slot that the other block waits for may be this one's.
+        // The next block's scores go in front of this one's product.  Where tiles take turns, and with the few slots of fp16 from
+        // codes, only if its K is there: the slot that it waits for may be this block's.
+        const bool always = !Q8 && own.step == 1;
         int scored = 0;
 #pragma unroll 1
         for (int k = 0; k < own.n; ++k) {
           if (scored == k && !(ok = score(scored++))) break;
           if (scored < own.n) {
-            bool there = true;
+            bool there = always || __all_sync(0xFFFFFFFFu, mbar_test_wait(&full[ks], kphase));
             while (there && at < own.off + scored * own.step) {
+              skip();
               there = __all_sync(0xFFFFFFFFu, mbar_test_wait(&full[ks], kphase));
-              if (there) skip();
             }
-            if (there && __all_sync(0xFFFFFFFFu, mbar_test_wait(&full[ks], kphase)) && !(ok = score(scored++))) break;
+            if (there && !(ok = score(scored++))) break;
           }
           if (!(ok = wait(&pready[2 * t + p_buf], p_phase))) break;
           if constexpr (Q8) {
@@ -990,7 +992,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
       const int first = w.first(), last = w.last(span), n = w.i1 - w.i0;
       const ChunkSpan sp = chunk_span(first, last, a.window, a.sinks);
       const Own own = own_blocks(w, sp, t, a.tok);
-      const bool half = w.half(a.tok), quarter = w.quarter(a.few);
+      const bool half = w.half(a.tok), quarter = !Q8 && w.quarter(a.few);
       const int row = quarter ? lane : r, row_tok = row / a.group, row_head = row - row_tok * a.group;
       const int tok = w.t0 + (half ? 0 : t * a.tok) + row_tok;
       const bool live = row_tok < (quarter ? a.few : a.tok) && tok < w.lq;
@@ -1207,8 +1209,9 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
           __syncwarp();
         }
         if (warp_live) {
-          ok = quarter ? block(std::integral_constant<int, kKeys / 4>(), sub * (kKeys / 4), k, buf, slot, kb)
-                       : block(std::integral_constant<int, kKeys>(), 0, k, buf, slot, kb);
+          if constexpr (Q8) ok = block(std::integral_constant<int, kKeys>(), 0, k, buf, slot, kb);
+          else ok = quarter ? block(std::integral_constant<int, kKeys / 4>(), sub * (kKeys / 4), k, buf, slot, kb)
+                            : block(std::integral_constant<int, kKeys>(), 0, k, buf, slot, kb);
           if (!ok) break;
         }
         __syncwarp();
@@ -1536,7 +1539,9 @@ extern "C" int adp_paged_chunk_attention(const adp_paged_kv* kv, const void* q, 
   a.n_rows = n_rows;
   a.group = group;
   a.tok = kRows / group;
-  a.few = 32 / group;
+  // Rows that fit a warp have quarters of tiles, but for e4m3, whose loops are bound by their instructions (32 sequences of up to 8
+  // tokens: 146 us without, 157 with them; over 16 bits 115 with and 130 without).
+  a.few = kv->dtype == ADP_E4M3 ? 0 : 32 / group;
   // (a scale of 0 becomes the least normal number: the scores' differences vanish all the same, and what is not seen stays at
   // -infinity)
   a.scale_log2 = fmaxf(log2_scale(fabsf(scale)), kScaleMin);

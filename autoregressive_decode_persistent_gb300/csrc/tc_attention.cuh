@@ -57,13 +57,13 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* b, uint32_t parity, vol
   return __all_sync(0xFFFFFFFFu, mbar_try_wait(b, parity)) ? true : mbar_wait_warp_slow(b, parity, abort);
 }
 // The same without a call, for kernels that share out their registers (whose calls would need the largest share), and as short
-// as can be: the kernel's loops have to stay in the instruction cache.  Gives up after about 2 s (3.5e9 cycles).
+// as can be: the kernel's loops have to stay in the instruction cache.  Its limit, in 2^20 cycles, lies 8 bytes behind the abort word.
 __device__ __forceinline__ bool mbar_wait_warp_inline(uint64_t* b, uint32_t parity, volatile int32_t* abort) {
   if (__all_sync(0xFFFFFFFFu, mbar_try_wait(b, parity))) return true;
-  const uint32_t t0 = (uint32_t)clock();
+  const uint32_t t0 = (uint32_t)(clock64() >> 20);
   do {
     if (__all_sync(0xFFFFFFFFu, mbar_try_wait(b, parity))) return true;
-  } while (__all_sync(0xFFFFFFFFu, *abort == 0 && (uint32_t)clock() - t0 < 3500000000u));
+  } while (__all_sync(0xFFFFFFFFu, *abort == 0 && (uint32_t)(clock64() >> 20) - t0 <= (uint32_t)abort[2]));
   return false;
 }
 
