@@ -345,9 +345,9 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], LOAD ? 4 : 1);
+      mbar_init(&full[s], Q8 ? 2 : LOAD ? 4 : 1);
       mbar_init(&empty[s], 2);  // tiles
-      if constexpr (Q8) mbar_init(&vfull[s], 4);
+      if constexpr (Q8) mbar_init(&vfull[s], 2);
       hole[s] = 0;
     }
     mbar_init(qfull, 1);
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
     }
     for (int i = 0; i < L::kRaw; ++i) {
       mbar_init(&rawfull[i], 1);
-      mbar_init(&rawempty[i], 4);
+      mbar_init(&rawempty[i], 2);
     }
     *ab = 0;
     *holes = 0;
@@ -410,11 +410,11 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
     atomicMin(&taken[0], kb);
     atomicMax(&taken[1], kb);
   };
-  // Four warps (lt: the thread among them) bring the codes of K (op 0) or V (op 1) of block g, at positions from kb on, to fp16
+  // Two warps (lt: the thread among them) bring the codes of K (op 0) or V (op 1) of block g, at positions from kb on, to fp16
   // (exactly) in the block's slot, which is free, and the rows' scales beside them.
   [[maybe_unused]] auto bring_codes = [&](int lt, int op, int g, int slot, int kb, int last, bool edge) {
     if constexpr (Q8) {
-      constexpr int PPR = HD / 16, RSTEP = 128 / PPR, NR = kKeys / RSTEP, R = L::kRaw;  // 16-byte pieces of a row; rows of this thread
+      constexpr int PPR = HD / 16, RSTEP = 64 / PPR, NR = kKeys / RSTEP, R = L::kRaw;  // 16-byte pieces of a row; rows of this thread
       const int q = lt >> 5, n_raw = 2 * g + op, rs = n_raw % R;
       // (head_dim 128: half a row of an even and of an odd position to every 8 lanes, so that their stores meet in no bank)
       const int piece = HD == 128 ? ((lane >> 3) & 1) * 4 + (lane & 3) : lane & 3;
@@ -427,9 +427,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(c[n].x), "=r"(c[n].y), "=r"(c[n].z), "=r"(c[n].w)
                      : "r"(raw + n * RSTEP * HD));
-      const bool mine = q < 2;  // holds a row's scale
-      float sc = 0.0f;
-      if (mine) sc = reinterpret_cast<const volatile float*>(smem + L::kRawAt + rs * L::kRawBytes + kKeys * HD)[lt];
+      float sc = reinterpret_cast<const volatile float*>(smem + L::kRawAt + rs * L::kRawBytes + kKeys * HD)[lt];
       const uint64_t out = *reinterpret_cast<volatile uint64_t*>(&rawhole[rs]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&rawempty[rs]);
@@ -469,19 +467,17 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
         asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to1 + n * RSTEP * 128), "r"(f[4]), "r"(f[5]), "r"(f[6]), "r"(f[7]) : "memory");
       }
       SlotScales& z = s_scale[slot];
-      if (mine) {
-        if (op == 0) {
-          z.k[lt] = sc;
-          if (lt == 0) hole[slot] = out;
-        } else {
-          const float lv = log2_scale_of(sc);
-          z.v[lt] = sc;
-          z.lv[lt] = lv;
-          float top = lv;
+      if (op == 0) {
+        z.k[lt] = sc;
+        if (lt == 0) hole[slot] = out;
+      } else {
+        const float lv = log2_scale_of(sc);
+        z.v[lt] = sc;
+        z.lv[lt] = lv;
+        float top = lv;
 #pragma unroll
-          for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-          if (lane == 0) z.top[q] = top;
-        }
+        for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        if (lane == 0) z.top[q] = top;
       }
       fence_async_smem();
       __syncwarp();
@@ -665,11 +661,20 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
           for (int i = g > NS ? g - NS : 0; i < g; ++i) mbar_wait(&full[i % NS], (i / NS) & 1, &never, a.wait_ns);
         __syncwarp();
       } else if constexpr (Q8) {
-        // ---- copies blocks of codes of K, then of V, with their scales: the rows of a page and head are consecutive
+        // ---- copies blocks of codes with their scales: the rows of a page and head are consecutive.  All of a block's copies go out
+        // at once, a lane's each: of a page K's codes, V's, K's scales and V's.  (This warp's instructions count: with K's and V's copies
+        // one after the other, 4 rows of each of 32 sequences over 8,192 positions in pages of 16 took 295 us, this way 255.)
         constexpr int R = L::kRaw;
-        const int lg = min(a.c.log2_page, 6), box = 1 << lg, boxes = kKeys >> lg, in_page = (1 << a.c.log2_page) - 1;
-        const uint32_t raw = smem_u32(smem + L::kRawAt);
-        int g = 0;  // blocks of K or of V so far
+        const int lg = min(a.c.log2_page, 6), box = 1 << lg, in_page = (1 << a.c.log2_page) - 1;
+        const bool is_v = lane & 1, is_scale = lane & 2;
+        const uint8_t* const base = is_scale ? reinterpret_cast<const uint8_t*>(is_v ? a.c.v_scale : a.c.k_scale) : is_v ? a.c.v : a.c.k;
+        const int64_t page_step = is_scale ? a.c.scale_stride * 4 : a.c.page_bytes;
+        const uint32_t row_bytes = is_scale ? 4 : HD, bytes = box * row_bytes;
+        const uint32_t raw = smem_u32(smem + L::kRawAt) + (is_scale ? kKeys * HD : 0);
+        const bool on = !is_scale || a.even_scales;
+        const uint32_t expect = kKeys * HD + (a.even_scales ? kKeys * 4 : 0);
+        uint32_t s = is_v, phase = 1;  // this lane's buffer, of the block's K or V
+        int g = 0;                     // blocks so far
         bool ok = true;
         for (int it = 0; ok; ++it) {
           const int is = it % kItems;
@@ -681,73 +686,53 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
           const int last = w.last(span);
           const ChunkSpan sp = chunk_span(w.first(), last, a.window, a.sinks);
           const int32_t* trow = a.c.table + (int64_t)w.b * a.c.table_width;
-          // 32 entries of the table row at a time, a lane's at entry base + lane
-          int base = -64, held = 0;
-          for (int i = w.i0; ok && i < w.i1; ++i) {
+          const uint8_t* const head = base + (int64_t)(w.h << a.c.log2_page) * row_bytes;
+          const int mine = (lane >> 2) << lg;  // this lane's first position of a block
+          int next = w.i0 < w.i1 ? table_entry(a, trow, chunk_block(sp, w.i0) * kKeys + mine) : 0;
+          for (int i = w.i0; i < w.i1; ++i, ++g) {
             const int kb = chunk_block(sp, i) * kKeys;
-            int page[2] = {-2, -2}, at[2] = {0, 0};  // of this lane's boxes
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              if (k * 32 >= boxes) continue;
-              const int c = min(lane + 32 * k, boxes - 1), pos = kb + c * box, index = pos >> a.c.log2_page;
-              const int lo = (kb + k * 32 * box) >> a.c.log2_page, hi = (kb + (min(boxes, k * 32 + 32) - 1) * box) >> a.c.log2_page;
-              if (lo < base || hi >= base + 32) {
-                base = lo;
-                held = __ldg(trow + min(base + lane, a.c.table_width - 1));
-              }
-              const int entry = __shfl_sync(0xFFFFFFFFu, held, index - base);
-              at[k] = pos & in_page;
-              page[k] = lane + 32 * k < boxes ? page_of(a, entry, pos, box, sp.low, last) : -2;
-            }
+            int entry = next;
+            if (i + 1 < w.i1) next = table_entry(a, trow, chunk_block(sp, i + 1) * kKeys + mine);
+            if (!(ok = wait(&rawempty[s], phase))) break;
             uint64_t out = 0;  // positions without a place
-            if (__any_sync(0xFFFFFFFFu, page[0] == -1 || page[1] == -1)) {
-              const uint32_t o0 = __ballot_sync(0xFFFFFFFFu, page[0] == -1), o1 = __ballot_sync(0xFFFFFFFFu, page[1] == -1);
-              for (int c = 0; c < boxes; ++c)
-                if (((c < 32 ? o0 : o1) >> (c & 31)) & 1) out |= (box == 64 ? ~0ull : (1ull << box) - 1) << (c * box);
-              if (lane == 0) {
-                *holes = 1;
-                report(a.status, ADP_ERR_INVALID_ARG);
-              }
+#pragma unroll 1
+            for (int at = mine; at - mine < kKeys; at += 8 << lg) {  // (more than once where a page has less than 8 positions)
+              const int pos = kb + at;
+              if (at != mine) entry = table_entry(a, trow, pos);
+              const int page = at < kKeys ? page_of(a, entry, pos, box, sp.low, last) : -2;
+              for (uint32_t m = __ballot_sync(0xFFFFFFFFu, page == -1); m; m &= m - 1)
+                out |= (box == 64 ? ~0ull : (1ull << box) - 1) << __shfl_sync(0xFFFFFFFFu, at, __ffs(m) - 1);
+              if (on && at < kKeys)
+                bulk_load(raw + s * L::kRawBytes + at * row_bytes,
+                          page < 0 ? reinterpret_cast<const uint8_t*>(zero_codes) : head + page * page_step + (pos & in_page) * row_bytes,
+                          bytes, &rawfull[s]);
             }
+            if (!a.even_scales) {
+              const uint32_t sk = __shfl_sync(0xFFFFFFFFu, s, 0), sv = __shfl_sync(0xFFFFFFFFu, s, 1);
 #pragma unroll 1
-            for (int op = 0; op < 2; ++op, ++g) {
-              const int s = g % R;
-              if (g >= R && !(ok = wait(&rawempty[s], (g / R - 1) & 1))) break;
-              const uint8_t* const codes = op ? a.c.v : a.c.k;
-              const float* const scales = op ? a.c.v_scale : a.c.k_scale;
-              const uint32_t to = raw + s * L::kRawBytes;
-              if (lane == 0) rawhole[s] = out;
-              if (!a.even_scales) {
-#pragma unroll 1
-                for (int r = lane; r < kKeys; r += 32) {
-                  const int pos = kb + r, e = page_of(a, table_entry(a, trow, pos), pos, 1, sp.low, last);
-                  reinterpret_cast<float*>(smem + L::kRawAt + s * L::kRawBytes + kKeys * HD)[r] =
-                      e < 0 ? 0.0f : scales[(int64_t)e * a.c.scale_stride + (w.h << a.c.log2_page) + (pos & in_page)];
-                }
-              }
-              __syncwarp();
-              if (lane == 0) mbar_arrive_expect_tx(&rawfull[s], kKeys * HD + (a.even_scales ? kKeys * 4 : 0));
-              __syncwarp();
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int c = lane + 32 * k;
-                if (c >= boxes) continue;
-                const int64_t cell = (w.h << a.c.log2_page) + at[k];
-                bulk_load(to + c * box * HD,
-                          page[k] < 0 ? reinterpret_cast<const uint8_t*>(zero_codes) : codes + (int64_t)page[k] * a.c.page_bytes + cell * HD,
-                          box * HD, &rawfull[s]);
-                if (a.even_scales)
-                  bulk_load(to + kKeys * HD + c * box * 4,
-                            page[k] < 0 ? reinterpret_cast<const float*>(zero_codes) : scales + (int64_t)page[k] * a.c.scale_stride + cell,
-                            box * 4, &rawfull[s]);
+              for (int x = lane; x < 2 * kKeys; x += 32) {
+                const int r = x % kKeys, pos = kb + r, e = page_of(a, table_entry(a, trow, pos), pos, 1, sp.low, last);
+                const float* const scales = x < kKeys ? a.c.k_scale : a.c.v_scale;
+                reinterpret_cast<float*>(smem + L::kRawAt + (x < kKeys ? sk : sv) * L::kRawBytes + kKeys * HD)[r] =
+                    e < 0 ? 0.0f : scales[(int64_t)e * a.c.scale_stride + (w.h << a.c.log2_page) + (pos & in_page)];
               }
               __syncwarp();
             }
+            if (lane < 2) {  // (K's buffer and V's; behind the copies, whose bytes count all the same)
+              rawhole[s] = out;
+              mbar_arrive_expect_tx(&rawfull[s], expect);
+            }
+            if (out && lane == 0) {
+              *holes = 1;
+              report(a.status, ADP_ERR_INVALID_ARG);
+            }
+            s += 2;
+            if (s >= R) s -= R, phase ^= 1;
           }
         }
         if (!ok) *ab = 1;
         if (lane == 0)
-          for (int i = g > R ? g - R : 0; i < g; ++i) mbar_wait(&rawfull[i % R], (i / R) & 1, &never, a.wait_ns);
+          for (int i = 2 * g > R ? 2 * g - R : 0; i < 2 * g; ++i) mbar_wait(&rawfull[i % R], (i / R) & 1, &never, a.wait_ns);
         __syncwarp();
       }
     } else {
@@ -865,7 +850,8 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
       bool ok = true;
       auto wait_slot = [&](int n) { return n < NS || wait(&empty[n % NS], (n / NS - 1) & 1); };
       if constexpr (Q8) {
-        // ---- four warps that bring codes to fp16 in the ring
+        // ---- two warps bring codes of K to fp16 in the ring, and two those of V (all four K's, then V's: 236 us for 4 rows of each of
+        // 32 sequences over 8,192 positions in pages of 64, this way 206)
         int g = 0, slot = 0;  // blocks so far, and the next one's slot
         for (int it = 0; ok; ++it) {
           const int is = it % kItems;
@@ -879,9 +865,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
           for (int i = w.i0; ok && i < w.i1; ++i, ++g) {
             const int kb = chunk_block(sp, i) * kKeys;
             const bool edge = edge_block(kb, first, last, a.window, a.sinks);
-#pragma unroll 1
-            for (int op = 0; ok && op < 2; ++op)
-              ok = (op == 1 || wait_slot(g)) && bring_codes(lt, op, g, slot, kb, last, edge);
+            ok = wait_slot(g) && bring_codes(lt & 63, lt >> 6, g, slot, kb, last, edge);
             if (++slot == NS) slot = 0;
           }
         }
@@ -1302,55 +1286,66 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
         for (int q = row; q < 2 * kRows; q += step) total = fmaf(exp2_fast(s_half[q] - base), s_half[2 * kRows + q], total);
         const float f = exp2_fast(m - base) * (w.part == 0 ? 1.0f : total == 0.0f ? 0.0f : 1.0f / total);
         if (w.part == 0 && live && says) a.part_ml[prow + row] = make_float2(top, total);
-        constexpr int C = L::kOutCols, P = C / 4;  // (two buffers of 256 rows of C floats each)
+        // (two buffers of 256 x C floats: of the tiles' rows, up to 32, 64 or 128, and as many times C columns as they leave room for;
+        // quarters have 32 rows eight times)
+        constexpr int C = L::kOutCols, P = C / 4;
+        const int fit = min(w.lq - w.t0, quarter ? a.few : a.tok) * a.group, lg = quarter || fit > 64 ? 7 : fit > 32 ? 6 : 5;
         auto cell = [&](int b, int q, int p) {
           return reinterpret_cast<float4*>(stage + (b * 2 * kRows + q) * C * 4 + ((p ^ (P == 4 ? (q >> 1) & 3 : (q >> 2) & 1)) << 4));
         };
-        // this thread adds up piece p of row rr of some columns (and, with four pieces, of row rr + 64 where all 128 rows differ)
-        const int id = t * kRows + r, p = id % P, rr = id / P, fit = min(w.lq - w.t0, quarter ? a.few : a.tok) * a.group;
+        // this thread adds up piece p of some columns of some rows
+        const int id = t * kRows + r, p = id % P;
         constexpr int kMine = P / 2;
         uint8_t* to[kMine];
-        int tok_of[kMine];
+        int of[kMine], col_of[kMine], tok_of[kMine];  // the cell of the first summand, the columns' and the row's place
 #pragma unroll
         for (int k = 0; k < kMine; ++k) {
-          const int q0 = rr + 64 * k;
+          const int x = id / P + 64 * k, q0 = x & ((1 << lg) - 1), set = x >> lg;
+          of[k] = q0 < fit ? (set << (lg + 1)) + q0 : -1;
+          col_of[k] = set * C + 4 * p;
           tok_of[k] = q0 / a.group;
           to[k] = w.part == 0 ? reinterpret_cast<uint8_t*>(a.part_o) + ((prow + (q0 & ~31)) * (HD / 4) + (q0 & 31)) * 16
                               : a.out + (int64_t)(w.q0 + w.t0 + tok_of[k]) * a.out_stride +
                                     (int64_t)(w.h * a.group + q0 - tok_of[k] * a.group) * HD * 2;
         }
         auto add_up = [&](int b, int k, int col) {
-          float4 x[8];
+          float4 v = *cell(b, of[k], p), y = *cell(b, of[k] + (1 << lg), p);
+          v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+          if (quarter) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            x[e] = quarter || e == 0 || e == 4 ? *cell(b, rr + 64 * k + 32 * e, p) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v.x += x[e].x, v.y += x[e].y, v.z += x[e].z, v.w += x[e].w;
+            for (int e = 1; e < 4; ++e) {
+              const float4 x0 = *cell(b, of[k] + 32 * e, p), x1 = *cell(b, of[k] + kRows + 32 * e, p);
+              v.x += x0.x + x1.x, v.y += x0.y + x1.y, v.z += x0.z + x1.z, v.w += x0.w + x1.w;
+            }
+          }
           if (hi >= 0) {
-            const float4 y = taken_out<HD, CDT>(a, w, w.len - w.lq + w.t0 + tok_of[k], col, lo, hi);
+            y = taken_out<HD, CDT>(a, w, w.len - w.lq + w.t0 + tok_of[k], col, lo, hi);
             v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
           }
           if (w.part == 0) *reinterpret_cast<float4*>(to[k] + col * 128) = v;  // (a piece's 32 rows are consecutive there)
           else *reinterpret_cast<uint2*>(to[k] + col * 2) = make_uint2(pack2(v.x, v.y, QDT), pack2(v.z, v.w, QDT));
         };
+        int b = 0;
 #pragma unroll 1
-        for (int c0 = 0; c0 < HD; c0 += C) {
-          const int b = (c0 / C) & 1;
+        for (int c0 = 0; c0 < HD; c0 += C << (7 - lg), b ^= 1) {
           if (warp_live) {
-            float o[16];  // (8 of them where C is 8)
-            load_o(c0 & ~15, f, o);
+#pragma unroll 1
+            for (int set = 0; set < 1 << (7 - lg); ++set) {
+              const int c = c0 + set * C;
+              float o[16];  // (8 of them where C is 8)
+              load_o(c & ~15, f, o);
 #pragma unroll
-            for (int e = 0; e < P; ++e) {
-              float4 v = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-              if (C == 8 && (c0 & 8)) v = make_float4(o[4 * e + 8], o[4 * e + 9], o[4 * e + 10], o[4 * e + 11]);
-              *cell(b, id, e) = v;
+              for (int e = 0; e < P; ++e) {
+                float4 v = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                if (C == 8 && (c & 8)) v = make_float4(o[4 * e + 8], o[4 * e + 9], o[4 * e + 10], o[4 * e + 11]);
+                *cell(b, (set << (lg + 1)) + (t << lg) + r, e) = v;
+              }
             }
           }
           if (!(ok = meet())) break;
 #pragma unroll
           for (int k = 0; k < kMine; ++k)
-            if (rr + 64 * k < fit) add_up(b, k, c0 + 4 * p);
+            if (of[k] >= 0) add_up(b, k, c0 + col_of[k]);
         }
         if (w.part == 0) __threadfence();
         if (ok) ok = meet();  // (what comes next takes these maxima, sums and results' place)
