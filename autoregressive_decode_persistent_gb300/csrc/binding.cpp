@@ -197,6 +197,14 @@ struct Workspace {
     p = held.data_ptr();
   }
 };
+// The library's call, without the interpreter's lock: a launch may wait for room in its stream's queue.
+template <class Call>
+void launch(const char* name, Call call) {
+  PyThreadState* const state = PyEval_SaveThread();
+  const int rc = call();
+  PyEval_RestoreThread(state);
+  check(rc, name);
+}
 void* stream_of(int device) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream(); }
 
 // k_pages, v_pages, table, lens, cu_rows, q, k, v, cos, sin, q_gain, k_gain, eps, k_scale, v_scale, out, status
@@ -261,8 +269,11 @@ PyObject* append(PyObject* const* o) {
   rope.eps = (float)number(o[12]);
   int32_t* status = status_of(where, o[16], d);
   const c10::cuda::CUDAGuard guard((c10::DeviceIndex)d);
-  check(lib.append(&kv, &rope, qp, k.data_ptr(), v.data_ptr(), dt, (int32_t)heads, qs, ks, vs, cu, (int32_t)n, op, odt, os, status, stream_of(d)),
-        "adp_paged_kv_append");
+  const void *kp = k.data_ptr(), *vp = v.data_ptr();
+  void* const stream = stream_of(d);
+  launch("adp_paged_kv_append", [&] {
+    return lib.append(&kv, &rope, qp, kp, vp, dt, (int32_t)heads, qs, ks, vs, cu, (int32_t)n, op, odt, os, status, stream);
+  });
   if (!q) Py_RETURN_NONE;
   return o[15] == Py_None ? THPVariable_Wrap(made) : Py_NewRef(o[15]);
 }
@@ -282,19 +293,23 @@ PyObject* attention(PyObject* const* o) {
   Out out(where, o[10], q, d);
   const float scale = scale_of(o[7], hd);
   const c10::cuda::CUDAGuard guard((c10::DeviceIndex)d);
+  const void* const qp = q.data_ptr();
+  void* const stream = stream_of(d);
   if (window) {
     Workspace w(where, o[11], q, d, [&](uint64_t* b) {
       check(lib.window_workspace(&kv, (int32_t)heads, window, sinks, b), "adp_paged_window_attention_workspace");
     });
     int32_t* status = status_of(where, o[12], d);
-    check(lib.window(&kv, q.data_ptr(), dt, (int32_t)heads, qs, scale, window, sinks, out.p, out.stride, w.p, w.bytes, status, stream_of(d)),
-          "adp_paged_window_attention");
+    launch("adp_paged_window_attention", [&] {
+      return lib.window(&kv, qp, dt, (int32_t)heads, qs, scale, window, sinks, out.p, out.stride, w.p, w.bytes, status, stream);
+    });
   } else {
     Workspace w(where, o[11], q, d,
                 [&](uint64_t* b) { check(lib.attention_workspace(&kv, (int32_t)heads, b), "adp_paged_attention_workspace"); });
     int32_t* status = status_of(where, o[12], d);
-    check(lib.attention(&kv, q.data_ptr(), dt, (int32_t)heads, qs, scale, out.p, out.stride, w.p, w.bytes, status, stream_of(d)),
-          "adp_paged_attention");
+    launch("adp_paged_attention", [&] {
+      return lib.attention(&kv, qp, dt, (int32_t)heads, qs, scale, out.p, out.stride, w.p, w.bytes, status, stream);
+    });
   }
   return out.result();
 }
@@ -319,9 +334,11 @@ PyObject* chunk(PyObject* const* o) {
     check(lib.chunk_workspace(&kv, (int32_t)heads, (int32_t)n, window, sinks, b), "adp_paged_chunk_attention_workspace");
   });
   int32_t* status = status_of(where, o[13], d);
-  check(lib.chunk(&kv, q.data_ptr(), dt, (int32_t)heads, qs, cu, (int32_t)n, scale, window, sinks, out.p, out.stride, w.p, w.bytes, status,
-                  stream_of(d)),
-        "adp_paged_chunk_attention");
+  const void* const qp = q.data_ptr();
+  void* const stream = stream_of(d);
+  launch("adp_paged_chunk_attention", [&] {
+    return lib.chunk(&kv, qp, dt, (int32_t)heads, qs, cu, (int32_t)n, scale, window, sinks, out.p, out.stride, w.p, w.bytes, status, stream);
+  });
   return out.result();
 }
 

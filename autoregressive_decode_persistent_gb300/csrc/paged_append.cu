@@ -217,7 +217,8 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
   }
 }
 
-// Warps that share a row: a row's line of heads is cut while there are fewer rows than warps that the GPU holds.
+// Warps that share a row: a row's line of heads is cut while there are fewer rows than warps that the GPU holds (4 rows of 32 + 16
+// heads: 2.7 us in a captured graph, 4.3 uncut; many rows gain nothing by it: 34,360 rows 137 us, 147 in halves, 198 in sixths).
 constexpr int kWarpsPerSm = 24;
 
 }  // namespace

@@ -1222,47 +1222,58 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
       uint8_t* const out = a.out + (int64_t)(w.q0 + tok) * a.out_stride + (int64_t)(w.h * a.group + row_head) * HD * 2;
       const int64_t prow = (int64_t)range * a.rows_cap;  // the first row of this range's partial result
       const bool says = !half || (t == 0 && (!quarter || sub == 0));  // of the warps with these rows, the one that speaks for them
-      if (w.part == 1 && says && warp_live) {
-        // ---- the first part of several: the others' results, of the next ranges in turn, come to its accumulators
-        for (int c = range + 1; ok && c < (int)gridDim.x; ++c) {
-          int32_t state = part_said(a, c);
-          if (state == kPartOpen) {
-            const uint64_t t0 = globaltimer();
-            while (ok && (state = part_said(a, c)) == kPartOpen) ok = *ab == 0 && globaltimer() - t0 <= a.wait_ns;
+      if (w.part == 1 && warp_live) {
+        // ---- the first part of several: the others' results, of the next ranges, come to its accumulators; warps that have the
+        // same rows take turns at them (8 rows over 16,000 positions, 19 parts a KV head: 39 us, 61 with one warp)
+        const int turns = quarter ? 8 : half ? 2 : 1, own_turn = quarter ? t * 4 + sub : half ? t : 0;
+        int n_parts = 0;
+        bool more = true;
+        for (int c0 = range + 1; more && c0 < (int)gridDim.x; c0 += 32) {  // a lane for every range
+          const uint64_t t0 = globaltimer();
+          uint32_t those;
+          while (true) {
+            const int32_t state = c0 + lane < (int)gridDim.x ? part_said(a, c0 + lane) : kPartNone;
+            const uint32_t ends = __ballot_sync(0xFFFFFFFFu, state == kPartEnds), open = __ballot_sync(0xFFFFFFFFu, state == kPartOpen);
+            const uint32_t mine = ends ^ (ends - 1);  // up to the first end, or all of them
+            those = __ballot_sync(0xFFFFFFFFu, state == kPartEnds || state == kPartGoesOn) & mine;
+            more = ends == 0;
+            if (!(open & mine)) break;
+            if (!(ok = __all_sync(0xFFFFFFFFu, *ab == 0 && globaltimer() - t0 <= a.wait_ns))) break;
           }
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          state = __shfl_sync(0xFFFFFFFFu, state, 0);
+          __syncwarp();
           if (!ok) break;
-          if (state == kPartNone) continue;
-          const int64_t base = (int64_t)c * a.rows_cap + (half ? row & ~31 : t * kRows + sub * 32);
-          const float2 ml = live ? a.part_ml[base + lane] : make_float2(-INFINITY, 0.0f);
-          const float4* from = reinterpret_cast<const float4*>(a.part_o) + base * (HD / 4) + lane;
-          const float mn = fmaxf(m, ml.x), to = mn == -INFINITY ? 0.0f : mn;
-          const float f = exp2_fast(m - to), g = exp2_fast(ml.x - to);
+          for (; those; those &= those - 1) {
+            if (n_parts++ % turns != own_turn) continue;
+            const int c = c0 + __ffs(those) - 1;
+            const int64_t base = (int64_t)c * a.rows_cap + (half ? row & ~31 : t * kRows + sub * 32);
+            const float2 ml = live ? a.part_ml[base + lane] : make_float2(-INFINITY, 0.0f);
+            const float4* from = reinterpret_cast<const float4*>(a.part_o) + base * (HD / 4) + lane;
+            const float mn = fmaxf(m, ml.x), to = mn == -INFINITY ? 0.0f : mn;
+            const float f = exp2_fast(m - to), g = exp2_fast(ml.x - to);
 #pragma unroll 1
-          for (int c0 = 0; c0 < HD; c0 += 64) {
-            float4 x[16];
+            for (int c0 = 0; c0 < HD; c0 += 64) {
+              float4 x[16];
 #pragma unroll
-            for (int p = 0; p < 16; ++p) x[p] = live ? from[(c0 / 4 + p) * 32] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              for (int p = 0; p < 16; ++p) x[p] = live ? from[(c0 / 4 + p) * 32] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              float o[16];
-              load_o(c0 + 16 * h, f, o);
-              uint32_t u[16];
+              for (int h = 0; h < 4; ++h) {
+                float o[16];
+                load_o(c0 + 16 * h, f, o);
+                uint32_t u[16];
 #pragma unroll
-              for (int p = 0; p < 4; ++p) {
-                const float4 y = x[4 * h + p];
-                u[4 * p] = __float_as_uint(fmaf(y.x, g, o[4 * p])), u[4 * p + 1] = __float_as_uint(fmaf(y.y, g, o[4 * p + 1]));
-                u[4 * p + 2] = __float_as_uint(fmaf(y.z, g, o[4 * p + 2])), u[4 * p + 3] = __float_as_uint(fmaf(y.w, g, o[4 * p + 3]));
+                for (int p = 0; p < 4; ++p) {
+                  const float4 y = x[4 * h + p];
+                  u[4 * p] = __float_as_uint(fmaf(y.x, g, o[4 * p])), u[4 * p + 1] = __float_as_uint(fmaf(y.y, g, o[4 * p + 1]));
+                  u[4 * p + 2] = __float_as_uint(fmaf(y.z, g, o[4 * p + 2])), u[4 * p + 3] = __float_as_uint(fmaf(y.w, g, o[4 * p + 3]));
+                }
+                tmem_st16(tO + c0 + 16 * h, u);
               }
-              tmem_st16(tO + c0 + 16 * h, u);
             }
+            tmem_st_wait();
+            m = mn;
+            l = fmaf(l, f, g * ml.y);
+            own_f = 1.0f;  // (O is relative to m now)
           }
-          tmem_st_wait();
-          m = mn;
-          l = fmaf(l, f, g * ml.y);
-          own_f = 1.0f;  // (O is relative to m now)
-          if (state == kPartEnds) break;
         }
         if (!ok) break;
       }

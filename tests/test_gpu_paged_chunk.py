@@ -232,6 +232,46 @@ def test_strided_queries_outputs_and_interleaved_pages(ops):
     assert (out[:, :2] == 5).all() and (out[:, 10:] == 5).all()
 
 
+@pytest.mark.parametrize("q_dtype,hd", [(F16, 64), (BF16, 128)])
+@pytest.mark.parametrize("page", [1, 4, 16, 64])
+def test_codes_and_scales_side_by_side_at_odd_addresses(ops, page, q_dtype, hd):
+    """K's and V's codes of a page one after the other; their scales an odd number of floats apart, from an odd one on."""
+    x = Chunk([50, 3, 0, 7], [130, 33, 5, 0], (8, 2), hd, page, E4M3, q_dtype, seed=9)
+    c = x.c
+    n = c.k.shape[0]
+    codes = torch.full((n, 2, 2, page, hd), NAN, device="cuda").to(E4M3)
+    raw(codes)[:, 0], raw(codes)[:, 1] = raw(c.k), raw(c.v)
+    step = 4 * page + 3
+    floats = torch.full((n * step + 1,), NAN, device="cuda")
+    k_scale, v_scale = (floats.as_strided((n, 2, page), (step, page, 1), at) for at in (1, 1 + 2 * page))
+    k_scale.copy_(c.scales["k_scale"])
+    v_scale.copy_(c.scales["v_scale"])
+    got = ops.paged_chunk_attention(x.q, codes[:, 0], codes[:, 1], c.table, c.len_t, x.cu, k_scale=k_scale, v_scale=v_scale)
+    x.check(got)
+    assert torch.equal(got, x.call(ops))
+
+
+def test_two_threads(ops):
+    """Calls of two threads of the host, each on its own stream."""
+    import threading
+    cases = [Chunk([7, 90], [700, 20], (8, 2), 64, 16, F16, seed=s) for s in (31, 32)]
+    want, got = [x.call(ops) for x in cases], [None, None]
+    torch.cuda.synchronize()
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            results = [cases[i].call(ops) for _ in range(30)]
+            torch.cuda.current_stream().synchronize()
+        got[i] = all(torch.equal(r, want[i]) for r in results)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert got == [True, True]
+
+
 @pytest.mark.parametrize("page", [4, 8, 16])
 @pytest.mark.parametrize("dtype", [F16, E4M3])
 def test_bad_pages_lengths_and_offsets_are_reported(ops, page, dtype):

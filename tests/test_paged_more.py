@@ -75,6 +75,17 @@ def test_tensors_off_the_gpu_are_refused():
         ops.paged_kv_append(pages, pages, table, lens, cu, rows, rows, rows, angles, angles)
 
 
+@pytest.mark.parametrize("which", range(6))
+def test_what_is_no_tensor_is_refused(which):
+    import torch
+    from autoregressive_decode_persistent_gb300 import adp, ops
+    for bad in (None, 3, [1.0]):
+        args = [torch.zeros(1)] * 6
+        args[which] = bad
+        with pytest.raises((adp.AdpError, TypeError, AttributeError)):
+            ops.paged_chunk_attention(*args)
+
+
 # ---------------------------------------------------------------- chunks of rows over the pages
 
 CHUNK = dict(q=FAKE, q_dtype=0, n_heads=20, q_stride=2560, cu_rows=FAKE, n_rows=50, scale=0.1, window=0, sinks=0, out=FAKE, out_stride=2560,
