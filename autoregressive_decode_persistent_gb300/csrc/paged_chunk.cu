@@ -30,7 +30,6 @@ struct ChunkArgs {
   uint8_t* out;
   int64_t out_stride;            // bytes
   int32_t n_rows, group, tok;    // query heads per KV head; tokens of a tile
-  int32_t few;                   // tokens of a quarter of a tile (0: a token does not fit, or there are no quarters)
   int32_t window, sinks;
   float scale_log2;              // of |scale|, and above 0
   int32_t even_scales;           // e4m3: four positions' scales are 16 aligned bytes wherever their pages lie
@@ -68,8 +67,6 @@ struct Item {
   __device__ __forceinline__ int last(int span) const { return len - lq + min(t0 + span, lq) - 1; }
   // its rows fit one tile: the tiles take turns at the blocks
   __device__ __forceinline__ bool half(int tok) const { return lq - t0 <= tok; }
-  // its rows fit a quarter of a tile: each warp of a tile has them all, and takes a quarter of a block's positions
-  __device__ __forceinline__ bool quarter(int few) const { return lq - t0 <= few; }
 };
 // Blocks that tile t of the item works on, and the way from one to the next.
 struct Own {
@@ -273,7 +270,7 @@ __device__ __forceinline__ float4 taken_out(const ChunkArgs& a, const Item& w, i
   float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int i = w.i0; i < w.i1; ++i) {
     const int kb = chunk_block(sp, i) * kKeys;
-    if (kb < lo || kb > hi || !(w.quarter(a.few) || edge_block(kb, first, last, a.window, a.sinks))) continue;
+    if (kb < lo || kb > hi || !edge_block(kb, first, last, a.window, a.sinks)) continue;
     for (int key = kb; key < kb + kKeys && key <= pos; ++key) {
       if (key < from && key >= a.sinks) continue;
       const int page = paged_page(a.c.table + (int64_t)w.b * a.c.table_width, a.c.table_width, a.c.n_pages, a.c.log2_page, key);
@@ -298,14 +295,14 @@ __device__ __forceinline__ float4 taken_out(const ChunkArgs& a, const Item& w, i
 //
 // Rows of a tile are tokens x query heads of one KV head (128 rows: K and V are read once for the heads that share them).  An
 // item of work is two tiles and the blocks that they see; S and O lie in TMEM, Q and a ring of K and V in shared memory, and a
-// thread of the softmax warps has a row.  Few rows still need both tiles' softmax warps: rows that fit one tile have the tiles
-// take turns at the blocks, and rows that fit a warp have each warp of a tile take a quarter of a block's positions (its
-// weights for the others are zeros); maxima, sums and results are added up at the end.  The line of all items (KV heads, in them
+// thread of the softmax warps has a row.  Where the rows fit one tile, the tiles take turns at the blocks, and maxima, sums and results are
+// added up at the end (quarters of a block's positions for each warp of a tile, where the rows fit a warp, were slower: 16 rows
+// over 77 positions 12.3 us for 10.3, 32 sequences of up to 8 rows over 16 bits 111 for 105).  The line of all items (KV heads, in them
 // sequences, pairs of tiles, blocks) is cut evenly over the SMs, whatever the lengths: the CTA that starts an item joins what
 // the next ones have of it.
 //
 // Measured: long chunks are bound by the MMAs and the softmax warps, which both fill most of a block's time (2,048 rows of 32/8
-// heads x 128 over 8,192 bf16 positions: 240 GFLOP in 180 us, 70% of the GEMM rate, the tensor pipe busy 57% of it; some
+// heads x 128 over 8,192 bf16 positions: 241 GFLOP in 180 us, 70% of the GEMM rate, the tensor pipe busy 57% of it; some
 // 1,280 cycles of a pair's block, 1,024 by the pipe's rate: S's 64 columns read Q again for every block).  Few rows over 16 bits are
 // bound by memory (32 sequences of 4 rows, 8,192 positions each: 1.07 GB in 178 us, 89% of the copy rate), over e4m3
 // by the conversion to fp16 and three slots of fp16 blocks beside the codes (the same in e4m3: 206 us, 40%).
@@ -315,7 +312,7 @@ __device__ __forceinline__ float4 taken_out(const ChunkArgs& a, const Item& w, i
 template <int HD, int CDT, int QDT, bool LOAD>
 __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                       const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mf, const ChunkArgs a) {
+                       const __grid_constant__ CUtensorMap mv, const ChunkArgs a) {
   using L = ChunkSmem<HD, CDT>;
   constexpr int NS = L::kSlots;
   constexpr bool Q8 = CDT == DT_E4M3;
@@ -594,15 +591,11 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
           if (i1 > p.j) {
             if (nq > 0 && !(ok = wait(qempty, (nq - 1) & 1))) break;
             if (lane == 0) {
-              // (a quarter of a tile four times, or the item's tiles)
-              const bool quarter = !Q8 && w.quarter(a.few);
-              const int boxes = quarter ? 4 : w.half(a.tok) ? 1 : 2, tok = quarter ? a.few : a.tok;
-              const uint32_t step = quarter ? 32 * 128 : L::kQTile;
-              mbar_arrive_expect_tx(qfull, (uint32_t)(boxes * tok * a.group) * 128 * (HD / 64));
+              const int boxes = w.half(a.tok) ? 1 : 2;
+              mbar_arrive_expect_tx(qfull, (uint32_t)(boxes * a.tok * a.group) * 128 * (HD / 64));
               for (int t = 0; t < boxes; ++t)
                 for (int c = 0; c < HD / 64; ++c)
-                  tma_load_3d(Qs + t * step + c * L::kQBlock, quarter ? &mf : &mq, c * 64, w.h * a.group,
-                              w.q0 + w.t0 + (quarter ? 0 : t * a.tok), qfull);
+                  tma_load_3d(Qs + t * L::kQTile + c * L::kQBlock, &mq, c * 64, w.h * a.group, w.q0 + w.t0 + t * a.tok, qfull);
             }
             ++nq;
             __syncwarp();
@@ -994,10 +987,10 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
       const int first = w.first(), last = w.last(span), n = w.i1 - w.i0;
       const ChunkSpan sp = chunk_span(first, last, a.window, a.sinks);
       const Own own = own_blocks(w, sp, t, a.tok);
-      const bool half = w.half(a.tok), quarter = !Q8 && w.quarter(a.few);
-      const int row = quarter ? lane : r, row_tok = row / a.group, row_head = row - row_tok * a.group;
+      const bool half = w.half(a.tok);
+      const int row_tok = r / a.group, row_head = r - row_tok * a.group;
       const int tok = w.t0 + (half ? 0 : t * a.tok) + row_tok;
-      const bool live = row_tok < (quarter ? a.few : a.tok) && tok < w.lq;
+      const bool live = row_tok < a.tok && tok < w.lq;
       const bool warp_live = __any_sync(0xFFFFFFFFu, live);
       const int pos = w.len - w.lq + tok;  // this row's position: it sees keys up to it
       const int from = max(max(pos, 0) - a.window + 1, 0);  // from its window's first on, and the first ones
@@ -1023,7 +1016,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
             }
             const uint32_t e2 = min(max(__float_as_uint(top) >> 23, 1u), 253u);
             const float inv = __uint_as_float((254u - e2) << 23);
-            if (row_tok < (quarter ? a.few : a.tok)) {
+            if (row_tok < a.tok) {
 #pragma unroll 4
               for (int c = 0; c < HD / 8; ++c) {
                 const uint4 v = *at(c);
@@ -1052,34 +1045,26 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
       // e4m3: what weighs V's codes are the products weight x value scale, which have a running maximum of their own, mo
       // (base-2 exponents: score + log2 of the scale); O is relative to it, and vc = 2^((m - mo) / 2), twice, brings them there
       float mo = -INFINITY, vc = 1.0f;
-      // The softmax of N columns from col on of own block k, whose scores lie in buffer buf: P takes their place, 16 bits each.
-      auto block = [&](auto columns, int col, int k, uint32_t buf, int slot, int kb) {
-        constexpr int N = decltype(columns)::value;
+      // The softmax of own block k, whose scores lie in buffer buf: P takes their place, 16 bits each.
+      auto block = [&](int k, uint32_t buf, int slot, int kb) {
+        constexpr int N = kKeys;
         float x[N];
-        if constexpr (N == kKeys) {
-          tmem_ld64(tS + buf * 64, x);
-        } else {
-          uint32_t u[N];
-          tmem_ld16(tS + buf * 64 + col, u);
-#pragma unroll
-          for (int c = 0; c < N; ++c) x[c] = __uint_as_float(u[c]);
-        }
+        tmem_ld64(tS + buf * 64, x);
         [[maybe_unused]] const SlotScales& z = s_scale[Q8 ? slot : 0];
         if constexpr (Q8) {
 #pragma unroll
           for (int c = 0; c < N; c += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(&z.k[col + c]);
+            const float4 f = *reinterpret_cast<const float4*>(&z.k[c]);
             const float2 u = __fmul2_rn(make_float2(x[c], x[c + 1]), make_float2(f.x, f.y));
             const float2 v = __fmul2_rn(make_float2(x[c + 2], x[c + 3]), make_float2(f.z, f.w));
             x[c] = u.x, x[c + 1] = u.y, x[c + 2] = v.x, x[c + 3] = v.y;
           }
         }
-        const int kc = kb + col;
-        const bool hidden = kc + N - 1 > warp_first || (kc <= warp_last - a.window && kc + N - 1 >= a.sinks);
+        const bool hidden = kb + N - 1 > warp_first || (kb <= warp_last - a.window && kb + N - 1 >= a.sinks);
         if (hidden || *holes) {
           // columns up to this row's position, from its window's first on or of the first ones, but those without a place
-          uint64_t see = below(pos - kc + 1) & (~below(from - kc) | below(a.sinks - kc));
-          if (*holes) see &= ~(*reinterpret_cast<volatile uint64_t*>(&hole[slot]) >> col);
+          uint64_t see = below(pos - kb + 1) & (~below(from - kb) | below(a.sinks - kb));
+          if (*holes) see &= ~*reinterpret_cast<volatile uint64_t*>(&hole[slot]);
           const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
 #pragma unroll
           for (int c = 0; c < N; ++c) x[c] = ((c < 32 ? lo : hi) >> (c & 31)) & 1 ? x[c] : -INFINITY;
@@ -1106,7 +1091,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
             float mw = -INFINITY;
 #pragma unroll
             for (int c = 0; c < N; c += 4) {
-              const float4 lv = *reinterpret_cast<const float4*>(&z.lv[col + c]);
+              const float4 lv = *reinterpret_cast<const float4*>(&z.lv[c]);
               mw = fmaxf(fmaxf(mw, fmaf(x[c], scale, lv.x)), fmaf(x[c + 1], scale, lv.y));
               mw = fmaxf(fmaxf(mw, fmaf(x[c + 2], scale, lv.z)), fmaf(x[c + 3], scale, lv.w));
             }
@@ -1132,14 +1117,13 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
         const float2 sc = make_float2(scale, scale), nm = make_float2(-ms, -ms);
         [[maybe_unused]] const float2 vc2 = make_float2(vc, vc);
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-        constexpr int NS2 = N < 32 ? N : 32;
 #pragma unroll
-        for (int c0 = 0; c0 < N; c0 += NS2) {
-          uint32_t u[NS2 / 2];
+        for (int c0 = 0; c0 < N; c0 += 32) {
+          uint32_t u[16];
 #pragma unroll
-          for (int e = 0; e < NS2; e += 4) {
+          for (int e = 0; e < 32; e += 4) {
             [[maybe_unused]] float4 f;
-            if constexpr (Q8) f = *reinterpret_cast<const float4*>(&z.v[col + c0 + e]);
+            if constexpr (Q8) f = *reinterpret_cast<const float4*>(&z.v[c0 + e]);
 #pragma unroll
             for (int d = 0; d < 4; d += 2) {
               const float2 y = __ffma2_rn(make_float2(x[c0 + e + d], x[c0 + e + d + 1]), sc, nm);
@@ -1150,15 +1134,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
               u[(e + d) >> 1] = pack2(p.x, p.y, BF ? DT_BF16 : DT_F16);
             }
           }
-          if constexpr (N == kKeys) {
-            tmem_st16(tS + buf * 64 + c0 / 2, u);
-          } else {  // the other warps have the other positions: weights of zero here
-            const uint32_t none[8] = {};
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (q != sub) tmem_st8(tS + buf * 64 + q * 8, none);
-            tmem_st8(tS + buf * 64 + sub * 8, u);
-          }
+          tmem_st16(tS + buf * 64 + c0 / 2, u);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -1174,9 +1150,8 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
         if constexpr (Q8) {  // (the scales of V come with V)
           if (!(ok = wait(&vfull[slot], ((g + i) / NS) & 1))) break;
         }
-        // ---- an edge block's values in 16 bits, looked through by the tiles that weigh them (they take out the same; and
-        // every block's where some warps' weights are zero)
-        if (!Q8 && (quarter || edge_block(kb, first, last, a.window, a.sinks))) {
+        // ---- an edge block's values in 16 bits, looked through by the tiles that weigh them (they take out the same)
+        if (!Q8 && edge_block(kb, first, last, a.window, a.sinks)) {
           uint8_t* vt = ring + slot * L::kPair + L::kTile;
           const int key = r >> 1;  // two threads to a key
           auto piece = [&](int c) {
@@ -1211,9 +1186,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
           __syncwarp();
         }
         if (warp_live) {
-          if constexpr (Q8) ok = block(std::integral_constant<int, kKeys>(), 0, k, buf, slot, kb);
-          else ok = quarter ? block(std::integral_constant<int, kKeys / 4>(), sub * (kKeys / 4), k, buf, slot, kb)
-                            : block(std::integral_constant<int, kKeys>(), 0, k, buf, slot, kb);
+          ok = block(k, buf, slot, kb);
           if (!ok) break;
         }
         __syncwarp();
@@ -1239,11 +1212,11 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
       };
       uint8_t* const out = a.out + (int64_t)(w.q0 + tok) * a.out_stride + (int64_t)(w.h * a.group + row_head) * HD * 2;
       const int64_t prow = (int64_t)range * a.rows_cap;  // the first row of this range's partial result
-      const bool says = !half || (t == 0 && (!quarter || sub == 0));  // of the warps with these rows, the one that speaks for them
+      const bool says = !half || t == 0;  // of the warps with these rows, the one that speaks for them
       if (w.part == 1 && warp_live) {
         // ---- the first part of several: the others' results, of the next ranges, come to its accumulators; warps that have the
-        // same rows take turns at them (8 rows over 16,000 positions, 19 parts a KV head: 39 us, 61 with one warp)
-        const int turns = quarter ? 8 : half ? 2 : 1, own_turn = quarter ? t * 4 + sub : half ? t : 0;
+        // same rows take turns at them (8 rows over 16,000 positions, 19 parts a KV head: 43 us, 61 with one warp)
+        const int turns = half ? 2 : 1, own_turn = half ? t : 0;
         int n_parts = 0;
         bool more = true;
         for (int c0 = range + 1; more && c0 < (int)gridDim.x; c0 += 32) {  // a lane for every range
@@ -1263,7 +1236,7 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
           for (; those; those &= those - 1) {
             if (n_parts++ % turns != own_turn) continue;
             const int c = c0 + __ffs(those) - 1;
-            const int64_t base = (int64_t)c * a.rows_cap + (half ? row & ~31 : t * kRows + sub * 32);
+            const int64_t base = (int64_t)c * a.rows_cap + (half ? 0 : t * kRows) + sub * 32;
             const float2 ml = live ? a.part_ml[base + lane] : make_float2(-INFINITY, 0.0f);
             const float4* from = reinterpret_cast<const float4*>(a.part_o) + base * (HD / 4) + lane;
             const float mn = fmaxf(m, ml.x), to = mn == -INFINITY ? 0.0f : mn;
@@ -1309,16 +1282,14 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
         if (!(ok = meet())) break;
         look();
         float top = -INFINITY, total = 0.0f;
-        const int step = quarter ? 32 : kRows;
-        for (int q = row; q < 2 * kRows; q += step) top = fmaxf(top, s_half[q]);
+        for (int q = r; q < 2 * kRows; q += kRows) top = fmaxf(top, s_half[q]);
         const float base = top == -INFINITY ? 0.0f : top;
-        for (int q = row; q < 2 * kRows; q += step) total = fmaf(exp2_fast(s_half[q] - base), s_half[2 * kRows + q], total);
+        for (int q = r; q < 2 * kRows; q += kRows) total = fmaf(exp2_fast(s_half[q] - base), s_half[2 * kRows + q], total);
         const float f = exp2_fast(m - base) * (w.part == 0 ? 1.0f : total == 0.0f ? 0.0f : 1.0f / total);
-        if (w.part == 0 && live && says) a.part_ml[prow + row] = make_float2(top, total);
-        // (two buffers of 256 x C floats: of the tiles' rows, up to 32, 64 or 128, and as many times C columns as they leave room for;
-        // quarters have 32 rows eight times)
+        if (w.part == 0 && live && says) a.part_ml[prow + r] = make_float2(top, total);
+        // (two buffers of 256 x C floats: of the tiles' rows, up to 32, 64 or 128, and as many times C columns as they leave room for)
         constexpr int C = L::kOutCols, P = C / 4;
-        const int fit = min(w.lq - w.t0, quarter ? a.few : a.tok) * a.group, lg = quarter || fit > 64 ? 7 : fit > 32 ? 6 : 5;
+        const int fit = min(w.lq - w.t0, a.tok) * a.group, lg = fit > 64 ? 7 : fit > 32 ? 6 : 5;
         auto cell = [&](int b, int q, int p) {
           return reinterpret_cast<float4*>(stage + (b * 2 * kRows + q) * C * 4 + ((p ^ (P == 4 ? (q >> 1) & 3 : (q >> 2) & 1)) << 4));
         };
@@ -1340,13 +1311,6 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
         auto add_up = [&](int b, int k, int col) {
           float4 v = *cell(b, of[k], p), y = *cell(b, of[k] + (1 << lg), p);
           v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
-          if (quarter) {
-#pragma unroll
-            for (int e = 1; e < 4; ++e) {
-              const float4 x0 = *cell(b, of[k] + 32 * e, p), x1 = *cell(b, of[k] + kRows + 32 * e, p);
-              v.x += x0.x + x1.x, v.y += x0.y + x1.y, v.z += x0.z + x1.z, v.w += x0.w + x1.w;
-            }
-          }
           if (hi >= 0) {
             y = taken_out<HD, CDT>(a, w, w.len - w.lq + w.t0 + tok_of[k], col, lo, hi);
             v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
@@ -1473,7 +1437,9 @@ bool encode_pages(CUtensorMap* map, const void* base, bool bf16, const adp_paged
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kMinCopyPage = 8;  // positions of a page that a tensor copy takes: whole swizzle atoms
+// Positions of a page that tensor copies take (32 sequences of up to 8 rows over pages of 8 bf16 positions: 180 us with tensor copies of 8
+// rows each, 119 by warps).
+constexpr int kMinCopyPage = 16;
 
 // How a call falls on the GPU: CTAs, rows of a partial result (0: no piece of work can be cut), bytes of the workspace.
 struct ChunkPlan {
@@ -1501,13 +1467,13 @@ template <int HD, int CDT, int QDT, bool LOAD>
 struct ChunkKey {};
 
 template <int HD, int CDT, int QDT, bool LOAD>
-cudaError_t chunk_launch(const CUtensorMap (&m)[4], const ChunkArgs& a, const ChunkPlan& p, cudaStream_t st) {
+cudaError_t chunk_launch(const CUtensorMap (&m)[3], const ChunkArgs& a, const ChunkPlan& p, cudaStream_t st) {
   auto* kernel = paged_chunk_kernel<HD, CDT, QDT, LOAD>;
   constexpr size_t smem = ChunkSmem<HD, CDT>::kBytes;
   cudaError_t e = allow_smem<ChunkKey<HD, CDT, QDT, LOAD>>((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
   if (a.part_state && (e = cudaMemsetAsync(a.part_state, 0, (size_t)p.ctas * sizeof(int32_t), st)) != cudaSuccess) return e;
-  kernel<<<p.ctas, LOAD ? 512 : 384, smem, st>>>(m[0], m[1], m[2], m[3], a);
+  kernel<<<p.ctas, LOAD ? 512 : 384, smem, st>>>(m[0], m[1], m[2], a);
   return cudaGetLastError();
 }
 
@@ -1563,9 +1529,6 @@ extern "C" int adp_paged_chunk_attention(const adp_paged_kv* kv, const void* q, 
   a.n_rows = n_rows;
   a.group = group;
   a.tok = kRows / group;
-  // Rows that fit a warp have quarters of tiles, but for e4m3, whose loops are bound by their instructions (32 sequences of up to 8
-  // tokens: 146 us without, 157 with them; over 16 bits 115 with and 130 without).
-  a.few = kv->dtype == ADP_E4M3 ? 0 : 32 / group;
   // (a scale of 0 becomes the least normal number: the scores' differences vanish all the same, and what is not seen stays at
   // -infinity)
   a.scale_log2 = fmaxf(log2_scale(fabsf(scale)), kScaleMin);
@@ -1581,9 +1544,8 @@ extern "C" int adp_paged_chunk_attention(const adp_paged_kv* kv, const void* q, 
   a.status = dev_status;
   const int64_t keys = (int64_t)kv->table_width * kv->page_size;
   a.wait_ns = packed_wait_ns((int32_t)keys, kv->n_seqs);
-  CUtensorMap m[4] = {};
+  CUtensorMap m[3] = {};
   if (!encode(&m[0], q, bf16, kv->head_dim, n_heads, n_rows, q_stride, group, a.tok)) return ADP_ERR_INVALID_ARG;
-  if (a.few && !encode(&m[3], q, bf16, kv->head_dim, n_heads, n_rows, q_stride, group, a.few)) return ADP_ERR_INVALID_ARG;
   if (!load && (!encode_pages(&m[1], kv->k, bf16, kv) || !encode_pages(&m[2], kv->v, bf16, kv))) return ADP_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   cudaError_t e = cudaErrorInvalidValue;

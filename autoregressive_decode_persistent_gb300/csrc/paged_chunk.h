@@ -8,9 +8,9 @@
 namespace adp {
 
 constexpr int kChunkKeys = 64;       // positions of a block
-// Blocks that a part of a piece has at least (8: 32 sequences of up to 8 tokens 130 us instead of 126, prompts and single tokens
-// together 76 instead of 74), and that are worth a CTA of their own (8 rows over 2,000 and over 16,000 positions: 26.5 and 39.0 us; 12:
-// 28.7 and 39.1; 24: 34.8 and 42.8).
+// Blocks that a part of a piece has at least (8: 32 sequences of up to 8 tokens 131 us instead of 127, prompts and single tokens
+// together 76 instead of 74), and that are worth a CTA of their own (8 rows over 2,000 and over 16,000 positions: 22.6 and 42.7 us; 16:
+// 24.7 and 39.5; 24: 27.7 and 39.7; over e4m3 28.7 and 48.5; 33 and 47; 39 and 48).
 constexpr int kChunkMinPart = 4;
 constexpr int kChunkMinWork = 8;
 constexpr int kNoWindow = 0x7FFFFFFF;
@@ -38,8 +38,8 @@ ADP_INLINE ChunkSpan chunk_span(int32_t first, int32_t last, int32_t window, int
 ADP_INLINE int32_t chunk_block(const ChunkSpan& s, int32_t i) { return i < s.head ? i : i + s.gap; }
 
 // What starting and ending a piece of work costs, in blocks of it: where its rows fit one tile, whose blocks cost half as much, and
-// warps share rows that have to be joined, twice as many (32 sequences of up to 8 tokens: 166 us instead of 174, prompts and single
-// tokens together 74 instead of 78 with 8 for both).
+// whose results the tiles add up, twice as many (4 for both: 32 sequences of up to 8 tokens 130.5 us instead of 127; 8 for both: prompts and
+// single tokens together 77.4 instead of 74).
 ADP_INLINE int32_t chunk_over(int32_t tokens, int32_t tile) { return tokens <= tile ? 8 : 4; }
 
 // Where a cut that falls j units behind a piece's blocks' start (negative: in front) goes: whole blocks, and no part of less than
