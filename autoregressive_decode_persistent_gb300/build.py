@@ -1,13 +1,17 @@
 """Build libadp.so (the engine's C ABI) in-tree with nvcc for sm_103a.
 
 Thirteen translation units compiled in parallel, then linked as a shared library with the
-static CUDA runtime (and binding.cpp, which PyTorch's headers and libraries make an extension module of its own). -fmad=false keeps every multiply-add that the arithmetic contract does
+static CUDA runtime. -fmad=false keeps every multiply-add that the arithmetic contract does
 not fuse explicitly as a separate multiply and add; no fast-math flags.
 
 A second library, libadp_test.so, links the same objects with the host engine compiled once more
 under -DADP_TEST_HOOKS: it also exports the test-only hooks (withholding a phase's outputs,
 shortening the in-kernel waits, moving the epoch counter).  The tests load it; the release
 library, which the benchmark and applications load, does not carry those hooks.
+
+Beside them binding.cpp becomes an extension module for the installed PyTorch and Python, whose headers the libraries do not
+need: where it cannot be built, build() warns and the libraries are there all the same; calls of ops.py that need it say
+that it is missing.
 """
 from __future__ import annotations
 
@@ -15,6 +19,8 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -43,26 +49,34 @@ def _extra_flags() -> list[str]:
 
 
 FLAGS_STAMP = os.path.join(HERE, "_build", "flags.txt")
+BINDING_SOURCE = "binding.cpp"
+
+
+def _older(products: list[str], sources: list[str]) -> bool:
+    """Whether a product is missing, or older than a source."""
+    if not all(os.path.exists(p) for p in products):
+        return True
+    t = min(os.path.getmtime(p) for p in products)
+    deps = [os.path.join(CSRC, f) for f in sources]
+    deps.append(os.path.join(os.path.dirname(HERE), "include", "adp.h"))
+    return any(os.path.getmtime(d) > t for d in deps)
 
 
 def _stale() -> bool:
-    if not all(os.path.exists(p) for p in (LIB, TEST_LIB, BINDING)):
-        return True
     try:
         if open(FLAGS_STAMP).read() != " ".join(_extra_flags()):
             return True
     except OSError:
         return True
-    t = min(os.path.getmtime(p) for p in (LIB, TEST_LIB, BINDING))
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps.append(os.path.join(os.path.dirname(HERE), "include", "adp.h"))
-    return any(os.path.getmtime(d) > t for d in deps)
+    return _older([LIB, TEST_LIB], [f for f in os.listdir(CSRC) if f != BINDING_SOURCE])
+
+
+def _stale_binding() -> bool:
+    return _older([BINDING], [BINDING_SOURCE])
 
 
 def _build_binding():
-    """_binding.so: the tensor checks of ops.py's calls, against the installed PyTorch's headers."""
-    import sysconfig
-
+    """The extension module with the tensor checks of ops.py's calls, against the installed PyTorch's headers."""
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
@@ -70,7 +84,7 @@ def _build_binding():
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-isystem{i}" for i in include),
-           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           os.path.join(CSRC, BINDING_SOURCE), "-o", tmp, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
            "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -79,8 +93,21 @@ def _build_binding():
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
-        return LIB
+    """Builds what is out of date; the path of libadp.so."""
+    with cf.ThreadPoolExecutor(1) as ex:
+        binding = ex.submit(_build_binding) if force or _stale_binding() else None
+        if force or _stale():
+            _build_libraries(verbose)
+        error = binding.exception() if binding else None
+    if error:
+        if os.path.exists(BINDING):
+            os.remove(BINDING)  # made of other sources
+        warnings.warn(f"{os.path.basename(BINDING)} could not be built ({type(error).__name__}: {error}): the calls of ops.py that need it "
+                      "will fail", RuntimeWarning, stacklevel=2)
+    return LIB
+
+
+def _build_libraries(verbose: bool):
     cc = nvcc()
     outdir = os.path.join(HERE, "_build")
     os.makedirs(outdir, exist_ok=True)
@@ -98,10 +125,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     jobs = [(src, [], src.replace(".cu", ".o")) for src in SOURCES]
     jobs.append(("engine.cu", ["-DADP_TEST_HOOKS"], "engine_hooks.o"))
-    with cf.ThreadPoolExecutor(len(jobs) + 1) as ex:
-        binding = ex.submit(_build_binding)
+    with cf.ThreadPoolExecutor(len(jobs)) as ex:
         objs = list(ex.map(compile_one, jobs))
-        binding.result()
     release = objs[:len(SOURCES)]
     test = [o if not o.endswith(os.sep + "engine.o") else objs[-1] for o in release]
     for lib, members in ((LIB, release), (TEST_LIB, test)):
@@ -113,7 +138,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
         os.replace(tmp, lib)
     with open(FLAGS_STAMP, "w") as fh:
         fh.write(" ".join(_extra_flags()))
-    return LIB
 
 
 if __name__ == "__main__":

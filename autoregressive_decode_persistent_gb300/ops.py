@@ -1,7 +1,8 @@
 """The paged KV cache operators and packed prompt attention on PyTorch tensors (include/adp.h has their semantics).
 
-Argument checks and marshalling only (those of the calls that serve single tokens and chunks in csrc/binding.cpp): every
-computation runs in libadp.so's kernels, on the current stream of the tensors' device, without synchronising.  Nothing is
+Argument checks and marshalling only (those of the calls that serve single tokens and chunks in csrc/binding.cpp, an
+extension module that paged_kv_append and paged_chunk_attention need and paged_attention is faster with): every computation
+runs in libadp.so's kernels, on the current stream of the tensors' device, without synchronising.  Nothing is
 differentiable.  Wrong arguments raise adp.AdpError before anything is launched; wrong lengths or page numbers, which only
 the GPU sees, set the optional `status` tensor (int32, one element).
 """
@@ -62,19 +63,25 @@ def _call(device: int, name: str, *args):
             adp._check(getattr(adp.load_library(), name)(*args, torch._C._cuda_getCurrentRawStream(device)), name)
 
 
-_binding = None
+_binding = _missing = None  # the extension module once it is loaded, or why it cannot be
 
 
-def _native():
+def _native(needed: bool = True):
     """The extension module with the checks of the calls below, given the addresses of the library's functions."""
-    global _binding
-    if _binding is None:
+    global _binding, _missing
+    if _binding is None and _missing is None:
         lib = adp.load_library()
-        from . import _binding as module  # (no fallback: build it with build.build())
-        names = ("adp_paged_kv_append", "adp_paged_attention", "adp_paged_attention_workspace", "adp_paged_window_attention",
-                 "adp_paged_window_attention_workspace", "adp_paged_chunk_attention", "adp_paged_chunk_attention_workspace")
-        module.setup(adp.AdpError, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
-        _binding = module
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            _missing = str(e)
+        else:
+            names = ("adp_paged_kv_append", "adp_paged_attention", "adp_paged_attention_workspace", "adp_paged_window_attention",
+                     "adp_paged_window_attention_workspace", "adp_paged_chunk_attention", "adp_paged_chunk_attention_workspace")
+            module.setup(adp.AdpError, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
+            _binding = module
+    if _binding is None and needed:
+        raise RuntimeError(f"the extension module of ops.py is missing, build it with build.build(): {_missing}")
     return _binding
 
 
@@ -186,7 +193,43 @@ def paged_attention(q, k_pages, v_pages, table, lens, *, window: int | None = No
     adp.adp_paged_attention_workspace bytes, with a window adp.adp_paged_window_attention_workspace bytes (not shared by calls
     that may run at the same time); by default one is allocated on the current stream.
     The work is split by the table's width, or the window's: a table no wider than the longest context is fastest."""
-    return _native().paged_attention(k_pages, v_pages, table, lens, q, window, sinks, scale, k_scale, v_scale, out, workspace, status)
+    native = _native(needed=False)
+    if native is not None:
+        return native.paged_attention(k_pages, v_pages, table, lens, q, window, sinks, scale, k_scale, v_scale, out, workspace, status)
+    # the same checks and call where libadp.so is all that could be built (12 us a call more)
+    where = "paged_attention"
+    if window is None:
+        if sinks != 0:
+            _refuse(where, "sinks go with a window")
+    elif window < 1 or sinks < 0:
+        _refuse(where, "window must be at least 1, sinks at least 0")
+    device = k_pages.get_device()
+    kv = _paged(where, k_pages, v_pages, table, lens, k_scale, v_scale, device)
+    dtype, shape = q.dtype, q.shape
+    dt = _HALF.get(dtype)
+    if dt is None or len(shape) != 3 or shape[0] != kv.n_seqs or shape[2] != kv.head_dim or shape[2] < 1:
+        _refuse(where, "q must be [seqs, heads, head_dim] of f16 or bf16")
+    qs = _rows(where, "q", q, shape, dtype, device)
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        os = shape[1] * shape[2]
+    else:
+        os = _rows(where, "out", out, shape, dtype, device)
+    name, seen = "adp_paged_attention", ()
+    if window is not None:
+        name, seen = "adp_paged_window_attention", (min(window, 2 ** 31 - 1), min(sinks, 2 ** 31 - 1))
+    if workspace is not None:
+        need = workspace.numel()
+        if workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != device:
+            _refuse(where, "workspace must be a contiguous uint8 tensor on the tensors' device")
+    else:
+        with torch.cuda.device(device):
+            need = getattr(adp, name + "_workspace")(kv, shape[1], *seen)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _call(device, name, kv, q.data_ptr(), dt, shape[1], qs, shape[2] ** -0.5 if scale is None else scale, *seen, out.data_ptr(), os,
+          workspace.data_ptr() if need else None, need, _status(where, status, device))
+    return out
 
 
 def paged_chunk_attention(q, k_pages, v_pages, table, lens, cu_rows, *, window: int | None = None, sinks: int = 0,
