@@ -26,7 +26,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libadp.so")
 TEST_LIB = os.path.join(HERE, "libadp_test.so")
-BINDING = os.path.join(HERE, "_binding.so")
+BINDING = os.path.join(HERE, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))  # (no other Python takes it)
 SOURCES = ["decode.cu", "decode_batch.cu", "prefill.cu", "repack.cu", "engine.cu", "noalloc.cu", "probe.cu",
            "paged_rows.cu", "paged_append.cu",
            "paged_attention.cu", "paged_window.cu", "paged_chunk.cu", "packed_attention.cu"]
@@ -49,6 +49,7 @@ def _extra_flags() -> list[str]:
 
 
 FLAGS_STAMP = os.path.join(HERE, "_build", "flags.txt")
+BINDING_STAMP = os.path.join(HERE, "_build", "binding.txt")
 BINDING_SOURCE = "binding.cpp"
 
 
@@ -71,7 +72,19 @@ def _stale() -> bool:
     return _older([LIB, TEST_LIB], [f for f in os.listdir(CSRC) if f != BINDING_SOURCE])
 
 
+def _binding_for() -> str:
+    """What an extension module is made for: PyTorch's version and C++ ABI, and Python's."""
+    import torch
+    return f"torch {torch.__version__}, C++11 ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, python {sysconfig.get_config_var('SOABI')}"
+
+
 def _stale_binding() -> bool:
+    try:
+        with open(BINDING_STAMP) as fh:
+            if fh.read() != _binding_for():
+                return True
+    except (ImportError, OSError):
+        return True  # (where PyTorch is missing, building the module says so)
     return _older([BINDING], [BINDING_SOURCE])
 
 
@@ -83,13 +96,16 @@ def _build_binding():
     include = [os.path.join(root, "include"), sysconfig.get_paths()["include"], cuda]
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-isystem{i}" for i in include),
-           os.path.join(CSRC, BINDING_SOURCE), "-o", tmp, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
-           "-ltorch_python"]
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DADP_TORCH_VERSION="{torch.__version__}"',
+           *(f"-isystem{i}" for i in include), os.path.join(CSRC, BINDING_SOURCE), "-o", tmp, "-L" + os.path.join(root, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stderr}")
     os.replace(tmp, BINDING)
+    os.makedirs(os.path.dirname(BINDING_STAMP), exist_ok=True)
+    with open(BINDING_STAMP, "w") as fh:
+        fh.write(_binding_for())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -101,7 +117,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         error = binding.exception() if binding else None
     if error:
         if os.path.exists(BINDING):
-            os.remove(BINDING)  # made of other sources
+            os.remove(BINDING)  # made of other sources, or for another PyTorch
         warnings.warn(f"{os.path.basename(BINDING)} could not be built ({type(error).__name__}: {error}): the calls of ops.py that need it "
                       "will fail", RuntimeWarning, stacklevel=2)
     return LIB

@@ -73,6 +73,9 @@ def _native(needed: bool = True):
         lib = adp.load_library()
         try:
             from . import _binding as module
+            made_for = getattr(module, "torch_version", "another version")
+            if made_for != torch.__version__:  # whose classes may lie otherwise in memory
+                raise ImportError(f"it was made for PyTorch {made_for}, this is {torch.__version__}")
         except ImportError as e:
             _missing = str(e)
         else:

@@ -1,6 +1,7 @@
-"""The build's steps without a compiler: what is made where the extension module cannot be."""
+"""The build's steps without a compiler: what is made where the extension module cannot be, and when that module is out of date."""
 import os
 import stat
+import sysconfig
 
 import pytest
 
@@ -15,7 +16,8 @@ def elsewhere(monkeypatch, tmp_path):
     (tmp_path / "include" / "adp.h").write_text("")
     for name in ("LIB", "TEST_LIB", "BINDING"):
         monkeypatch.setattr(build, name, str(here / os.path.basename(getattr(build, name))))
-    monkeypatch.setattr(build, "FLAGS_STAMP", str(here / "_build" / "flags.txt"))
+    for name in ("FLAGS_STAMP", "BINDING_STAMP"):
+        monkeypatch.setattr(build, name, str(here / "_build" / (name + ".txt")), raising=False)
     monkeypatch.setattr(build, "HERE", str(here))
     fake = tmp_path / "nvcc"
     fake.write_text('#!/bin/sh\nwhile [ $# -gt 0 ]; do if [ "$1" = -o ]; then : > "$2"; fi; shift; done\n')
@@ -57,3 +59,40 @@ def test_a_pytorch_that_is_missing_is_said(elsewhere, monkeypatch):
     with pytest.warns(RuntimeWarning, match="torch"):
         build.build()
     assert os.path.exists(build.LIB)
+
+
+def test_a_module_made_for_another_pytorch_or_python_is_out_of_date(elsewhere, monkeypatch):
+    import torch
+    build = elsewhere
+
+    def compiles(cmd, **kw):
+        with open(cmd[cmd.index("-o") + 1], "w"):
+            return build.subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(build.subprocess, "run", compiles)
+    assert build._stale_binding()
+    build.build()
+    assert not build._stale_binding()
+    assert build.BINDING.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "1.0")
+        assert build._stale_binding() and not build._stale()
+        build.build()
+        assert not build._stale_binding()
+    assert build._stale_binding()
+    build.build()
+    assert not build._stale_binding()
+    os.remove(build.BINDING)
+    assert build._stale_binding()
+
+
+def test_a_module_made_for_another_pytorch_is_not_called(monkeypatch):
+    import torch
+    from autoregressive_decode_persistent_gb300 import build, ops
+    build.build()
+    assert ops._native() is not None
+    monkeypatch.setattr(ops, "_binding", None)
+    monkeypatch.setattr(ops, "_missing", None)
+    monkeypatch.setattr(torch, "__version__", "1.0")
+    with pytest.raises(RuntimeError, match="1.0"):
+        ops.paged_kv_append(*[None] * 10)
