@@ -7,9 +7,11 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <exception>
 #include <optional>
 #include <string>
 
@@ -357,8 +359,8 @@ PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t n) {
       Py_DECREF(e);
     }
   } catch (const PythonError&) {
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {  // PyTorch's own errors keep their types (OutOfMemoryError among them)
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }
