@@ -15,6 +15,15 @@ namespace {
 
 constexpr int kAppendThreads = 32;  // a warp: the last CTAs of a call leave few SMs idle (64: 140 us instead of 137, 256: 148)
 
+constexpr float kLeastMean = 8.0779357e-28f;  // 2^-90: above it no square that counts underflows
+
+// The power of two that brings the larger of a head's largest magnitude and the root of eps to between 1 and 4, as far as fp32 has one.
+__device__ __forceinline__ float power_near(float top, float eps) {
+  const int of_top = (int)(__float_as_uint(top) >> 23) - 127;
+  const int of_eps = eps > 0.0f ? ((int)(__float_as_uint(eps) >> 23) - 127) >> 1 : -126;
+  return __uint_as_float((uint32_t)(127 - min(max(max(of_top, of_eps), -126), 126)) << 23);
+}
+
 struct AppendArgs {
   PagedView c;
   const uint8_t *q, *k, *v;
@@ -34,8 +43,9 @@ struct AppendArgs {
 // HD / 16 lanes hold a head, two pieces of 8 elements each: a lane with rotated elements has both halves of its pairs (pieces
 // u and u + turned), so that the rotation needs no other lane, and the mean square and the largest magnitude take three
 // exchanges a head.  A lane's 8 cosines and sines are the same for all of the row's heads.  Per head: a norm's x / sqrt(mean(x^2) +
-// eps) x gain, then x_i cos - x_(i+r) sin and x_(i+r) cos + x_i sin; everything in fp32, in pairs where there are
-// instructions for them, and rounded once on the way out (keys to codes x scale in e4m3 pages).
+// eps) x gain (a head whose squares leave fp32's range is scaled first), then x_i cos - x_(i+r) sin and x_(i+r) cos + x_i sin;
+// everything in fp32, in pairs where there are instructions for them, and rounded once on the way out (keys to codes x scale
+// in e4m3 pages).
 // Bound by the bytes where rows are many (34,360 rows of 32 + 16 heads x 128 in bf16: 845 MB in 137 us, 92% of the copy rate), and by
 // the look-ups of a row in a line (offsets, length, page, angles) with 17 warps an SM where they are fewer (5,593 rows, normed, to
 // e4m3 pages: 127 MB in 37 us, 51%; in thirds of a row 37, in sixths 44).
@@ -155,16 +165,36 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
             gains(gain, pb, g[1]);
             held = gain;
           }
-          float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sum = __ffma2_rn(x[k][e], x[k][e], sum);
-          float ss = sum.x + sum.y;
           const uint32_t mates = (LPH == 32 ? ~0u : (1u << LPH) - 1) << (lane / LPH * LPH);
+          auto mean_square = [&]() {
+            float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-          for (int d = LPH / 2; d >= 1; d >>= 1) ss += __shfl_xor_sync(mates, ss, d);
-          const float f = rsqrtf(ss * (1.0f / HD) + a.eps);
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sum = __ffma2_rn(x[k][e], x[k][e], sum);
+            float ss = sum.x + sum.y;
+#pragma unroll
+            for (int d = LPH / 2; d >= 1; d >>= 1) ss += __shfl_xor_sync(mates, ss, d);
+            return ss * (1.0f / HD);
+          };
+          float f = mean_square() + a.eps;
+          if (!(f >= kLeastMean && f < INFINITY)) {
+            // (rare) squares leave fp32's range: the head and eps are scaled by a power of two that brings the larger of them near 1
+            float top = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) top = fmaxf(fmaxf(top, fabsf(x[k][e].x)), fabsf(x[k][e].y));
+#pragma unroll
+            for (int d = LPH / 2; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(mates, top, d));
+            const float s = power_near(top, a.eps);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[k][e] = __fmul2_rn(x[k][e], make_float2(s, s));
+            f = mean_square() + a.eps * s * s;
+          }
+          f = rsqrtf(f);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
 #pragma unroll

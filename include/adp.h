@@ -417,9 +417,10 @@ typedef struct {
  *  n_heads     query heads, at most 4096; 0: keys and values only (q and out are ignored)
  *  out         DEVICE rows [n_rows][n_heads][head_dim] of out_dtype (ADP_F16, ADP_BF16 or ADP_F32), 16-byte aligned; may be q where
  *              types and strides are the same
- * Everything is computed in fp32 (a mean of squares beyond its range gives zeros) and rounded once.  A row without a page is not
- * written and reported as adp_paged_kv_write does, one at a position behind the cosines' is not written and reported as
- * ADP_ERR_CONTEXT_OVERFLOW; both give zeros in out.  Padding rows of out are left as they were. */
+ * Everything is computed in fp32 and rounded once; a head whose squares leave its range is scaled by a power of two in front of its
+ * norm.  (With eps 0 a head of zeros has no norm, and gives NaN.)  A row without a page is not written and reported as
+ * adp_paged_kv_write does, one at a position behind the cosines' is not written and reported as ADP_ERR_CONTEXT_OVERFLOW; both
+ * give zeros in out.  Padding rows of out are left as they were. */
 int adp_paged_kv_append(const adp_paged_kv* kv, const adp_rope* rope, const void* q, const void* k, const void* v,
                         int32_t rows_dtype, int32_t n_heads, int64_t q_stride, int64_t k_stride, int64_t v_stride,
                         const int32_t* cu_rows, int32_t n_rows, void* out, int32_t out_dtype, int64_t out_stride,
