@@ -50,6 +50,13 @@ ADP_INLINE int32_t split_parts(int64_t total, int32_t ctas) {
   return want < 1 ? 1 : (want > ctas ? ctas : (int32_t)want);
 }
 
+// Heads that a warp takes of a row's line of `heads`, `step` of them at a time: the line is cut over several warps as long as the
+// call's warps, for n_rows rows, are no more than the `held` that run at once.
+ADP_INLINE int32_t row_part_heads(int32_t heads, int32_t step, int32_t n_rows, int32_t held) {
+  const int32_t most = (heads + step - 1) / step, room = held / n_rows, parts = room < 1 ? 1 : room > most ? most : room;
+  return (most + parts - 1) / parts * step;
+}
+
 // How long a wait inside packed attention may take: some wait for a whole piece of work, which sees up to n_k keys (13 ns a
 // key, measured), and some for the search of the next one, which looks through up to n_seqs sequences (about 2 us for 32).
 ADP_INLINE uint64_t packed_wait_ns(int32_t n_k, int32_t n_seqs) {

@@ -47,7 +47,7 @@ struct AppendArgs {
 // everything in fp32, in pairs where there are instructions for them, and rounded once on the way out (keys to codes x scale
 // in e4m3 pages).
 // Bound by the bytes where rows are many (34,360 rows of 32 + 16 heads x 128 in bf16: 845 MB in 137 us, 92% of the copy rate), and by
-// the look-ups of a row in a line (offsets, length, page, angles) with 17 warps an SM where they are fewer (5,593 rows, normed, to
+// the look-ups of a row in a line (offsets, length, page, angles) with 16 warps an SM where they are fewer (5,593 rows, normed, to
 // e4m3 pages: 127 MB in 37 us, 51%; in thirds of a row 37, in sixths 44).
 template <int ROWDT, int CDT, int HD>
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendArgs a) {
@@ -250,9 +250,32 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
   }
 }
 
-// Warps that share a row: a row's line of heads is cut while there are fewer rows than warps that the GPU holds (4 rows of 20 + 8
-// heads: 2.7 us in a captured graph, 4.3 uncut; many rows gain nothing by it: 34,360 rows 137 us, 147 in halves, 198 in sixths).
-constexpr int kWarpsPerSm = 24;
+// Launches one instance: a row's line of heads is cut over warps while all of the call's warps run at once (4 rows of 20 + 8
+// heads: 2.6 us in a captured graph, 4.3 uncut; many rows gain nothing by it: 34,360 rows 137 us, 147 in halves, 198 in sixths).
+// An SM holds 16 of these warps (four of up to 128 registers a thread on each of its quarters).  Cut by 24, calls of 2 rows
+// of 32 + 16 bf16 heads an SM took 5.1 us instead of 3.5 and 12 rows an SM 8.8 instead of 7.1, some of their warps in a second
+// round; by 12, 8 rows an SM 6.3 instead of 5.6.
+template <int ROWDT, int CDT, int HD>
+cudaError_t append_launch(AppendArgs& a, int sms, cudaStream_t st) {
+  auto* kernel = paged_append_kernel<ROWDT, CDT, HD>;
+  static int known[64];  // warps that an SM of a device holds
+  int dev = 0, held = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64) held = known[dev];
+  if (!held) {
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&held, kernel, kAppendThreads, 0);
+    if (e != cudaSuccess) return e;
+    held *= kAppendThreads / 32;
+    if (dev < 64) known[dev] = held;
+  }
+  const int heads = a.n_heads + 2 * a.c.n_kv_heads;
+  a.part_heads = row_part_heads(heads, 32 / (HD / 16), a.n_rows, sms * held);
+  a.parts = (heads + a.part_heads - 1) / a.part_heads;
+  const int64_t grid = ((int64_t)a.n_rows * a.parts + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
+  kernel<<<(unsigned)grid, kAppendThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
 
 }  // namespace
 }  // namespace adp
@@ -310,19 +333,13 @@ extern "C" int adp_paged_kv_append(const adp_paged_kv* kv, const adp_rope* rope,
   a.out_dt = n_heads > 0 ? out_dtype : ADP_F16;
   a.gain_dt = rope->gain_dtype;
   a.eps = rope->eps;
-  const int heads = n_heads + 2 * kv->n_kv_heads, step = 32 / (kv->head_dim / 16);
-  const int most = (heads + step - 1) / step, want = sms * kWarpsPerSm / n_rows;
-  a.parts = want < 1 ? 1 : want > most ? most : want;
-  a.part_heads = (most + a.parts - 1) / a.parts * step;
-  a.parts = (heads + a.part_heads - 1) / a.part_heads;
-  const int64_t grid = ((int64_t)n_rows * a.parts + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
-  if (grid > 0x7FFFFFFF) return ADP_ERR_UNSUPPORTED_CONFIG;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  cudaError_t e = cudaSuccess;
   auto by_rows = [&](auto cdt, auto hd) {
     constexpr int C = decltype(cdt)::value, H = decltype(hd)::value;
-    if (rows_dtype == ADP_F16) paged_append_kernel<DT_F16, C, H><<<(unsigned)grid, kAppendThreads, 0, st>>>(a);
-    else if (rows_dtype == ADP_BF16) paged_append_kernel<DT_BF16, C, H><<<(unsigned)grid, kAppendThreads, 0, st>>>(a);
-    else paged_append_kernel<DT_F32, C, H><<<(unsigned)grid, kAppendThreads, 0, st>>>(a);
+    if (rows_dtype == ADP_F16) e = append_launch<DT_F16, C, H>(a, sms, st);
+    else if (rows_dtype == ADP_BF16) e = append_launch<DT_BF16, C, H>(a, sms, st);
+    else e = append_launch<DT_F32, C, H>(a, sms, st);
   };
   auto by_cache = [&](auto hd) {
     if (kv->dtype == ADP_F16) by_rows(std::integral_constant<int, DT_F16>(), hd);
@@ -331,5 +348,5 @@ extern "C" int adp_paged_kv_append(const adp_paged_kv* kv, const adp_rope* rope,
   };
   if (kv->head_dim == 128) by_cache(std::integral_constant<int, 128>());
   else by_cache(std::integral_constant<int, 64>());
-  return cuda_status(cudaGetLastError(), "adp_paged_kv_append");
+  return cuda_status(e, "adp_paged_kv_append");
 }
