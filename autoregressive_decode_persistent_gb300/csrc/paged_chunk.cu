@@ -302,10 +302,11 @@ __device__ __forceinline__ float4 taken_out(const ChunkArgs& a, const Item& w, i
 // the next ones have of it.
 //
 // Measured: long chunks are bound by the MMAs and the softmax warps, which both fill most of a block's time (2,048 rows of 32/8
-// heads x 128 over 8,192 bf16 positions: 241 GFLOP in 180 us, 70% of the GEMM rate, the tensor pipe busy 57% of it; some
+// heads x 128 over 8,192 bf16 positions: 241 GFLOP in 181 us, 70% of the GEMM rate, the tensor pipe busy 57% of it; some
 // 1,280 cycles of a pair's block, 1,024 by the pipe's rate: S's 64 columns read Q again for every block).  Few rows over 16 bits are
 // bound by memory (32 sequences of 4 rows, 8,192 positions each: 1.07 GB in 178 us, 89% of the copy rate), over e4m3
-// by the conversion to fp16 and three slots of fp16 blocks beside the codes (the same in e4m3: 206 us, 40%).
+// by a block's way from codes to O, on which two tiles and three slots of fp16 blocks keep two blocks at a time, 0.8 us each (the
+// same in e4m3: 206 us, 40%; with three quarters of the conversions left out 32 sequences of up to 8 rows took 144 us for 146).
 //
 // CDT: the pages' type; QDT: the queries' (that of 16-bit pages).  LOAD: four warps bring K and V into the ring (e4m3 pages,
 // which become fp16 there, and pages too small for tensor copies), else tensor copies do.
@@ -392,7 +393,8 @@ __global__ void __launch_bounds__(LOAD ? 512 : 384, 1)
     mbar_fence_init();
   }
   // A range's last piece is joined by the CTA that starts it, which waits for the next range's beginning: that range belongs to a CTA
-  // with a lower number, which is launched no later.
+  // with a lower number, which is launched no later.  (So this GPU does it; the programming model does not promise it, and the wait
+  // is bounded: a CTA that gives up reports it, and its rows stay unset.)
   const int range = (int)(gridDim.x - 1 - blockIdx.x);
   // ---- units and pairs of every 32 sequences (one warp's worth: the finding warp adds them up alone)
   const int n_chunks = (a.c.n_seqs + 31) / 32, span = 2 * a.tok;

@@ -39,7 +39,7 @@ ADP_INLINE int32_t chunk_block(const ChunkSpan& s, int32_t i) { return i < s.hea
 
 // What starting and ending a piece of work costs, in blocks of it: where its rows fit one tile, whose blocks cost half as much, and
 // whose results the tiles add up, twice as many (4 for both: 32 sequences of up to 8 tokens 130.5 us instead of 127; 8 for both: prompts and
-// single tokens together 77.4 instead of 74).
+// single tokens together 77.4 instead of 74).  A block itself counts as one for both: the line is cut by blocks, not by their time.
 ADP_INLINE int32_t chunk_over(int32_t tokens, int32_t tile) { return tokens <= tile ? 8 : 4; }
 
 // Where a cut that falls j units behind a piece's blocks' start (negative: in front) goes: whole blocks, and no part of less than

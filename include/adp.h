@@ -476,11 +476,11 @@ int adp_paged_window_attention_workspace(const adp_paged_kv* kv, int32_t n_heads
  *              is 0); its contents do not matter.  Calls that may run at the same time need one each.
  * Scores, softmax and sums are fp32; before they weigh V, probabilities are rounded to the cache's 16-bit type (fp16 ones held
  * 2^7 times larger), over e4m3 pages probability x value scale to fp16 as in adp_paged_attention.  A row that sees nothing
- * gives zeros.  What a row does not see does not reach it, whatever it holds.  Bad pages and lengths are treated and reported as in
- * adp_paged_attention; a sequence with more rows than positions (its first rows give zeros) and offsets that do not start at
- * 0, descend or lie outside [0, n_rows] (cut to it) are reported as ADP_ERR_INVALID_ARG; a wait inside the kernel that ran out
- * (1 s and more) is reported as ADP_ERR_PIPELINE_TIMEOUT, and leaves rows of out unset: only dev_status tells.  Equal inputs
- * give equal bits on one GPU. */
+ * gives zeros.  What a row does not see does not reach it, whatever it holds (but neighbouring rows decide together when their sums
+ * are rescaled, which may round one of them otherwise).  Bad pages and lengths are treated and reported as in adp_paged_attention;
+ * a sequence with more rows than positions (its first rows give zeros) and offsets that do not start at 0, descend or lie outside
+ * [0, n_rows] (cut to it) are reported as ADP_ERR_INVALID_ARG; a wait inside the kernel that ran out (1 s and more) is reported as
+ * ADP_ERR_PIPELINE_TIMEOUT, and leaves rows of out unset: only dev_status tells.  Equal inputs give equal bits on one GPU. */
 int adp_paged_chunk_attention(const adp_paged_kv* kv, const void* q, int32_t q_dtype, int32_t n_heads, int64_t q_stride,
                               const int32_t* cu_rows, int32_t n_rows, float scale, int32_t window, int32_t sinks, void* out,
                               int64_t out_stride, void* workspace, uint64_t workspace_bytes, int32_t* dev_status,
